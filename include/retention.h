@@ -280,6 +280,81 @@ ret_status_t retention_score_map(const ret_desc_t *desc, const void *q, const vo
 ret_status_t retention_chunkwise_error(const void *workspace, size_t workspace_bytes, int32_t *error_word,
                                        hipStream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Gated delta rule: retention's recurrence with a decay per token and a write
+ * that replaces what the state already holds along a key. Per value head, with
+ * a_t = exp(log_decay_t),
+ *     S' = a_t S_{t-1},   u_t = beta_t (v_t - S'^T k_t),
+ *     S_t = S' + k_t u_t^T,   o_t = scale S_t^T q_t.
+ * Value head h reads key head h / (v_heads / k_heads).
+ *     q, k              [batch, seqlen, k_heads, dk]   dtype of the descriptor
+ *     v, o              [batch, seqlen, v_heads, dv]   dtype of the descriptor
+ *     log_decay, beta   [batch, seqlen, v_heads]       fp32, 4-byte aligned
+ *     state             [batch, v_heads, dk, dv]       fp32
+ * log_decay is meant to be <= 0 (-infinity: the state is forgotten; values
+ * below -1e5 count as that) and beta in [0, 2] with keys of length at most 1;
+ * then no state grows. Other values are computed as they stand. There is no
+ * rotation, GroupNorm or gate in these calls (retention_head_norm_fwd follows).
+ *
+ * Packed sequences: with cu_seqlens (DEVICE int32 [batch + 1], as in
+ * retention_chunkwise_varlen_fwd) the tensors are [total_tokens, heads, d] (and
+ * [total_tokens, v_heads]), seqlen bounds every length, empty sequences are
+ * allowed, rows outside every sequence are not written, and bounds that have
+ * to be clamped set bit 1 of control word 1 (retention_chunkwise_error reads
+ * it from these workspaces too). With cu_seqlens NULL total_tokens is ignored.
+ *
+ * Supported: dk == dv in {64, 128, 256}; fp32 or bf16; v_heads <= 128 and a
+ * multiple of k_heads; at most 2^31 - 1 tokens. bf16 tensors are multiplied on
+ * the matrix cores as they are; what the recurrence carries (state, written
+ * values) enters the products as the sum of two bf16 values, so that the fp32
+ * states and gradients a call returns are good to a few 1e-6. A NaN or
+ * infinity in a token reaches no other sequence and no output of an earlier
+ * block of 64 tokens.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch;    /* >= 1: sequences                                         */
+  int32_t seqlen;   /* >= 1: tokens of each, or a bound on them when packed    */
+  int32_t k_heads;  /* heads of q and k                                        */
+  int32_t v_heads;  /* heads of v, o, log_decay, beta and the state, .. 128    */
+  int32_t dk, dv;   /* head dimensions (equal)                                 */
+  int32_t dtype;    /* ret_dtype_t of q, k, v, o and their gradients           */
+  float scale;      /* of the output, finite                                   */
+} ret_delta_desc_t;
+
+/* Chunkwise form (prefill and training): blocks of 64 tokens, the state
+ * carried from block to block. state_in NULL: zeros; state_out NULL: not
+ * written; state_out == state_in is allowed. The two forms of the recurrence
+ * are those of the retention calls ("Summary": parallel inside a chunk, the
+ * recurrent state passed between chunks). */
+size_t retention_delta_workspace_bytes(const ret_delta_desc_t *desc, int32_t packed, int64_t total_tokens);
+ret_status_t retention_delta_fwd(const ret_delta_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
+                                 const void *q, const void *k, const void *v, const float *log_decay,
+                                 const float *beta, void *o, const float *state_in, float *state_out, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dout (.) o) + sum(d_state_out (.) state_out) (the second
+ * term only when d_state_out is given) with respect to q, k, v, log_decay,
+ * beta and state_in (d_state_in non-NULL exactly when state_in is). Key heads
+ * that several value heads share receive the sum. The forward's walk is run
+ * again; its states take workspace: per 64 tokens and value head four times
+ * dk dv elements of the dtype, and a quarter of dk dv fp32. */
+size_t retention_delta_bwd_workspace_bytes(const ret_delta_desc_t *desc, int32_t packed, int64_t total_tokens);
+ret_status_t retention_delta_bwd(const ret_delta_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
+                                 const void *q, const void *k, const void *v, const float *log_decay,
+                                 const float *beta, const void *dout, const float *state_in, const float *d_state_out,
+                                 void *dq, void *dk, void *dv, float *d_log_decay, float *d_beta, float *d_state_in,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One decode step for a batch of single tokens (desc->seqlen must be 1), the
+ * state in place. state is a pool [num_slots, v_heads, dk, dv]; sequence b uses
+ * slot slots[b] (DEVICE int32 [batch], 4-byte aligned), or slot b with slots
+ * NULL (then num_slots must equal batch). A slot that is negative, outside the
+ * pool or already named by an earlier sequence of the batch is inactive: that
+ * sequence's output rows are zero and no state changes for it. */
+ret_status_t retention_delta_step(const ret_delta_desc_t *desc, const void *q, const void *k, const void *v,
+                                  const float *log_decay, const float *beta, void *o, float *state,
+                                  const int32_t *slots, int64_t num_slots, hipStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *retention_status_string(ret_status_t status);
 

@@ -9,6 +9,9 @@ gfx950 behind a C ABI (include/retention.h), with a thin ctypes binding.
     parallel_bwd     gradients of the parallel form (q, k, v and the gate)
     chunkwise_bwd    the same gradients, each product run as the chunkwise form
     score_map        one query token's retention weights, summed over heads
+    delta_chunkwise_fwd   gated delta rule over whole (or packed) sequences, state in and out
+    delta_chunkwise_bwd   its gradients
+    delta_recurrent_step  its decode step, state (or a pool of states) in place
     check_chunkwise  raise if a chunkwise call's control word reports an error
 """
 
@@ -22,6 +25,9 @@ from .binding import (  # noqa: F401
     chunkwise_varlen_fwd,
     chunkwise_varlen_workspace_bytes,
     chunkwise_workspace_bytes,
+    delta_chunkwise_bwd,
+    delta_chunkwise_fwd,
+    delta_recurrent_step,
     lib,
     parallel_bwd,
     parallel_fwd,

@@ -50,6 +50,11 @@ EXPORTS = (
     "retention_score_map_workspace_bytes",
     "retention_score_map",
     "retention_chunkwise_error",
+    "retention_delta_workspace_bytes",
+    "retention_delta_fwd",
+    "retention_delta_bwd_workspace_bytes",
+    "retention_delta_bwd",
+    "retention_delta_step",
     "retention_status_string",
     "retention_abi_version",
 )
@@ -69,6 +74,21 @@ class RetDesc(ctypes.Structure):
         ("rotary_base", ctypes.c_double),
         ("pos_offset", ctypes.c_int64),
         ("gn_eps", ctypes.c_float),
+    ]
+
+
+class DeltaDesc(ctypes.Structure):
+    """Mirror of ret_delta_desc_t."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("seqlen", ctypes.c_int32),
+        ("k_heads", ctypes.c_int32),
+        ("v_heads", ctypes.c_int32),
+        ("dk", ctypes.c_int32),
+        ("dv", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -135,6 +155,17 @@ def lib():
         h.retention_score_map.restype = st
         h.retention_chunkwise_error.argtypes = [vp, sz, ctypes.POINTER(i32), vp]
         h.retention_chunkwise_error.restype = st
+        pdd, i64 = ctypes.POINTER(DeltaDesc), ctypes.c_int64
+        h.retention_delta_workspace_bytes.argtypes = [pdd, i32, i64]
+        h.retention_delta_workspace_bytes.restype = sz
+        h.retention_delta_fwd.argtypes = [pdd, vp, i64] + [vp] * 9 + [sz, vp]
+        h.retention_delta_fwd.restype = st
+        h.retention_delta_bwd_workspace_bytes.argtypes = [pdd, i32, i64]
+        h.retention_delta_bwd_workspace_bytes.restype = sz
+        h.retention_delta_bwd.argtypes = [pdd, vp, i64] + [vp] * 15 + [sz, vp]
+        h.retention_delta_bwd.restype = st
+        h.retention_delta_step.argtypes = [pdd] + [vp] * 8 + [i64, vp]
+        h.retention_delta_step.restype = st
         h.retention_status_string.argtypes = [st]
         h.retention_status_string.restype = ctypes.c_char_p
         h.retention_abi_version.argtypes = []
@@ -490,4 +521,152 @@ def recurrent_step(q, k, v, state, g=None, *, gammas=None, rotary_base=0.0, pos=
         _check(lib().retention_recurrent_step_positions(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                                                         _ptr(out), _ptr(state), _ptr(positions), _stream(q)))
     del keep
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Gated delta rule
+# ---------------------------------------------------------------------------
+def _delta_inputs(q, k, v, log_decay, beta, more, cu_seqlens, max_seqlen):
+    """Checks of the chunkwise calls' tensors; returns (batch, seqlen,
+    total_tokens). `more`: further tensors of v's shape and dtype, by name."""
+    packed = cu_seqlens is not None
+    dims = 3 if packed else 4
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    for name, t in (("q", q), ("k", k), ("v", v), *more):
+        _on_device(name, t, q)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {q.dtype}")
+        if t.dim() != dims:
+            raise ValueError(f"{name} must be " + ("[total_tokens, heads, d]" if packed else
+                                                   "[batch, seqlen, heads, d]"))
+    if k.shape != q.shape:
+        raise ValueError("k must have the shape of q")
+    if v.shape[:-2] != q.shape[:-2]:
+        raise ValueError("v must agree with q on its tokens")
+    for name, t in more:
+        if t.shape != v.shape:
+            raise ValueError(f"{name} must have the shape of v")
+    for name, t in (("log_decay", log_decay), ("beta", beta)):
+        _on_device(name, t, q)
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != v.shape[:-1]:
+            raise ValueError(f"{name} must be a contiguous fp32 tensor {list(v.shape[:-1])}")
+    if not packed:
+        if max_seqlen is not None:
+            raise ValueError("max_seqlen goes with cu_seqlens")
+        return q.shape[0], q.shape[1], 0
+    _on_device("cu_seqlens", cu_seqlens, q)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous GPU int32 tensor [batch + 1]")
+    if max_seqlen is None:
+        raise ValueError("max_seqlen (a bound on every length) goes with cu_seqlens")
+    return cu_seqlens.numel() - 1, int(max_seqlen), q.shape[0]
+
+
+def _delta_desc(batch, seqlen, q, v, scale):
+    return DeltaDesc(batch, seqlen, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1], _dtype_code(q), float(scale))
+
+
+def _delta_state(name, t, batch, q, v):
+    if t is None:
+        return
+    _on_device(name, t, q)
+    shape = (batch, v.shape[-2], q.shape[-1], v.shape[-1])
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous fp32 [batch, v_heads, dk, dv] tensor")
+
+
+class _current:
+    """The tensor's device as the current one (kernels launch there)."""
+
+    def __init__(self, t):
+        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *err):
+        if self.guard is not None:
+            self.guard.__exit__(*err)
+
+
+def delta_chunkwise_fwd(q, k, v, log_decay, beta, *, scale=1.0, state_in=None, state_out=None, cu_seqlens=None,
+                        max_seqlen=None, out=None, workspace=None, check=False):
+    """Gated delta rule over whole sequences: q, k [batch, seqlen, k_heads, d],
+    v [batch, seqlen, v_heads, d], log_decay and beta fp32 [batch, seqlen,
+    v_heads]; returns the output (v's shape) and fills state_out (fp32 [batch,
+    v_heads, d, d], may be state_in itself) if it is given. Packed sequences:
+    [total_tokens, heads, d] tensors with cu_seqlens (GPU int32 [batch + 1])
+    and max_seqlen; rows outside every sequence are left as they were. check:
+    synchronize and raise RetentionError if cu_seqlens had to be clamped
+    (check_chunkwise does the same later for a caller's workspace)."""
+    out = torch.empty_like(v) if out is None else out
+    batch, seqlen, total = _delta_inputs(q, k, v, log_decay, beta, (("out", out),), cu_seqlens, max_seqlen)
+    _delta_state("state_in", state_in, batch, q, v)
+    _delta_state("state_out", state_out, batch, q, v)
+    desc = _delta_desc(batch, seqlen, q, v, scale)
+    L = lib()
+    need = L.retention_delta_workspace_bytes(ctypes.byref(desc), int(cu_seqlens is not None), total)
+    workspace, ws_bytes, _ = _workspace(workspace, need, q)
+    with _current(q):
+        _check(L.retention_delta_fwd(ctypes.byref(desc), _ptr(cu_seqlens), total, _ptr(q), _ptr(k), _ptr(v),
+                                     _ptr(log_decay), _ptr(beta), _ptr(out), _ptr(state_in), _ptr(state_out),
+                                     _ptr(workspace), ws_bytes, _stream(q)))
+    if check:
+        check_chunkwise(workspace)
+    return out
+
+
+def delta_chunkwise_bwd(q, k, v, log_decay, beta, dout, *, scale=1.0, state_in=None, d_state_out=None,
+                        cu_seqlens=None, max_seqlen=None, workspace=None, check=False):
+    """Gradients of sum(dout * out) (+ sum(d_state_out * state_out)) with out,
+    state_out = delta_chunkwise_fwd(q, k, v, log_decay, beta, ...). Returns
+    (dq, dk, dv, dlog_decay, dbeta), and d_state_in after them when state_in
+    is given. Packed sequences and check as in the forward; gradient rows
+    outside every sequence are zero."""
+    batch, seqlen, total = _delta_inputs(q, k, v, log_decay, beta, (("dout", dout),), cu_seqlens, max_seqlen)
+    _delta_state("state_in", state_in, batch, q, v)
+    _delta_state("d_state_out", d_state_out, batch, q, v)
+    new = torch.empty_like if cu_seqlens is None else torch.zeros_like
+    grads = [new(t) for t in (q, k, v, log_decay, beta)]
+    if state_in is not None:
+        grads.append(torch.empty_like(state_in))
+    desc = _delta_desc(batch, seqlen, q, v, scale)
+    L = lib()
+    need = L.retention_delta_bwd_workspace_bytes(ctypes.byref(desc), int(cu_seqlens is not None), total)
+    workspace, ws_bytes, _ = _workspace(workspace, need, q)
+    with _current(q):
+        _check(L.retention_delta_bwd(ctypes.byref(desc), _ptr(cu_seqlens), total, _ptr(q), _ptr(k), _ptr(v),
+                                     _ptr(log_decay), _ptr(beta), _ptr(dout), _ptr(state_in), _ptr(d_state_out),
+                                     *(_ptr(t) for t in grads[:5]), _ptr(grads[5]) if state_in is not None else None,
+                                     _ptr(workspace), ws_bytes, _stream(q)))
+    if check:
+        check_chunkwise(workspace)
+    return tuple(grads)
+
+
+def delta_recurrent_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=None, out=None):
+    """One decode step of the gated delta rule (q, k: [batch, 1, k_heads, d],
+    v: [batch, 1, v_heads, d]); updates `state` in place and returns the
+    output. state: fp32 [batch, v_heads, d, d], or with `slots` (GPU int32
+    [batch]) a pool [num_slots, v_heads, d, d] of which sequence b uses slot
+    slots[b]; a slot that is negative, outside the pool or named by an earlier
+    sequence is inactive (its output is zero)."""
+    out = torch.empty_like(v) if out is None else out
+    batch, seqlen, _ = _delta_inputs(q, k, v, log_decay, beta, (("out", out),), None, None)
+    if seqlen != 1:
+        raise ValueError("delta_recurrent_step takes one token per sequence (seqlen 1)")
+    _delta_state("state", state, batch if slots is None else state.shape[0], q, v)
+    if slots is not None:
+        _on_device("slots", slots, q)
+        if slots.dtype != torch.int32 or not slots.is_contiguous() or tuple(slots.shape) != (batch,):
+            raise ValueError("slots must be a contiguous GPU int32 tensor [batch]")
+    desc = _delta_desc(batch, 1, q, v, scale)
+    with _current(q):
+        _check(lib().retention_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
+                                          _ptr(out), _ptr(state), _ptr(slots), state.shape[0], _stream(q)))
     return out

@@ -5,6 +5,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "host_checks.hpp"
 #include "launch.hpp"
 #include "retention.h"
 
@@ -12,10 +13,10 @@ namespace {
 
 using ret::Shape;
 
-constexpr size_t kWsAlign = 256;
-size_t align_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t elem_size(int32_t dtype) { return dtype == RET_BF16 ? 2 : 4; }
+using ret_host::align_up;
+using ret_host::aligned16;
+using ret_host::elem_size;
+using ret_host::overlaps;
 
 // Decay of head h: the caller's value, or g_h = 1 - 2^(-5-h) (per-head decay
 // of "Retentive Network: A Successor to Transformer...", Elamur summary,
@@ -47,12 +48,6 @@ ret_status_t check_desc(const ret_desc_t* d) {
 ret_status_t check_eps(const ret_desc_t* d, const void* g) {
   if (g && !(std::isfinite(d->gn_eps) && d->gn_eps > 0.0f)) return RET_ERR_ARG;
   return RET_OK;
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
 }
 
 // bytes of one [batch][seqlen][heads][d] tensor and of one fp32 state
