@@ -81,7 +81,7 @@ void carve_bwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_d
   c.part(p.odo, sums);
   c.part(p.vdv, sums);
   c.part(p.xu, sums);
-  c.part(p.adot, l.groups * d->v_heads * (dd / 2048) * sizeof(float));  // a value per wave of 2048 elements
+  c.part(p.adot, l.groups * d->v_heads * l.slices * 4 * sizeof(float));  // a value of each of the four waves
 }
 
 size_t workspace_bytes_of(const ret_delta_desc_t* d, bool packed, int64_t total, bool grad) {

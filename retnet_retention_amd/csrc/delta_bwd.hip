@@ -21,140 +21,128 @@ namespace ret {
 
 hipError_t launch_delta_forward(const DeltaParams& p, int d, int dtype, bool grad, hipStream_t stream);
 
-template <typename T, int D>
-struct ReverseIn {
-  using CS = ChainShape<T, D>;
-  static constexpr int NP = Planes<T>::N;
-  frag_t<T> k[2][4];                  // rows of K, the wave's 64 key columns
-  frag_t<T> tt[NP][2], pt[NP][2];     // rows 16 w .. + 15 of T^T and P^T
-  T v[CS::CG][4][2], dout[CS::CG][4][2], u[NP][CS::CG][4][2];
-  f32x4 eg, el, beta;
-  float last;
-};
-
-template <typename T, int D>
-__device__ __forceinline__ void load_reverse(ReverseIn<T, D>& in, const DeltaParams& p, int64_t row0, int rows,
-                                             int64_t slot, int h, int hk, int slice, int w, int lane) {
-  using CS = ChainShape<T, D>;
-  constexpr int NP = Planes<T>::N;
-  const int n = lane & 31, h2 = lane >> 5, g16 = lane >> 4, c = lane & 15;
-  const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
-  const float* vec = p.vec + slot * (4 * kB);
-  const T* tm = reinterpret_cast<const T*>(p.tt) + slot * (NP * kB * kB) + (16 * w + c) * kB + 8 * g16;
-  const T* pm = reinterpret_cast<const T*>(p.pt) + slot * (NP * kB * kB) + (16 * w + c) * kB + 8 * g16;
-  if (w < CS::WAVES) {
-    const T* K = reinterpret_cast<const T*>(p.k) + row0 * qs + hk * D + 64 * (w % CS::RG) + 8 * h2;
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) in.k[rt][ks] = global_row8(K + (32 * rt + n) * qs + 16 * ks, 32 * rt + n < rows);
-  }
-#pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    if (ks < (w >> 1)) continue;  // upper triangular
-#pragma unroll
-    for (int pl = 0; pl < NP; ++pl) {
-      in.tt[pl][ks] = global_row8(tm + pl * kB * kB + 32 * ks, true);
-      in.pt[pl][ks] = global_row8(pm + pl * kB * kB + 32 * ks, true);
-    }
-  }
-  const int r4 = 16 * w + 4 * g16;
-  const int64_t at = row0 * vs + h * D + slice * CS::SL + 2 * c, plane = (int64_t)p.total * vs;
-  const T* V = reinterpret_cast<const T*>(p.v) + at;
-  const T* DO = reinterpret_cast<const T*>(p.dout) + at;
-  const T* U = reinterpret_cast<const T*>(p.u) + at;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int cg = 0; cg < CS::CG; ++cg)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int64_t o = (r4 + i) * vs + 32 * cg + e;
-        const bool keep = r4 + i < rows;
-        in.v[cg][i][e] = keep ? V[o] : (T)0.f;
-        in.dout[cg][i][e] = keep ? DO[o] : (T)0.f;
-#pragma unroll
-        for (int pl = 0; pl < NP; ++pl) in.u[pl][cg][i][e] = keep ? U[pl * plane + o] : (T)0.f;
-      }
-  in.eg = *reinterpret_cast<const f32x4*>(vec + r4);
-  in.el = *reinterpret_cast<const f32x4*>(vec + kB + r4);
-  in.beta = *reinterpret_cast<const f32x4*>(vec + 2 * kB + r4);
-  in.last = vec[kB - 1];
-}
-
-// The gradient of the state, from a sequence's last block to its first; the
+// The gradient of the state, from a sequence's last block to its first: the
 // same division of work and the same three exchanges as delta_chain_kernel.
+// The second four waves form P^T dO, put Q and scale e^G dO where the state
+// waves read them, and take the row sums.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
-  using KT = typename CS::KTile;
-  constexpr int NP = Planes<T>::N;
+  using KT = KeyTile<T, CS::KR>;
+  constexpr int NP = Planes<T>::N, SZ = sizeof(T);
+  constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
+  // where LDS has no room for a second tile, Q's products follow K's in the same one
+  constexpr bool kTwoTiles = SZ == 2 || D == 128;
   T* const tag = nullptr;
-  // fp32 at d = 256 has no room for a second tile: Q's products follow K's in the same one
-  constexpr bool kTwoTiles = !(sizeof(T) == 4 && D == 256);
-  __shared__ __attribute__((aligned(1024))) char kt[CS::WAVES * KT::BYTES], qt[kTwoTiles ? CS::WAVES * KT::BYTES : 16];
-  __shared__ __attribute__((aligned(16))) f32x4 part_k[CS::WAVES * 512];
-  __shared__ __attribute__((aligned(16))) T od[CS::OPLANE], oq[CS::OPND], ox[CS::OPND], ow[CS::OPND];
+  __shared__ __attribute__((aligned(16))) char kt[4 * KT::BYTES], qt[kTwoTiles ? 4 * KT::BYTES : 16];
+  __shared__ __attribute__((aligned(16))) f32x4 part[4 * 512];
+  // each quarter's P^T dO on its way to the state wave, then its dX on the way back
+  __shared__ __attribute__((aligned(16))) f32x4 quarter[16 * CT * 16];
+  __shared__ __attribute__((aligned(16))) T od[OPLANE], oq[CS::OPND], ox[CS::OPND], ow[CS::OPND];
 
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform_i(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i(tid >> 6), w = wave & 3;
   const int id = xcd_swizzle(blockIdx.x, gridDim.x);
   const int slice = id % CS::NSL, bh = id / CS::NSL, h = bh % p.heads, b = bh / p.heads;
   const int hk = h / (p.heads / p.k_heads);
-  const int rg = w % CS::RG, cg_w = w / CS::RG;
-  const bool holds = w < CS::WAVES;
   const int n = lane & 31, h2 = lane >> 5, g16 = lane >> 4, c = lane & 15;
+  const int r4 = 16 * w + 4 * g16;
   int64_t tok0;
   int len, base;
   seq_span(p, b, tok0, len, base);
   const int nblk = (len + kB - 1) / kB;
   const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
-  const int krow = 64 * rg, vcol = slice * CS::SL + 32 * cg_w + n;
-  f32x16 s[2] = {zero16(), zero16()};
-  if (holds && p.d_state_out) {
-    const float* si = p.d_state_out + (int64_t)bh * D * D;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[t][i] = si[(krow + 32 * t + state_row(i, h2)) * D + vcol];
-  }
-  char* my_kt = kt + w * KT::BYTES;
-  char* my_qt = kTwoTiles ? qt + w * KT::BYTES : my_kt;
-  TileLoads<T, KT, 1> loads;
-  loads.init(qs, lane);
-  auto load_tile = [&](char* to, const void* from, int64_t row0, int rows) {
-    const T* src = reinterpret_cast<const T*>(from) + row0 * qs + hk * D + krow;
-    if (rows == kB)
-      loads.issue(to, src, qs, 0, 0);
-    else
-      loads.issue_clamped(to, src, qs, 0, rows - 1, 0);
+  const uint32_t qrow = (uint32_t)qs * SZ, vrow = (uint32_t)vs * SZ;
+  // descriptors of block blk (no rows: nothing is read)
+  auto rows_of = [&](int blk) { return blk >= 0 ? min(kB, len - blk * kB) : 0; };
+  auto key_rsrc = [&](const void* x, int blk) {
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + (tok0 + (int64_t)blk * kB) * qs + hk * D, rows_of(blk) * qrow);
   };
-  constexpr bool kAhead = sizeof(T) == 2;
-  ReverseIn<T, D> in;
-  if (kAhead && nblk) {
-    const int last = nblk - 1;
-    load_reverse<T, D>(in, p, tok0 + last * kB, len - last * kB, (int64_t)(base + last) * p.heads + h, h, hk, slice, w,
-                       lane);
-  }
+  auto value_rsrc = [&](const void* x, int blk) {
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + (tok0 + (int64_t)blk * kB) * vs + h * D, rows_of(blk) * vrow);
+  };
+  auto slot_of = [&](int blk) { return (int64_t)(base + blk) * p.heads + h; };
+  auto mat_rsrc = [&](const void* x, int blk) {
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + slot_of(blk) * (NP * kB * kB), blk >= 0 ? NP * kB * kB * SZ : 0);
+  };
+  auto vec_rsrc = [&](int blk) { return scalar_rsrc(p.vec + slot_of(blk) * (4 * kB), blk >= 0 ? 4 * kB * 4 : 0); };
+  const uint32_t mat_off = ((16 * w + c) * kB + 8 * g16) * SZ;
+  uint32_t pair_off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pair_off[i] = (r4 + i) * vrow + (slice * CS::SL + 2 * c) * SZ;
+  const int krow = CS::KR * (w % RG), cg = w / RG, vcol = slice * CS::SL + 32 * cg + n;
+  const uint32_t key_off[2] = {n * qrow + (krow + 8 * h2) * SZ, (32 + n) * qrow + (krow + 8 * h2) * SZ};
+  // rows 16 w .. of an upper triangular matrix
+  auto load_upper = [&](frag_t<T>(&f)[NP][2], const void* x, int blk) {
+    const auto rs = mat_rsrc(x, blk);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if (ks < (w >> 1)) continue;
+#pragma unroll
+      for (int pl = 0; pl < NP; ++pl) f[pl][ks] = buf_frag(rs, mat_off + (pl * kB * kB + 32 * ks) * SZ, tag);
+    }
+  };
+  auto load_keys = [&](frag_t<T>(&f)[2][CS::KS], const void* x, int blk) {
+    const auto rs = key_rsrc(x, blk);
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int ks = 0; ks < CS::KS; ++ks) f[rt][ks] = buf_frag(rs, key_off[rt] + 16 * ks * SZ, tag);
+  };
+  auto put_keys = [&](char* tile, const frag_t<T>(&f)[2][CS::KS]) {
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int ks = 0; ks < CS::KS; ++ks) KT::put(tile, 32 * rt + n, 16 * ks + 8 * h2, f[rt][ks]);
+  };
+  auto load_pairs = [&](PairOf<T>(&x)[CG][4], const void* from, int blk) {
+    const auto rs = value_rsrc(from, blk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < CG; ++g) x[g][i] = buf_pair(rs, pair_off[i] + 32 * g * SZ, tag);
+  };
+  f32x4* my_quarter = quarter + (4 * w + g16) * (CT * 16) + c;
 
-  for (int blk = nblk - 1; blk >= 0; --blk) {
-    const int64_t row0 = tok0 + (int64_t)blk * kB;
-    const int rows = min(kB, len - blk * kB);
-    const int64_t slot = (int64_t)(base + blk) * p.heads + h;
-    const int r4 = 16 * w + 4 * g16;
-    if constexpr (!kAhead) load_reverse<T, D>(in, p, row0, rows, slot, h, hk, slice, w, lane);
-    if (holds) {
-      __builtin_amdgcn_s_waitcnt(kWaitLds);  // the last block's reads of the tiles
-      load_tile(my_kt, p.k, row0, rows);
-      if constexpr (kTwoTiles) load_tile(my_qt, p.q, row0, rows);
+  if (wave < 4) {
+    f32x16 s[TPW];
+#pragma unroll
+    for (int t = 0; t < TPW; ++t) s[t] = zero16();
+    if (p.d_state_out) {
+      const float* si = p.d_state_out + (int64_t)bh * D * D;
+#pragma unroll
+      for (int t = 0; t < TPW; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[t][i] = si[(krow + 32 * t + state_row(i, h2)) * D + vcol];
+    }
+    char* my_kt = kt + w * KT::BYTES;
+    const char* my_qt = kTwoTiles ? qt + w * KT::BYTES : my_kt;
+    frag_t<T> kf[2][CS::KS], tf[NP][2];
+    f32x4 eg, el, beta;
+    float last;
+    auto load_rest = [&](int blk) {
+      load_upper(tf, p.tt, blk);
+      const auto er = vec_rsrc(blk);
+      eg = buf_f4(er, r4 * 4);
+      el = buf_f4(er, (kB + r4) * 4);
+      beta = buf_f4(er, (2 * kB + r4) * 4);
+      last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, (kB - 1) * 4, 0, 0));
+    };
+    load_keys(kf, p.k, nblk - 1);
+    load_rest(nblk - 1);
+    lds_barrier();
+
+    for (int blk = nblk - 1; blk >= 0; --blk) {
+      const int rows = min(kB, len - blk * kB);
+      const int64_t slot = slot_of(blk);
       const bool group_end = (blk + 1) % kDeltaGroup == 0 || blk == nblk - 1;
       if (group_end && (blk != nblk - 1 || p.d_state_out)) {
         // <state, its gradient> at the group's end, this wave's part
-        const int64_t at = (((int64_t)(base / kDeltaGroup + b + blk / kDeltaGroup) * p.heads + h) * CS::NSL + slice) *
-                               CS::WAVES + w;
-        const float* an = p.anchor + at * 2048 + lane * 4;
+        const int64_t at =
+            (((int64_t)(base / kDeltaGroup + b + blk / kDeltaGroup) * p.heads + h) * CS::NSL + slice) * 4 + w;
+        const float* an = p.anchor + at * (TPW * 1024) + lane * 4;
         float dot = 0.f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TPW; ++t)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f32x4 x = *reinterpret_cast<const f32x4*>(an + (4 * t + q) * 256);
@@ -166,137 +154,184 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaParams p) {
       }
       f32x16 ksum[2] = {zero16(), zero16()};
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TPW; ++t)
         static_for<2>([&](auto sl) {
           constexpr int SLI = decltype(sl)::value;
           const Split<T> f = split_acc<SLI>(s[t], tag);
           const int ks = 2 * t + SLI;
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
+          for (int pl = 0; pl < NP; ++pl)
 #pragma unroll
-            for (int pl = 0; pl < NP; ++pl) ksum[rt] = mma32(in.k[rt][ks], f.f[pl], ksum[rt]);
-          T* sn = reinterpret_cast<T*>(p.dsnap) + (slot * D + vcol) * D + krow + 32 * t + 16 * SLI + 8 * h2;
+            for (int rt = 0; rt < 2; ++rt) ksum[rt] = mma32(kf[rt][ks], f.f[pl], ksum[rt]);
+          T* sn = reinterpret_cast<T*>(p.dsnap) + (slot * D + vcol) * D + krow + 16 * ks + 8 * h2;
           *reinterpret_cast<frag_t<T>*>(sn) = f.f[0];
         });
-      put_partial(part_k, w, ksum, lane);
-    }
-    // dO of the quarter as the other waves' operand (exact in T)
-#pragma unroll
-    for (int ct = 0; ct < CS::CT; ++ct) {
-      vec4_t<T> x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = in.dout[ct >> 1][i][ct & 1];
-      *reinterpret_cast<vec4_t<T>*>(od + (16 * ct + c) * CS::PITCH + r4) = x;
-    }
-    __syncthreads();
+      put_partial(part, w, ksum, lane);
+      put_keys(my_kt, kf);
+      load_keys(kf, p.k, blk - 1);
+      lds_barrier();
 
-    // dV' of the quarter
+      // dV' of the quarter
 #pragma unroll
-    for (int ct = 0; ct < CS::CT; ++ct) {
-      f32x4 x = get_partial<CS::RG>(part_k, ct, 4 * w + g16, c);
-      f32x4 xd;
+      for (int ct = 0; ct < CT; ++ct) {
+        f32x4 x = get_partial<RG>(part, ct, 4 * w + g16, c) * el + my_quarter[16 * ct];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = r4 + i < rows ? x[i] * in.el[i] : 0.f;
-        xd[i] = p.scale * in.eg[i] * (float)in.dout[ct >> 1][i][ct & 1];
+        for (int i = 0; i < 4; ++i) x[i] = r4 + i < rows ? x[i] : 0.f;
+        put_opnd<PITCH, OPLANE>(ox, 16 * ct + c, r4, x);
       }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (ks < (w >> 1)) continue;
-        const frag_t<T> df = lds_row8(od + (16 * ct + c) * CS::PITCH + 32 * ks + 8 * g16);
-#pragma unroll
-        for (int pl = 0; pl < NP; ++pl) x = mma(in.pt[pl][ks], df, x);
-      }
-      put_opnd<CS::PITCH, CS::OPLANE>(ox, 16 * ct + c, r4, x);
-      put_opnd<CS::PITCH, CS::OPLANE>(oq, 16 * ct + c, 16 * w + quad_place(g16), xd);
-    }
-    __syncthreads();
+      lds_barrier();
 
-    // dX = T^T dV', dv = beta dX
-    f32x4 vdv = zero4(), xu = zero4();
+      // dX = T^T dV'; the state takes -e^G beta dX
+      const f32x4 scale = eg * beta;
 #pragma unroll
-    for (int ct = 0; ct < CS::CT; ++ct) {
-      f32x4 dx = zero4();
+      for (int ct = 0; ct < CT; ++ct) {
+        f32x4 dx = zero4();
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (ks < (w >> 1)) continue;
-        frag_t<T> tf[NP], xf[NP];
+        for (int ks = 0; ks < 2; ++ks) {
+          if (ks < (w >> 1)) continue;
+          frag_t<T> a[NP], x[NP];
 #pragma unroll
-        for (int pl = 0; pl < NP; ++pl) {
-          tf[pl] = in.tt[pl][ks];
-          xf[pl] = lds_row8(ox + pl * CS::OPLANE + (16 * ct + c) * CS::PITCH + 32 * ks + 8 * g16);
+          for (int pl = 0; pl < NP; ++pl) {
+            a[pl] = tf[pl][ks];
+            x[pl] = lds_row8(ox + pl * OPLANE + (16 * ct + c) * PITCH + 32 * ks + 8 * g16);
+          }
+          dx = mma_split2(a, x, dx, tag);
         }
-        dx = mma_split2(tf, xf, dx, tag);
+        put_opnd<PITCH, OPLANE>(ow, 16 * ct + c, 16 * w + quad_place(g16), -scale * dx);
+        my_quarter[16 * ct] = dx;
       }
-      f32x4 ed;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float dv = in.beta[i] * dx[i];
-        ed[i] = -in.eg[i] * dv;
-        float u = 0.f;
-#pragma unroll
-        for (int pl = 0; pl < NP; ++pl) u += (float)in.u[pl][ct >> 1][i][ct & 1];
-        vdv[i] += dv * (float)in.v[ct >> 1][i][ct & 1];
-        xu[i] += dx[i] * u;
-        if (r4 + i < rows)
-          reinterpret_cast<T*>(p.dv)[(row0 + r4 + i) * vs + h * D + slice * CS::SL + 32 * (ct >> 1) + 2 * c +
-                                     (ct & 1)] = (T)dv;
-      }
-      put_opnd<CS::PITCH, CS::OPLANE>(ow, 16 * ct + c, 16 * w + quad_place(g16), ed);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      vdv[i] = sum16(vdv[i]);
-      xu[i] = sum16(xu[i]);
-    }
-    if (c == 0) {
-      *reinterpret_cast<f32x4*>(p.vdv + (slot * CS::NSL + slice) * kB + r4) = vdv;
-      *reinterpret_cast<f32x4*>(p.xu + (slot * CS::NSL + slice) * kB + r4) = xu;
-    }
-    const float last = in.last;
-    __builtin_amdgcn_s_waitcnt(0);  // the tiles (LDS loads run past the compiler's counting)
-    __syncthreads();
+      const float decay = last;
+      load_rest(blk - 1);
+      lds_barrier();
 
-    ReverseIn<T, D> nx;
-    if (kAhead && blk > 0)
-      load_reverse<T, D>(nx, p, row0 - kB, kB, slot - p.heads, h, hk, slice, w, lane);
-    if (holds) {
       auto add = [&](const char* tile, const T* opnd) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           frag_t<T> f[NP];
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl)
-            f[pl] = lds_row8(opnd + pl * CS::OPLANE + (32 * cg_w + col_place(n)) * CS::PITCH + 16 * ks + 8 * h2);
+            f[pl] = lds_row8(opnd + pl * OPLANE + (32 * cg + col_place(n)) * PITCH + 16 * ks + 8 * h2);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const frag_t<T> a = state_col8<KT>(tile, 16 * ks, 32 * t, lane, tag);
+          for (int t = 0; t < TPW; ++t) {
+            const frag_t<T> a = KT::col(tile, 16 * ks, 32 * t, lane);
 #pragma unroll
             for (int pl = 0; pl < NP; ++pl) s[t] = mma32(a, f[pl], s[t]);
           }
         }
       };
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[t][i] *= last;
+      for (int t = 0; t < TPW; ++t) s[t] *= decay;
       add(my_kt, ow);
       if constexpr (!kTwoTiles) {
-        __builtin_amdgcn_s_waitcnt(kWaitLds);
-        load_tile(my_qt, p.q, row0, rows);
-        __builtin_amdgcn_s_waitcnt(0);
+        frag_t<T> qf[2][CS::KS];
+        load_keys(qf, p.q, blk);
+        put_keys(my_kt, qf);
+        __builtin_amdgcn_wave_barrier();
       }
       add(my_qt, oq);
     }
-    if (kAhead && blk > 0) in = nx;
-  }
-
-  if (holds && p.d_state_in) {
-    float* so = p.d_state_in + (int64_t)bh * D * D;
+    if (p.d_state_in) {
+      float* so = p.d_state_in + (int64_t)bh * D * D;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TPW; ++t)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
+        for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
+    }
+  } else {
+    frag_t<T> qf[2][CS::KS], pf[NP][2];
+    PairOf<T> dout[CG][4], dnext[CG][4], v[CG][4], u[NP][CG][4];
+    f32x4 eg, beta;
+    auto put_dout = [&](const PairOf<T>(&x)[CG][4]) {  // exact in T
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        vec4_t<T> y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (T)x[ct >> 1][i].get(ct & 1);
+        *reinterpret_cast<vec4_t<T>*>(od + (16 * ct + c) * PITCH + r4) = y;
+      }
+    };
+    auto load_values = [&](int blk) {
+      load_pairs(v, p.v, blk);
+#pragma unroll
+      for (int pl = 0; pl < NP; ++pl) load_pairs(u[pl], reinterpret_cast<const T*>(p.u) + pl * (int64_t)p.total * vs, blk);
+      const auto er = vec_rsrc(blk);
+      eg = buf_f4(er, r4 * 4);
+      beta = buf_f4(er, (2 * kB + r4) * 4);
+    };
+    load_pairs(dout, p.dout, nblk - 1);
+    load_upper(pf, p.pt, nblk - 1);
+    if constexpr (kTwoTiles) load_keys(qf, p.q, nblk - 1);
+    load_values(nblk - 1);
+    load_pairs(dnext, p.dout, nblk - 2);
+    put_dout(dout);
+    lds_barrier();
+    for (int blk = nblk - 1; blk >= 0; --blk) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        f32x4 x = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (ks < (w >> 1)) continue;
+          const frag_t<T> d = lds_row8(od + (16 * ct + c) * PITCH + 32 * ks + 8 * g16);
+#pragma unroll
+          for (int pl = 0; pl < NP; ++pl) x = mma(pf[pl][ks], d, x);
+        }
+        my_quarter[16 * ct] = x;
+      }
+      load_upper(pf, p.pt, blk - 1);
+      lds_barrier();
+      if constexpr (kTwoTiles) {
+        put_keys(qt + w * KT::BYTES, qf);
+        load_keys(qf, p.q, blk - 1);
+      }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        f32x4 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = p.scale * eg[i] * dout[ct >> 1][i].get(ct & 1);
+        put_opnd<PITCH, OPLANE>(oq, 16 * ct + c, 16 * w + quad_place(g16), x);
+      }
+      put_dout(dnext);
+#pragma unroll
+      for (int g = 0; g < CG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dout[g][i] = dnext[g][i];
+      load_pairs(dnext, p.dout, blk - 2);
+      lds_barrier();
+      lds_barrier();
+      // dv and the row sums of the quarter
+      const auto rs = value_rsrc(p.dv, blk);
+      f32x4 vdv = zero4(), xu = zero4();
+#pragma unroll
+      for (int g = 0; g < CG; ++g) {
+        f32x4 dv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const f32x4 dx = my_quarter[16 * (2 * g + e)];
+          dv[e] = beta * dx;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y = 0.f;
+#pragma unroll
+            for (int pl = 0; pl < NP; ++pl) y += u[pl][g][i].get(e);
+            vdv[i] += dv[e][i] * v[g][i].get(e);
+            xu[i] += dx[i] * y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) buf_put_pair(rs, pair_off[i] + 32 * g * SZ, dv[0][i], dv[1][i], tag);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vdv[i] = sum16(vdv[i]);
+        xu[i] = sum16(xu[i]);
+      }
+      if (c == 0) {
+        *reinterpret_cast<f32x4*>(p.vdv + (slot_of(blk) * CS::NSL + slice) * kB + r4) = vdv;
+        *reinterpret_cast<f32x4*>(p.xu + (slot_of(blk) * CS::NSL + slice) * kB + r4) = xu;
+      }
+      load_values(blk - 1);
+    }
   }
 }
 
@@ -498,7 +533,7 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
 }
 
 // d log decay and d beta from the row sums, one wave per (group of blocks, head).
-__global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int slices, int waves) {
+__global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int slices) {
   const int groups = (p.blocks_max + kDeltaGroup - 1) / kDeltaGroup;
   const int b = blockIdx.x / groups, grp = blockIdx.x % groups, h = blockIdx.y, lane = threadIdx.x;
   int64_t tok0;
@@ -509,8 +544,8 @@ __global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int 
   const int last = min(nblk, (grp + 1) * kDeltaGroup) - 1;
   float carry = 0.f;
   if (last != nblk - 1 || p.d_state_out) {
-    const float* ad = p.adot + ((int64_t)(base / kDeltaGroup + b + grp) * p.heads + h) * slices * waves;
-    for (int i = 0; i < slices * waves; ++i) carry += ad[i];
+    const float* ad = p.adot + ((int64_t)(base / kDeltaGroup + b + grp) * p.heads + h) * slices * 4;
+    for (int i = 0; i < slices * 4; ++i) carry += ad[i];
   }
   for (int blk = last; blk >= grp * kDeltaGroup; --blk) {
     const int64_t slot = (int64_t)(base + blk) * p.heads + h;
@@ -541,14 +576,13 @@ __global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int 
 template <typename T, int D>
 static hipError_t launch_backward(const DeltaParams& p, hipStream_t stream) {
   using CS = ChainShape<T, D>;
-  hipLaunchKernelGGL((delta_reverse_kernel<T, D>), dim3(CS::NSL * p.batch * p.heads), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((delta_reverse_kernel<T, D>), dim3(CS::NSL * p.batch * p.heads), dim3(512), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((delta_qk_grad_kernel<T, D>), dim3(p.batch * p.blocks_max, p.k_heads), dim3(2 * D), 0, stream, p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int groups = (p.blocks_max + kDeltaGroup - 1) / kDeltaGroup;
-  hipLaunchKernelGGL(delta_gate_grad_kernel, dim3(p.batch * groups, p.heads), dim3(64), 0, stream, p, CS::NSL,
-                     CS::WAVES);
+  hipLaunchKernelGGL(delta_gate_grad_kernel, dim3(p.batch * groups, p.heads), dim3(64), 0, stream, p, CS::NSL);
   return hipGetLastError();
 }
 

@@ -87,52 +87,79 @@ __device__ __forceinline__ void seq_span(const DeltaParams& p, int b, int64_t& t
 //   key row within the tile of accumulator element i, half h:
 __device__ __forceinline__ constexpr int state_row(int i, int h) { return 16 * (i / 8) + 8 * h + (i % 8); }
 
-// Column fragment (tile_col8w) of 32 key columns from n0 in that order: inside
-// 16 columns the groups of four come as 0, 2, 1, 3.
-template <typename TL>
-__device__ __forceinline__ bf16x8 state_col8(const char* t, int k0, int n0, int lane, bf16*) {
-  const int grp = lane >> 4, m = lane & 15, h = grp >> 1;
-  const int q = m & 3, cg = ((q & 1) << 1) | (q >> 1);
-  const char* p = t + TL::off(k0 + 4 * h + (m >> 2), n0 + 16 * (grp & 1) + 4 * cg);
-  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + TL::row_step(8)));
-  typedef short i16x8 __attribute__((ext_vector_type(8)));
-  const i16x8 w = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  return __builtin_bit_cast(bf16x8, w);
-}
-template <typename TL>
-__device__ __forceinline__ f32x8 state_col8(const char* t, int k0, int n0, int lane, float*) {
-  const int n = lane & 31, h = lane >> 5;
-  const int q = (n >> 2) & 3, cg = ((q & 1) << 1) | (q >> 1);
-  const int col = n0 + (n & 16) + 4 * cg + (n & 3);
-  f32x8 f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[j] = *reinterpret_cast<const float*>(t + TL::off(k0 + 4 * h + j, col));
-    f[4 + j] = *reinterpret_cast<const float*>(t + TL::off(k0 + 8 + 4 * h + j, col));
-  }
-  return f;
-}
-
 // ---------------------------------------------------------------------------
-// How a workgroup of four waves holds the state of 32 CG value columns: wave w
-// the key rows 64 (w % RG) .. + 63 of the columns 32 (w / RG) .. + 31, two
-// 32x32 tiles. The fp32 type takes twice the LDS, so at d = 128 it has half
-// the columns.
+// How a workgroup holds the state of SL value columns: four waves, wave w the
+// key rows 32 TPW (w % RG) .. of the columns 32 (w / RG) .. + 31, TPW tiles of
+// 32 x 32. Another four waves of the workgroup take what is not on the way
+// from one block's state to the next.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 struct ChainShape {
-  static constexpr int RG = D / 64;
-  static constexpr int CG = (D == 256 || (sizeof(T) == 4 && D == 128)) ? 1 : 2;
-  static constexpr int WAVES = RG * CG;  // waves that hold state, of 4
-  static constexpr int SL = 32 * CG;     // value columns of a workgroup
+  static constexpr int TPW = D == 256 ? 2 : 1;
+  static constexpr int RG = D == 64 ? 2 : 4;
+  static constexpr int CG = 4 / RG;
+  static constexpr int KR = 32 * TPW;   // key rows of a wave
+  static constexpr int KS = 2 * TPW;    // contraction steps over them
+  static constexpr int SL = 32 * CG;    // value columns of a workgroup
   static constexpr int NSL = D / SL;
-  static constexpr int CT = 2 * CG;  // 16-column tiles of a wave's quarter of the rows
+  static constexpr int CT = 2 * CG;     // 16-column tiles of a wave's quarter of the tokens
   // operand copies [column][token] in LDS: 64 tokens and padding
   static constexpr int PITCH = sizeof(T) == 2 ? 72 : 68;
   static constexpr int OPLANE = SL * PITCH;  // elements of one plane
   static constexpr int OPND = OPLANE * Planes<T>::N;
-  using KTile = LTile<T, kB, 64, kColTile>;  // a wave's 64 key columns of a block
+  // copy of the state [column][key row] in LDS
+  static constexpr int SPITCH = D + (sizeof(T) == 2 ? 8 : 4);
+  static constexpr int SPLANE = SL * SPITCH;
+};
+
+// A wave's 64 tokens x KR key columns in LDS, written by rows (8 elements of a
+// token's row) and read by columns. 16-byte chunks of a bf16 row are swapped
+// within the row by its number, so that 16 rows' writes of one chunk and the
+// transposed reads of 4 rows x 4 chunks meet distinct banks.
+template <typename T, int KR> struct KeyTile;
+template <int KR> struct KeyTile<bf16, KR> {
+  static constexpr int BYTES = kB * KR * 2;
+  __device__ static __forceinline__ int chunk(int r, int ch) {
+    const int f = KR == 64 ? ((((r >> 1) & 1) << 2) | ((r >> 2) & 3)) : ((r >> 2) & 3);
+    return r * (KR * 2) + ((ch ^ f) << 4);
+  }
+  __device__ static __forceinline__ void put(char* t, int r, int col, const bf16x8& x) {
+    *reinterpret_cast<bf16x8*>(t + chunk(r, col >> 3)) = x;
+  }
+  // Column fragment of tokens k0 .. k0 + 15 (k0 a multiple of 16, lane half h
+  // the tokens k0 + 4h .. and k0 + 8 + 4h ..) and of the 32 key columns from n0
+  // in the accumulator's order: inside 16 columns the groups of four come as
+  // 0, 2, 1, 3.
+  __device__ static __forceinline__ bf16x8 col(const char* t, int k0, int n0, int lane) {
+    const int grp = lane >> 4, m = lane & 15, h = grp >> 1;
+    const int q = m & 3, cg = ((q & 1) << 1) | (q >> 1);
+    const int c = n0 + 16 * (grp & 1) + 4 * cg, r = k0 + 4 * h + (m >> 2);
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(t + chunk(r, c >> 3) + 2 * (c & 7)));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(t + chunk(r + 8, c >> 3) + 2 * (c & 7)));
+    typedef short i16x8 __attribute__((ext_vector_type(8)));
+    const i16x8 w = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8, w);
+  }
+};
+template <int KR> struct KeyTile<float, KR> {
+  static constexpr int BYTES = kB * KR * 4;
+  __device__ static __forceinline__ void put(char* t, int r, int col, const f32x8& x) {
+    f32x4* p = reinterpret_cast<f32x4*>(t + (r * KR + col) * 4);
+    p[0] = f32x4{x[0], x[1], x[2], x[3]};
+    p[1] = f32x4{x[4], x[5], x[6], x[7]};
+  }
+  __device__ static __forceinline__ f32x8 col(const char* t, int k0, int n0, int lane) {
+    const int n = lane & 31, h = lane >> 5;
+    const int q = (n >> 2) & 3, cg = ((q & 1) << 1) | (q >> 1);
+    const float* p = reinterpret_cast<const float*>(t) + (k0 + 4 * h) * KR + n0 + (n & 16) + 4 * cg + (n & 3);
+    f32x8 f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = p[j * KR];
+      f[4 + j] = p[(8 + j) * KR];
+    }
+    return f;
+  }
 };
 
 // A value column of a workgroup and its place: the quarter-row products take
@@ -180,8 +207,52 @@ __device__ __forceinline__ void put_opnd(float* m, int row, int at, const f32x4&
 // reads its two quads side by side
 __device__ __forceinline__ constexpr int quad_place(int g) { return 4 * (((g & 1) << 1) | (g >> 1)); }
 
-// s_waitcnt immediate: LDS accesses done, loads and stores may be in flight
-constexpr int kWaitLds = 0xC07F;
+// ---------------------------------------------------------------------------
+// Reads and writes through a buffer descriptor whose end is the end of what
+// exists: rows behind it read as zero and are not written, without a branch.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ u32x4b raw_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+}
+__device__ __forceinline__ bf16x8 buf_frag(__amdgpu_buffer_rsrc_t rs, uint32_t off, bf16*) {
+  return __builtin_bit_cast(bf16x8, raw_load16(rs, off));
+}
+__device__ __forceinline__ f32x8 buf_frag(__amdgpu_buffer_rsrc_t rs, uint32_t off, float*) {
+  const f32x4 a = __builtin_bit_cast(f32x4, raw_load16(rs, off)), b = __builtin_bit_cast(f32x4, raw_load16(rs, off + 16));
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+__device__ __forceinline__ f32x4 buf_f4(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  return __builtin_bit_cast(f32x4, raw_load16(rs, off));
+}
+// two neighbouring elements
+typedef uint32_t u32x2b __attribute__((ext_vector_type(2)));
+template <typename T> struct PairOf;
+template <> struct PairOf<bf16> {
+  uint32_t w;
+  __device__ __forceinline__ float get(int e) const { return __uint_as_float(e ? w & 0xffff0000u : w << 16); }
+};
+template <> struct PairOf<float> {
+  u32x2b w;
+  __device__ __forceinline__ float get(int e) const { return __uint_as_float(w[e]); }
+};
+__device__ __forceinline__ PairOf<bf16> buf_pair(__amdgpu_buffer_rsrc_t rs, uint32_t off, bf16*) {
+  return PairOf<bf16>{__builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0)};
+}
+__device__ __forceinline__ PairOf<float> buf_pair(__amdgpu_buffer_rsrc_t rs, uint32_t off, float*) {
+  return PairOf<float>{__builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0)};
+}
+__device__ __forceinline__ void buf_put_pair(__amdgpu_buffer_rsrc_t rs, uint32_t off, float a, float b, bf16*) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 x = {(bf16)a, (bf16)b};
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), rs, off, 0, 0);
+}
+__device__ __forceinline__ void buf_put_pair(__amdgpu_buffer_rsrc_t rs, uint32_t off, float a, float b, float*) {
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2b{__float_as_uint(a), __float_as_uint(b)}, rs, off, 0, 0);
+}
+
+// Barrier of the waves' LDS traffic alone: loads and stores of global memory
+// stay in flight across it.
+__device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ int xcd_swizzle(int id, int total) {
   // workgroups go round the 8 XCDs; neighbours in the result share an XCD's L2

@@ -195,318 +195,321 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
   }
 }
 
-// What a wave reads of a block before it can start on it.
-template <typename T, int D, bool GRAD>
-struct BlockIn {
-  using CS = ChainShape<T, D>;
-  static constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1;
-  frag_t<T> k[2][4], q[2][4];       // rows of K and Q, the wave's 64 key columns
-  frag_t<T> t[NP][2], p[PP][2];     // rows 16 w .. + 15 of T and P
-  T v[CS::CG][4][2];                // the quarter's values
-  T dout[GRAD ? CS::CG : 1][4][2];
-  f32x4 eg, el, beta;
-  float last;
-};
-
-template <typename T, int D, bool GRAD>
-__device__ __forceinline__ void load_block(BlockIn<T, D, GRAD>& in, const DeltaParams& p, int64_t row0, int rows,
-                                           int64_t slot, int h, int hk, int slice, int w, int lane) {
-  using CS = ChainShape<T, D>;
-  constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1;
-  const int n = lane & 31, h2 = lane >> 5, g16 = lane >> 4, c = lane & 15;
-  const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
-  const float* vec = p.vec + slot * (4 * kB);
-  const T* tm = reinterpret_cast<const T*>(p.t) + slot * (NP * kB * kB) + (16 * w + c) * kB + 8 * g16;
-  const T* pm = reinterpret_cast<const T*>(p.p) + slot * (PP * kB * kB) + (16 * w + c) * kB + 8 * g16;
-  if (w < CS::WAVES) {
-    const int64_t at = row0 * qs + hk * D + 64 * (w % CS::RG) + 8 * h2;
-    const T* K = reinterpret_cast<const T*>(p.k) + at;
-    const T* Q = reinterpret_cast<const T*>(p.q) + at;
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const int r = 32 * rt + n;
-        in.k[rt][ks] = global_row8(K + r * qs + 16 * ks, r < rows);
-        in.q[rt][ks] = global_row8(Q + r * qs + 16 * ks, r < rows);
-      }
-  }
-#pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    if (ks > (w >> 1)) break;  // T and P are lower triangular
-#pragma unroll
-    for (int pl = 0; pl < NP; ++pl) in.t[pl][ks] = global_row8(tm + pl * kB * kB + 32 * ks, true);
-#pragma unroll
-    for (int pl = 0; pl < PP; ++pl) in.p[pl][ks] = global_row8(pm + pl * kB * kB + 32 * ks, true);
-  }
-  const int r4 = 16 * w + 4 * g16;
-  const T* V = reinterpret_cast<const T*>(p.v) + row0 * vs + h * D + slice * CS::SL + 2 * c;
-  const T* DO = GRAD ? reinterpret_cast<const T*>(p.dout) + row0 * vs + h * D + slice * CS::SL + 2 * c : nullptr;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int cg = 0; cg < CS::CG; ++cg)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        in.v[cg][i][e] = r4 + i < rows ? V[(r4 + i) * vs + 32 * cg + e] : (T)0.f;
-        if constexpr (GRAD) in.dout[cg][i][e] = r4 + i < rows ? DO[(r4 + i) * vs + 32 * cg + e] : (T)0.f;
-      }
-  in.eg = *reinterpret_cast<const f32x4*>(vec + r4);
-  in.el = *reinterpret_cast<const f32x4*>(vec + kB + r4);
-  in.beta = *reinterpret_cast<const f32x4*>(vec + 2 * kB + r4);
-  in.last = vec[kB - 1];
-}
-
 // The state's way through one sequence's blocks, for SL value columns of one
 // head; GRAD: the same walk for the backward, which keeps V', the states and
 // the row sums o . dO in place of the output.
-// A block takes three exchanges between the waves: each wave multiplies its 64
-// key rows of S into K S (partial sums of all 64 tokens); a quarter of the
-// tokens each, the waves add these up to X; V' = T X, a quarter each; then
-// every wave adds K^T V' to its rows. Q S and P V' follow in the gaps.
+// Bound by the way from one block's state to the next, which takes three
+// exchanges between the four state waves: each multiplies its key rows of S
+// into K S (partial sums of all 64 tokens); a quarter of the tokens each, they
+// add these up to X; V' = T X, a quarter each; then every wave adds K^T V' to
+// its rows. The other four waves follow with the output, a quarter of the
+// tokens each: Q S from a copy of the state in LDS while the state waves are at
+// X and V', then P V'. What a block reads is asked for a block ahead.
 template <typename T, int D, bool GRAD>
-__global__ __launch_bounds__(256) void delta_chain_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
-  using KT = typename CS::KTile;
-  constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1;
+  using KT = KeyTile<T, CS::KR>;
+  constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1, SZ = sizeof(T);
+  constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
   T* const tag = nullptr;
-  __shared__ __attribute__((aligned(1024))) char kt[CS::WAVES * KT::BYTES];
-  __shared__ __attribute__((aligned(16))) f32x4 part_k[CS::WAVES * 512], part_q[CS::WAVES * 512];
+  __shared__ __attribute__((aligned(16))) char kt[4 * KT::BYTES];
+  __shared__ __attribute__((aligned(16))) f32x4 part[4 * 512];
   __shared__ __attribute__((aligned(16))) T ox[CS::OPND], ov[CS::OPND], ow[CS::OPND];
+  __shared__ __attribute__((aligned(16))) T os[CS::SPLANE * PP];
 
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform_i(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i(tid >> 6), w = wave & 3;
   const int id = xcd_swizzle(blockIdx.x, gridDim.x);
   const int slice = id % CS::NSL, bh = id / CS::NSL, h = bh % p.heads, b = bh / p.heads;
   const int hk = h / (p.heads / p.k_heads);
-  const int rg = w % CS::RG, cg_w = w / CS::RG;
-  const bool holds = w < CS::WAVES;
   const int n = lane & 31, h2 = lane >> 5, g16 = lane >> 4, c = lane & 15;
+  const int r4 = 16 * w + 4 * g16;  // the lane's four tokens of the wave's quarter
   int64_t tok0;
   int len, base;
   seq_span(p, b, tok0, len, base);
   const int nblk = (len + kB - 1) / kB;
   const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
-
-  // the state's element (tile t, i): key row krow + 32 t + state_row(i, h2),
-  // value column vcol
-  const int krow = 64 * rg, vcol = slice * CS::SL + 32 * cg_w + n;
-  f32x16 s[2] = {zero16(), zero16()};
-  if (holds && p.state_in) {
-    const float* si = p.state_in + (int64_t)bh * D * D;
+  const uint32_t qrow = (uint32_t)qs * SZ, vrow = (uint32_t)vs * SZ;
+  // descriptors of block blk (no rows: nothing is read)
+  auto rows_of = [&](int blk) { return blk < nblk ? min(kB, len - blk * kB) : 0; };
+  auto key_rsrc = [&](const void* x, int blk) {
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + (tok0 + (int64_t)blk * kB) * qs + hk * D, rows_of(blk) * qrow);
+  };
+  auto value_rsrc = [&](const void* x, int blk) {
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + (tok0 + (int64_t)blk * kB) * vs + h * D, rows_of(blk) * vrow);
+  };
+  auto slot_of = [&](int blk) { return (int64_t)(base + blk) * p.heads + h; };
+  auto mat_rsrc = [&](const void* x, int planes, int blk) {
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + slot_of(blk) * (planes * kB * kB),
+                       blk < nblk ? planes * kB * kB * SZ : 0);
+  };
+  auto vec_rsrc = [&](int blk) { return scalar_rsrc(p.vec + slot_of(blk) * (4 * kB), blk < nblk ? 4 * kB * 4 : 0); };
+  const uint32_t mat_off = ((16 * w + c) * kB + 8 * g16) * SZ;
+  uint32_t pair_off[4];  // the lane's pairs of value columns, token i
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+  for (int i = 0; i < 4; ++i) pair_off[i] = (r4 + i) * vrow + (slice * CS::SL + 2 * c) * SZ;
+
+  if (wave < 4) {
+    const int rg = w % RG, cg = w / RG;
+    // the state's element (tile t, i): key row krow + 32 t + state_row(i, h2), value column vcol
+    const int krow = CS::KR * rg, vcol = slice * CS::SL + 32 * cg + n;
+    f32x16 s[TPW];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[t][i] = si[(krow + 32 * t + state_row(i, h2)) * D + vcol];
-  }
+    for (int t = 0; t < TPW; ++t) s[t] = zero16();
+    if (p.state_in) {
+      const float* si = p.state_in + (int64_t)bh * D * D;
+#pragma unroll
+      for (int t = 0; t < TPW; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[t][i] = si[(krow + 32 * t + state_row(i, h2)) * D + vcol];
+    }
+    char* my_kt = kt + w * KT::BYTES;
+    const uint32_t key_off[2] = {n * qrow + (krow + 8 * h2) * SZ, (32 + n) * qrow + (krow + 8 * h2) * SZ};
+    T* my_os = os + (32 * cg + col_place(n)) * CS::SPITCH + krow + 8 * h2;
 
-  char* my_kt = kt + w * KT::BYTES;
-  TileLoads<T, KT, 1> loads;
-  loads.init(qs, lane);
-  // bf16 reads a block ahead; the fp32 operands do not fit the registers twice
-  constexpr bool kAhead = sizeof(T) == 2;
-  BlockIn<T, D, GRAD> in;
-  if (kAhead && nblk)
-    load_block<T, D, GRAD>(in, p, tok0, min(kB, len), (int64_t)base * p.heads + h, h, hk, slice, w, lane);
+    frag_t<T> kf[2][CS::KS], tf[NP][2];
+    PairOf<T> v[CG][4];
+    f32x4 eg, el, beta;
+    float last;
+    auto load_keys = [&](int blk) {
+      const auto rs = key_rsrc(p.k, blk);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int ks = 0; ks < CS::KS; ++ks) kf[rt][ks] = buf_frag(rs, key_off[rt] + 16 * ks * SZ, tag);
+    };
+    auto load_rest = [&](int blk) {
+      const auto tr = mat_rsrc(p.t, NP, blk);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if (ks > (w >> 1)) break;  // T is lower triangular
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) tf[pl][ks] = buf_frag(tr, mat_off + (pl * kB * kB + 32 * ks) * SZ, tag);
+      }
+      const auto vr = value_rsrc(p.v, blk);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int g = 0; g < CG; ++g) v[g][i] = buf_pair(vr, pair_off[i] + 32 * g * SZ, tag);
+      const auto er = vec_rsrc(blk);
+      eg = buf_f4(er, r4 * 4);
+      el = buf_f4(er, (kB + r4) * 4);
+      beta = buf_f4(er, (2 * kB + r4) * 4);
+      last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, (kB - 1) * 4, 0, 0));
+    };
+    load_keys(0);
+    load_rest(0);
 
-  for (int blk = 0; blk < nblk; ++blk) {
-    const int64_t row0 = tok0 + (int64_t)blk * kB;
-    const int rows = min(kB, len - blk * kB);
-    const int64_t slot = (int64_t)(base + blk) * p.heads + h;
-    if constexpr (!kAhead) load_block<T, D, GRAD>(in, p, row0, rows, slot, h, hk, slice, w, lane);
-    f32x16 qsum[2] = {zero16(), zero16()};
-    if (holds) {
-      // K's tile for the state's update, read after the third exchange
-      const T* Kt = reinterpret_cast<const T*>(p.k) + row0 * qs + hk * D + krow;
-      __builtin_amdgcn_s_waitcnt(kWaitLds);  // the last block's reads of the tile
-      if (rows == kB)
-        loads.issue(my_kt, Kt, qs, 0, 0);
-      else
-        loads.issue_clamped(my_kt, Kt, qs, 0, rows - 1, 0);
+    for (int blk = 0; blk < nblk; ++blk) {
+      const int rows = min(kB, len - blk * kB);
       f32x16 ksum[2] = {zero16(), zero16()};
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TPW; ++t)
         static_for<2>([&](auto sl) {
           constexpr int SLI = decltype(sl)::value;
           const Split<T> f = split_acc<SLI>(s[t], tag);
           const int ks = 2 * t + SLI;
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt) {
+          for (int pl = 0; pl < NP; ++pl)
 #pragma unroll
-            for (int pl = 0; pl < NP; ++pl) ksum[rt] = mma32(in.k[rt][ks], f.f[pl], ksum[rt]);
+            for (int rt = 0; rt < 2; ++rt) ksum[rt] = mma32(kf[rt][ks], f.f[pl], ksum[rt]);
 #pragma unroll
-            for (int pl = 0; pl < PP; ++pl) qsum[rt] = mma32(in.q[rt][ks], f.f[pl], qsum[rt]);
-          }
-          if constexpr (GRAD) {
-            // the state at the block's start, [dv][dk], for the gradients of q and k
-            T* sn = reinterpret_cast<T*>(p.snap) + (slot * D + vcol) * D + krow + 32 * t + 16 * SLI + 8 * h2;
-            *reinterpret_cast<frag_t<T>*>(sn) = f.f[0];
-          }
+          for (int pl = 0; pl < PP; ++pl)
+            *reinterpret_cast<frag_t<T>*>(my_os + pl * CS::SPLANE + 16 * ks) = f.f[pl];
         });
+      put_partial(part, w, ksum, lane);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int ks = 0; ks < CS::KS; ++ks) KT::put(my_kt, 32 * rt + n, 16 * ks + 8 * h2, kf[rt][ks]);
+      load_keys(blk + 1);
       if constexpr (GRAD) {
         if (blk && blk % kDeltaGroup == 0) {
           float* an = p.anchor + ((((int64_t)(base / kDeltaGroup + b + blk / kDeltaGroup - 1) * p.heads + h) * CS::NSL +
-                                   slice) * CS::WAVES + w) * 2048 + lane * 4;
+                                   slice) * 4 + w) * (TPW * 1024) + lane * 4;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < TPW; ++t)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               *reinterpret_cast<f32x4*>(an + (4 * t + q) * 256) =
                   f32x4{s[t][4 * q], s[t][4 * q + 1], s[t][4 * q + 2], s[t][4 * q + 3]};
         }
       }
-      put_partial(part_k, w, ksum, lane);
-    }
-    __syncthreads();
+      lds_barrier();
 
-    // X of rows 16 w + 4 g16 + i
+      // X of the quarter
 #pragma unroll
-    for (int ct = 0; ct < CS::CT; ++ct) {
-      const f32x4 ks = get_partial<CS::RG>(part_k, ct, 4 * w + g16, c);
-      f32x4 x;
+      for (int ct = 0; ct < CT; ++ct) {
+        const f32x4 ks = get_partial<RG>(part, ct, 4 * w + g16, c);
+        f32x4 x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float y = in.beta[i] * ((float)in.v[ct >> 1][i][ct & 1] - in.eg[i] * ks[i]);
-        x[i] = 16 * w + 4 * g16 + i < rows ? y : 0.f;
-      }
-      put_opnd<CS::PITCH, CS::OPLANE>(ox, 16 * ct + c, 16 * w + 4 * g16, x);
-    }
-    if (holds) put_partial(part_q, w, qsum, lane);
-    __syncthreads();
-
-    // V' = T X
-    f32x4 u[CS::CT];
-#pragma unroll
-    for (int ct = 0; ct < CS::CT; ++ct) {
-      u[ct] = zero4();
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (ks > (w >> 1)) break;
-        frag_t<T> tf[NP], xf[NP];
-#pragma unroll
-        for (int pl = 0; pl < NP; ++pl) {
-          tf[pl] = in.t[pl][ks];
-          xf[pl] = lds_row8(ox + pl * CS::OPLANE + (16 * ct + c) * CS::PITCH + 32 * ks + 8 * g16);
+        for (int i = 0; i < 4; ++i) {
+          const float y = beta[i] * (v[ct >> 1][i].get(ct & 1) - eg[i] * ks[i]);
+          x[i] = r4 + i < rows ? y : 0.f;
         }
-        u[ct] = mma_split2(tf, xf, u[ct], tag);
+        put_opnd<PITCH, OPLANE>(ox, 16 * ct + c, r4, x);
       }
-      put_opnd<CS::PITCH, CS::OPLANE>(ov, 16 * ct + c, 16 * w + 4 * g16, u[ct]);
-      f32x4 ud;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ud[i] = u[ct][i] * in.el[i];
-      put_opnd<CS::PITCH, CS::OPLANE>(ow, 16 * ct + c, 16 * w + quad_place(g16), ud);
-    }
-    const float last = in.last;
-    __builtin_amdgcn_s_waitcnt(0);  // the K tile (LDS loads run past the compiler's counting)
-    __syncthreads();
+      lds_barrier();
 
-    // the next block's reads overlap the state's update
-    BlockIn<T, D, GRAD> nx;
-    if (kAhead && blk + 1 < nblk)
-      load_block<T, D, GRAD>(nx, p, row0 + kB, min(kB, len - (blk + 1) * kB), slot + p.heads, h, hk, slice, w, lane);
+      // V' = T X
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        f32x4 u = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (ks > (w >> 1)) break;
+          frag_t<T> a[NP], x[NP];
+#pragma unroll
+          for (int pl = 0; pl < NP; ++pl) {
+            a[pl] = tf[pl][ks];
+            x[pl] = lds_row8(ox + pl * OPLANE + (16 * ct + c) * PITCH + 32 * ks + 8 * g16);
+          }
+          u = mma_split2(a, x, u, tag);
+        }
+        put_opnd<PITCH, OPLANE>(ow, 16 * ct + c, 16 * w + quad_place(g16), u * el);
+        put_opnd<PITCH, OPLANE>(ov, 16 * ct + c, r4, u);
+      }
+      const float decay = last;
+      load_rest(blk + 1);
+      lds_barrier();
 
-    if (holds) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[t][i] *= last;
+      for (int t = 0; t < TPW; ++t) s[t] *= decay;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         frag_t<T> uf[NP];
 #pragma unroll
         for (int pl = 0; pl < NP; ++pl)
-          uf[pl] = lds_row8(ow + pl * CS::OPLANE + (32 * cg_w + col_place(n)) * CS::PITCH + 16 * ks + 8 * h2);
+          uf[pl] = lds_row8(ow + pl * OPLANE + (32 * cg + col_place(n)) * PITCH + 16 * ks + 8 * h2);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const frag_t<T> kf = state_col8<KT>(my_kt, 16 * ks, 32 * t, lane, tag);
+        for (int t = 0; t < TPW; ++t) {
+          const frag_t<T> a = KT::col(my_kt, 16 * ks, 32 * t, lane);
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl) s[t] = mma32(kf, uf[pl], s[t]);
+          for (int pl = 0; pl < NP; ++pl) s[t] = mma32(a, uf[pl], s[t]);
         }
       }
     }
-    // O of the quarter
-    f32x4 dot = zero4();
+    if (p.state_out) {
+      float* so = p.state_out + (int64_t)bh * D * D;
 #pragma unroll
-    for (int cg = 0; cg < CS::CG; ++cg) {
-      f32x4 o2[2];
+      for (int t = 0; t < TPW; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int ct = 2 * cg + e;
-        f32x4 o = get_partial<CS::RG>(part_q, ct, 4 * w + g16, c);
+        for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
+    }
+    if constexpr (GRAD) {
+      if (nblk && p.d_state_out) {  // the last group's copy: only a gradient of the final state meets it
+        float* an = p.anchor + ((((int64_t)(base / kDeltaGroup + b + (nblk - 1) / kDeltaGroup) * p.heads + h) * CS::NSL +
+                                 slice) * 4 + w) * (TPW * 1024) + lane * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] *= p.scale * in.eg[i];
+        for (int t = 0; t < TPW; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(an + (4 * t + q) * 256) =
+                f32x4{s[t][4 * q], s[t][4 * q + 1], s[t][4 * q + 2], s[t][4 * q + 3]};
+      }
+    }
+  } else {
+    frag_t<T> qf[D / 32], pf[PP][2];
+    PairOf<T> dout[CG][4];
+    f32x4 eg;
+    auto load_queries = [&](int blk) {
+      const auto rs = key_rsrc(p.q, blk);
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks) qf[ks] = buf_frag(rs, (16 * w + c) * qrow + (32 * ks + 8 * g16) * SZ, tag);
+    };
+    auto load_rest = [&](int blk) {
+      const auto pr = mat_rsrc(p.p, PP, blk);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if (ks > (w >> 1)) break;
+#pragma unroll
+        for (int pl = 0; pl < PP; ++pl) pf[pl][ks] = buf_frag(pr, mat_off + (pl * kB * kB + 32 * ks) * SZ, tag);
+      }
+      eg = buf_f4(vec_rsrc(blk), r4 * 4);
+      if constexpr (GRAD) {
+        const auto dr = value_rsrc(p.dout, blk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int g = 0; g < CG; ++g) dout[g][i] = buf_pair(dr, pair_off[i] + 32 * g * SZ, tag);
+      }
+    };
+    load_queries(0);
+    load_rest(0);
+    for (int blk = 0; blk < nblk; ++blk) {
+      lds_barrier();
+      f32x4 o[CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) o[ct] = zero4();
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int pl = 0; pl < PP; ++pl)
+            o[ct] = mma(qf[ks], lds_row8(os + pl * CS::SPLANE + (16 * ct + c) * CS::SPITCH + 32 * ks + 8 * g16), o[ct]);
+      load_queries(blk + 1);
+      if constexpr (GRAD) {
+        // the state at the block's start, [dv][dk], for the gradients of q and k
+        T* sn = reinterpret_cast<T*>(p.snap) + slot_of(blk) * D * D;
+        for (int i = tid - 256; i < CS::SL * D / 8; i += 256) {
+          const int row = i / (D / 8), at = i % (D / 8) * 8, pl = row & 31;
+          const int col = slice * CS::SL + (row & 32) + 2 * (pl & 15) + (pl >> 4);
+          copy8(sn + (int64_t)col * D + at, os + row * CS::SPITCH + at);
+        }
+      }
+      lds_barrier();
+      lds_barrier();
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        o[ct] *= p.scale * eg;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           if (ks > (w >> 1)) break;
-          frag_t<T> vf[NP];
+          frag_t<T> u[NP];
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl)
-            vf[pl] = lds_row8(ov + pl * CS::OPLANE + (16 * ct + c) * CS::PITCH + 32 * ks + 8 * g16);
+          for (int pl = 0; pl < NP; ++pl) u[pl] = lds_row8(ov + pl * OPLANE + (16 * ct + c) * PITCH + 32 * ks + 8 * g16);
           if constexpr (GRAD) {
-            frag_t<T> pf[NP];
+            frag_t<T> a[NP];
 #pragma unroll
-            for (int pl = 0; pl < NP; ++pl) pf[pl] = in.p[pl][ks];
-            o = mma_split2(pf, vf, o, tag);
+            for (int pl = 0; pl < NP; ++pl) a[pl] = pf[pl][ks];
+            o[ct] = mma_split2(a, u, o[ct], tag);
           } else {
 #pragma unroll
-            for (int pl = 0; pl < NP; ++pl) o = mma(in.p[0][ks], vf[pl], o);
-          }
-        }
-        o2[e] = o;
-        if constexpr (GRAD) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dot[i] += o[i] * (float)in.dout[cg][i][e];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * w + 4 * g16 + i;
-        if (r >= rows) continue;
-        const int64_t at = (row0 + r) * vs + h * D + slice * CS::SL + 32 * cg + 2 * c;
-        if constexpr (!GRAD) {
-          T* o = reinterpret_cast<T*>(p.o) + at;
-          o[0] = (T)o2[0][i];
-          o[1] = (T)o2[1][i];
-        } else {
-          // V' in planes of whole tensors
-          const int64_t plane = (int64_t)p.total * vs;
-          T* uo = reinterpret_cast<T*>(p.u) + at;
-          float r0 = u[2 * cg][i], r1 = u[2 * cg + 1][i];
-#pragma unroll
-          for (int pl = 0; pl < NP; ++pl) {
-            const T a0 = (T)r0, a1 = (T)r1;
-            uo[pl * plane] = a0;
-            uo[pl * plane + 1] = a1;
-            r0 -= (float)a0;
-            r1 -= (float)a1;
+            for (int pl = 0; pl < NP; ++pl) o[ct] = mma(pf[0][ks], u[pl], o[ct]);
           }
         }
       }
-    }
-    if constexpr (GRAD) {
+      if constexpr (!GRAD) {
+        const auto orsrc = value_rsrc(p.o, blk);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dot[i] = sum16(dot[i]);
-      if (c == 0) *reinterpret_cast<f32x4*>(p.odo + (slot * CS::NSL + slice) * kB + 16 * w + 4 * g16) = dot;
-    }
-    if (kAhead && blk + 1 < nblk) in = nx;
-  }
-
-  if (holds && p.state_out) {
-    float* so = p.state_out + (int64_t)bh * D * D;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+          for (int g = 0; g < CG; ++g)
+            buf_put_pair(orsrc, pair_off[i] + 32 * g * SZ, o[2 * g][i], o[2 * g + 1][i], tag);
+      } else {
+        f32x4 dot = zero4();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
-  }
-  if constexpr (GRAD) {
-    if (holds && nblk && p.d_state_out) {  // the last group's copy: only a gradient of the final state meets it
-      float* an = p.anchor + ((((int64_t)(base / kDeltaGroup + b + (nblk - 1) / kDeltaGroup) * p.heads + h) * CS::NSL +
-                               slice) * CS::WAVES + w) * 2048 + lane * 4;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+          for (int ct = 0; ct < CT; ++ct) dot[i] += o[ct][i] * dout[ct >> 1][i].get(ct & 1);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<f32x4*>(an + (4 * t + q) * 256) =
-              f32x4{s[t][4 * q], s[t][4 * q + 1], s[t][4 * q + 2], s[t][4 * q + 3]};
+        for (int i = 0; i < 4; ++i) dot[i] = sum16(dot[i]);
+        if (c == 0) *reinterpret_cast<f32x4*>(p.odo + (slot_of(blk) * CS::NSL + slice) * kB + r4) = dot;
+        // V' in planes of whole tensors
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) {
+          const auto ur = value_rsrc(reinterpret_cast<const T*>(p.u) + pl * (int64_t)p.total * vs, blk);
+#pragma unroll
+          for (int g = 0; g < CG; ++g) {
+            const vec4_t<T> x = *reinterpret_cast<const vec4_t<T>*>(ov + pl * OPLANE + (32 * g + c) * PITCH + r4);
+            const vec4_t<T> y = *reinterpret_cast<const vec4_t<T>*>(ov + pl * OPLANE + (32 * g + 16 + c) * PITCH + r4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              buf_put_pair(ur, pair_off[i] + 32 * g * SZ, (float)x[i], (float)y[i], tag);
+          }
+        }
+      }
+      load_rest(blk + 1);
     }
   }
 }
@@ -517,7 +520,7 @@ static hipError_t launch_forward(const DeltaParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<T, D, GRAD>), dim3(p.batch * p.blocks_max, p.heads), dim3(256), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((delta_chain_kernel<T, D, GRAD>), dim3(CS::NSL * p.batch * p.heads), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((delta_chain_kernel<T, D, GRAD>), dim3(CS::NSL * p.batch * p.heads), dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 
