@@ -355,6 +355,56 @@ ret_status_t retention_delta_step(const ret_delta_desc_t *desc, const void *q, c
                                   const float *log_decay, const float *beta, void *o, float *state,
                                   const int32_t *slots, int64_t num_slots, hipStream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Norms around a token mixer, over rows of `width` values. norm(x) is x /
+ * sqrt(mean(x^2) + eps), or with `center` (x - mean(x)) / sqrt(variance + eps)
+ * (biased). Rows in the descriptor's dtype, weights and their gradients fp32
+ * [width]; sums in fp32. With rows == 0 nothing but weight gradients (zeros)
+ * is written, and the row pointers may be NULL.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t rows;   /* >= 0, at most 2^31 - 1 (head norm: tokens * heads)        */
+  int32_t width;  /* 1 .. 16384                                                */
+  int32_t dtype;  /* ret_dtype_t                                               */
+  int32_t center; /* nonzero: subtract the mean                                */
+  float eps;      /* > 0                                                       */
+} ret_norm_desc_t;
+
+/* The norm on a mixer's output with its gate: out = norm(x) (.) weight (.)
+ * swish(gate), one group per head (a row is one head of one token). weight and
+ * gate may be NULL (ones). With centring and no weight it is the GroupNorm and
+ * swish gate that the retention calls apply themselves ("Summary"; "Key
+ * points", fourth item); without a gate and with weight d^(-1/2) it makes
+ * keys of unit length for the delta rule. The gradients are of
+ * sum(dout (.) out); dweight, dgate are non-NULL exactly when weight, gate
+ * are. The workspace (0 bytes without a weight) holds partial sums of dweight. */
+ret_status_t retention_head_norm_fwd(const ret_norm_desc_t *desc, const void *x, const float *weight,
+                                     const void *gate, void *out, hipStream_t stream);
+size_t retention_head_norm_bwd_workspace_bytes(const ret_norm_desc_t *desc);
+ret_status_t retention_head_norm_bwd(const ret_norm_desc_t *desc, const void *x, const float *weight,
+                                     const void *gate, const void *dout, void *dx, float *dweight, void *dgate,
+                                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* From one block to the next: the block's output y is normalised (when
+ * post_weight is given), scaled and added to the residual stream x, and the sum
+ * is normalised for the next block:
+ *     z = norm(y) (.) post_weight   (post_weight NULL: z = y)
+ *     residual = skip x + scale (.) z   (scale NULL: ones)
+ *     out = norm(residual) (.) weight
+ * residual == x exactly is allowed. The norm takes the unrounded residual. The
+ * gradients are of sum(dout (.) out) + sum(dresidual (.) residual) (dresidual
+ * NULL: zero); dpost_weight, dscale are non-NULL exactly when post_weight,
+ * scale are. The workspace holds partial sums of the weights' gradients. */
+ret_status_t retention_residual_norm_fwd(const ret_norm_desc_t *desc, float skip, const void *x, const void *y,
+                                         const float *weight, const float *post_weight, const float *scale, void *out,
+                                         void *residual, hipStream_t stream);
+size_t retention_residual_norm_bwd_workspace_bytes(const ret_norm_desc_t *desc);
+ret_status_t retention_residual_norm_bwd(const ret_norm_desc_t *desc, float skip, const void *x, const void *y,
+                                         const float *weight, const float *post_weight, const float *scale,
+                                         const void *dout, const void *dresidual, void *dx, void *dy, float *dweight,
+                                         float *dpost_weight, float *dscale, void *workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *retention_status_string(ret_status_t status);
 

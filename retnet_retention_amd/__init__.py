@@ -12,6 +12,8 @@ gfx950 behind a C ABI (include/retention.h), with a thin ctypes binding.
     delta_chunkwise_fwd   gated delta rule over whole (or packed) sequences, state in and out
     delta_chunkwise_bwd   its gradients
     delta_recurrent_step  its decode step, state (or a pool of states) in place
+    head_norm_fwd, head_norm_bwd          per-head norm with weight and swish gate, gradients
+    residual_norm_fwd, residual_norm_bwd  norm after a block, scaled residual, norm before the next
     check_chunkwise  raise if a chunkwise call's control word reports an error
 """
 
@@ -28,9 +30,13 @@ from .binding import (  # noqa: F401
     delta_chunkwise_bwd,
     delta_chunkwise_fwd,
     delta_recurrent_step,
+    head_norm_bwd,
+    head_norm_fwd,
     lib,
     parallel_bwd,
     parallel_fwd,
     recurrent_step,
+    residual_norm_bwd,
+    residual_norm_fwd,
     score_map,
 )

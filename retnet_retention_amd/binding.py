@@ -55,6 +55,12 @@ EXPORTS = (
     "retention_delta_bwd_workspace_bytes",
     "retention_delta_bwd",
     "retention_delta_step",
+    "retention_head_norm_fwd",
+    "retention_head_norm_bwd_workspace_bytes",
+    "retention_head_norm_bwd",
+    "retention_residual_norm_fwd",
+    "retention_residual_norm_bwd_workspace_bytes",
+    "retention_residual_norm_bwd",
     "retention_status_string",
     "retention_abi_version",
 )
@@ -89,6 +95,18 @@ class DeltaDesc(ctypes.Structure):
         ("dv", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
         ("scale", ctypes.c_float),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    """Mirror of ret_norm_desc_t."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("width", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("center", ctypes.c_int32),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -166,6 +184,19 @@ def lib():
         h.retention_delta_bwd.restype = st
         h.retention_delta_step.argtypes = [pdd] + [vp] * 8 + [i64, vp]
         h.retention_delta_step.restype = st
+        pnd, f32 = ctypes.POINTER(NormDesc), ctypes.c_float
+        h.retention_head_norm_fwd.argtypes = [pnd] + [vp] * 5
+        h.retention_head_norm_fwd.restype = st
+        h.retention_head_norm_bwd_workspace_bytes.argtypes = [pnd]
+        h.retention_head_norm_bwd_workspace_bytes.restype = sz
+        h.retention_head_norm_bwd.argtypes = [pnd] + [vp] * 8 + [sz, vp]
+        h.retention_head_norm_bwd.restype = st
+        h.retention_residual_norm_fwd.argtypes = [pnd, f32] + [vp] * 8
+        h.retention_residual_norm_fwd.restype = st
+        h.retention_residual_norm_bwd_workspace_bytes.argtypes = [pnd]
+        h.retention_residual_norm_bwd_workspace_bytes.restype = sz
+        h.retention_residual_norm_bwd.argtypes = [pnd, f32] + [vp] * 13 + [sz, vp]
+        h.retention_residual_norm_bwd.restype = st
         h.retention_status_string.argtypes = [st]
         h.retention_status_string.restype = ctypes.c_char_p
         h.retention_abi_version.argtypes = []
@@ -670,3 +701,99 @@ def delta_recurrent_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=No
         _check(lib().retention_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
                                           _ptr(out), _ptr(state), _ptr(slots), state.shape[0], _stream(q)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Norms around a token mixer
+# ---------------------------------------------------------------------------
+def _norm_inputs(x, rows, weights):
+    """Checks of a norm call's tensors: `rows` like x, `weights` fp32 [width]."""
+    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
+        raise ValueError("x must be a contiguous GPU tensor [..., width]")
+    for name, t in rows:
+        if t is None:
+            continue
+        _on_device(name, t, x)
+        if t.dtype != x.dtype or not t.is_contiguous() or t.shape != x.shape:
+            raise ValueError(f"{name} must be a contiguous tensor of x's shape and dtype")
+    for name, t in weights:
+        if t is None:
+            continue
+        _on_device(name, t, x)
+        if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (x.shape[-1],):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor [{x.shape[-1]}]")
+
+
+def _norm_desc(x, center, eps):
+    width = x.shape[-1]
+    return NormDesc(x.numel() // width if width else 0, width, _dtype_code(x), int(bool(center)), float(eps))
+
+
+def head_norm_fwd(x, weight=None, gate=None, *, center=False, eps=1e-5, out=None):
+    """Norm over the last dimension (a head of a token), times weight (fp32
+    [d]) and swish(gate) where given; center: subtract the mean (GroupNorm, one
+    group per head), else the root mean square alone."""
+    out = torch.empty_like(x) if out is None else out
+    _norm_inputs(x, (("gate", gate), ("out", out)), (("weight", weight),))
+    desc = _norm_desc(x, center, eps)
+    with _current(x):
+        _check(lib().retention_head_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(gate), _ptr(out),
+                                             _stream(x)))
+    return out
+
+
+def head_norm_bwd(x, dout, weight=None, gate=None, *, center=False, eps=1e-5, workspace=None):
+    """Gradients of sum(dout * head_norm_fwd(x, weight, gate, ...)): (dx,
+    dweight, dgate), None where there is no such input."""
+    _norm_inputs(x, (("dout", dout), ("gate", gate)), (("weight", weight),))
+    dx = torch.empty_like(x)
+    dweight = torch.empty_like(weight) if weight is not None else None
+    dgate = torch.empty_like(gate) if gate is not None else None
+    desc = _norm_desc(x, center, eps)
+    L = lib()
+    need = L.retention_head_norm_bwd_workspace_bytes(ctypes.byref(desc)) if weight is not None else 0
+    workspace, ws_bytes, _ = _workspace(workspace, need, x)
+    with _current(x):
+        _check(L.retention_head_norm_bwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(gate), _ptr(dout), _ptr(dx),
+                                         _ptr(dweight), _ptr(dgate), _ptr(workspace), ws_bytes, _stream(x)))
+    return dx, dweight, dgate
+
+
+def residual_norm_fwd(x, y, weight, *, post_weight=None, scale=None, skip=1.0, center=False, eps=1e-5, out=None,
+                      residual=None):
+    """The step from one block to the next over rows [..., width]: z = norm(y)
+    post_weight (or y), residual = skip x + scale z, out = norm(residual)
+    weight; returns (out, residual). residual may be x itself. post_weight,
+    scale, weight: fp32 [width]."""
+    out = torch.empty_like(x) if out is None else out
+    residual = torch.empty_like(x) if residual is None else residual
+    _norm_inputs(x, (("y", y), ("out", out), ("residual", residual)),
+                 (("weight", weight), ("post_weight", post_weight), ("scale", scale)))
+    desc = _norm_desc(x, center, eps)
+    with _current(x):
+        _check(lib().retention_residual_norm_fwd(ctypes.byref(desc), float(skip), _ptr(x), _ptr(y), _ptr(weight),
+                                                 _ptr(post_weight), _ptr(scale), _ptr(out), _ptr(residual), _stream(x)))
+    return out, residual
+
+
+def residual_norm_bwd(x, y, weight, dout, dresidual=None, *, post_weight=None, scale=None, skip=1.0, center=False,
+                      eps=1e-5, workspace=None):
+    """Gradients of sum(dout * out) (+ sum(dresidual * residual)) with out,
+    residual = residual_norm_fwd(x, y, weight, ...): (dx, dy, dweight,
+    dpost_weight, dscale), None where there is no such input. x and y are the
+    forward's inputs (x before a residual written over it)."""
+    _norm_inputs(x, (("y", y), ("dout", dout), ("dresidual", dresidual)),
+                 (("weight", weight), ("post_weight", post_weight), ("scale", scale)))
+    dx, dy, dweight = torch.empty_like(x), torch.empty_like(y), torch.empty_like(weight)
+    dpost = torch.empty_like(post_weight) if post_weight is not None else None
+    dscale = torch.empty_like(scale) if scale is not None else None
+    desc = _norm_desc(x, center, eps)
+    L = lib()
+    need = L.retention_residual_norm_bwd_workspace_bytes(ctypes.byref(desc))
+    workspace, ws_bytes, _ = _workspace(workspace, need, x)
+    with _current(x):
+        _check(L.retention_residual_norm_bwd(ctypes.byref(desc), float(skip), _ptr(x), _ptr(y), _ptr(weight),
+                                             _ptr(post_weight), _ptr(scale), _ptr(dout), _ptr(dresidual), _ptr(dx),
+                                             _ptr(dy), _ptr(dweight), _ptr(dpost), _ptr(dscale), _ptr(workspace),
+                                             ws_bytes, _stream(x)))
+    return dx, dy, dweight, dpost, dscale

@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libretention.so")
 
 SOURCES = ["api.hip", "rotary_table.hip", "recurrent_step.hip", "retention_fwd.hip", "backward.hip", "score_map.hip",
-           "delta_api.hip", "delta_fwd.hip", "delta_bwd.hip", "delta_step.hip"]
+           "delta_api.hip", "delta_fwd.hip", "delta_bwd.hip", "delta_step.hip", "norm_api.hip",
+           "norm_fwd.hip", "norm_bwd.hip"]
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}",

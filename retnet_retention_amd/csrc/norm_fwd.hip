@@ -1,0 +1,92 @@
+// Norms around a token mixer, forward. Per row x of `width` values, norm(x) =
+// (x - mean) / sqrt(mean square of it + eps), the mean only when centred:
+//     head norm:      out = norm(x) (weight) swish(gate)
+//     residual norm:  z = norm(y) post  (or y),  residual = skip x + scale z,
+//                     out = norm(residual) weight
+// Bound by memory: every tensor is read or written once, the row stays in
+// registers between its sums. The residual's norm takes the fp32 value, not
+// the rounded one that is stored.
+#include "norm_rows.hpp"
+
+namespace ret {
+
+template <typename T, typename R>
+__global__ __launch_bounds__(R::THREADS) void head_norm_fwd_kernel(NormParams p) {
+  __shared__ float sh[64];
+  int turn = 0;
+  const int l = threadIdx.x % R::LPR;
+  const int64_t row = (int64_t)blockIdx.x * R::RPB + threadIdx.x / R::LPR;
+  const bool keep = row < p.rows;
+  const int64_t at = row * p.width;
+  float x[R::E], y[R::E];
+  R::load(x, reinterpret_cast<const T*>(p.x) + at, p.width, l, keep);
+  if (p.gate) R::load(y, reinterpret_cast<const T*>(p.gate) + at, p.width, l, keep);
+  normalize<R>(x, p.width, p.center, p.eps, l, sh, turn);
+  if (p.gate) {
+#pragma unroll
+    for (int j = 0; j < R::E; ++j) x[j] *= swish(y[j]);
+  }
+  if (p.weight) {
+    R::load(y, p.weight, p.width, l);
+#pragma unroll
+    for (int j = 0; j < R::E; ++j) x[j] *= y[j];
+  }
+  if (keep) R::store(reinterpret_cast<T*>(p.out) + at, x, p.width, l);
+}
+
+template <typename T, typename R>
+__global__ __launch_bounds__(R::THREADS) void residual_norm_fwd_kernel(NormParams p) {
+  __shared__ float sh[64];
+  int turn = 0;
+  const int l = threadIdx.x % R::LPR;
+  const int64_t row = (int64_t)blockIdx.x * R::RPB + threadIdx.x / R::LPR;
+  const bool keep = row < p.rows;
+  const int64_t at = row * p.width;
+  float x[R::E], z[R::E], w[R::E];
+  R::load(x, reinterpret_cast<const T*>(p.x) + at, p.width, l, keep);
+  R::load(z, reinterpret_cast<const T*>(p.y) + at, p.width, l, keep);
+  R::load(w, p.weight, p.width, l);
+  float f[R::E];
+  if (p.scale) {
+    R::load(f, p.scale, p.width, l);
+  } else {
+#pragma unroll
+    for (int j = 0; j < R::E; ++j) f[j] = 1.f;
+  }
+  if (p.post) {
+    float post[R::E];
+    R::load(post, p.post, p.width, l);
+    normalize<R>(z, p.width, p.center, p.eps, l, sh, turn);
+#pragma unroll
+    for (int j = 0; j < R::E; ++j) z[j] *= post[j];
+  }
+#pragma unroll
+  for (int j = 0; j < R::E; ++j) x[j] = p.skip * x[j] + f[j] * z[j];
+  if (keep) R::store(reinterpret_cast<T*>(p.residual) + at, x, p.width, l);
+  normalize<R>(x, p.width, p.center, p.eps, l, sh, turn);
+#pragma unroll
+  for (int j = 0; j < R::E; ++j) x[j] *= w[j];
+  if (keep) R::store(reinterpret_cast<T*>(p.out) + at, x, p.width, l);
+}
+
+template <typename T>
+static hipError_t launch_fwd(const NormParams& p, bool residual, hipStream_t stream) {
+  return with_rows<T>(p.width, p.width % 8 == 0, [&](auto r) {
+    using R = decltype(r);
+    const dim3 grid((unsigned)((p.rows + R::RPB - 1) / R::RPB));
+    if (residual)
+      hipLaunchKernelGGL((residual_norm_fwd_kernel<T, R>), grid, dim3(R::THREADS), 0, stream, p);
+    else
+      hipLaunchKernelGGL((head_norm_fwd_kernel<T, R>), grid, dim3(R::THREADS), 0, stream, p);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_head_norm_fwd(const NormParams& p, int dtype, hipStream_t stream) {
+  return dtype == 1 ? launch_fwd<bf16>(p, false, stream) : launch_fwd<float>(p, false, stream);
+}
+hipError_t launch_residual_norm_fwd(const NormParams& p, int dtype, hipStream_t stream) {
+  return dtype == 1 ? launch_fwd<bf16>(p, true, stream) : launch_fwd<float>(p, true, stream);
+}
+
+}  // namespace ret

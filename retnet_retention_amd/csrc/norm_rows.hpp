@@ -1,0 +1,147 @@
+// Rows of a norm in registers: how they are divided over lanes, their sums,
+// the norm and its gradient.
+#pragma once
+
+#include "common.hpp"
+#include "norms.hpp"
+
+namespace ret {
+
+// LPR lanes hold a row, 8 NV elements each. VEC: 16-byte accesses, lane l the
+// elements 8 (v LPR + l) .. + 7; else single elements, j LPR + l (widths that
+// are no multiple of 8 leave rows unaligned). A workgroup of 256 lanes (or LPR)
+// holds RPB rows.
+template <typename T, int LPR_, int NV, bool VEC>
+struct NormRow {
+  static constexpr int LPR = LPR_, E = 8 * NV;
+  static constexpr int THREADS = LPR > 256 ? LPR : 256;
+  static constexpr int RPB = THREADS / LPR;
+
+  template <typename U>
+  __device__ static __forceinline__ void load(float* x, const U* row, int width, int l, bool keep = true) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = 8 * (v * LPR + l);
+        F8 y = {};
+        if (keep && at < width) y = load8(row + at);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[8 * v + e] = y.x[e];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = keep && j * LPR + l < width ? (float)row[j * LPR + l] : 0.f;
+    }
+  }
+  template <typename U>
+  __device__ static __forceinline__ void store(U* row, const float* x, int width, int l) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = 8 * (v * LPR + l);
+        F8 y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y.x[e] = x[8 * v + e];
+        if (at < width) store8(row + at, y);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (j * LPR + l < width) row[j * LPR + l] = (U)x[j];
+    }
+  }
+  // whether element j of the lane exists
+  __device__ static __forceinline__ bool inside(int j, int width, int l) {
+    return (VEC ? 8 * ((j / 8) * LPR + l) : j * LPR + l) < width;
+  }
+};
+
+// Sums over a row's lanes, N at a time. Rows of more than a wave go through
+// LDS with one barrier a sum: `turn` alternates between two halves of `sh`, so
+// a half is written again only after everybody has passed the barrier that
+// follows its reads. Every lane of the workgroup calls it.
+template <int LPR, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], float* sh, int& turn) {
+  if constexpr (LPR <= 64) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = sum_lanes<LPR>(s[i]);
+  } else {
+    constexpr int WPR = LPR / 64;
+    const int wave = threadIdx.x >> 6;
+    float* at = sh + turn * 32;
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = sum64(s[i]);
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[wave * N + i] = s[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) s[i] += at[(wave / WPR * WPR + w) * N + i];
+    }
+  }
+}
+
+// x becomes (x - mean) / deviation (mean 0 unless `center`); returns the
+// inverse deviation. The variance is summed from the centred values.
+template <typename R>
+__device__ __forceinline__ float normalize(float* x, int width, int center, float eps, int l, float* sh, int& turn) {
+  const float inv = 1.f / width;
+  if (center) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < R::E; ++j) s[0] += x[j];
+    row_sums<R::LPR>(s, sh, turn);
+#pragma unroll
+    for (int j = 0; j < R::E; ++j) x[j] = R::inside(j, width, l) ? x[j] - s[0] * inv : 0.f;
+  }
+  float s[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < R::E; ++j) s[0] += x[j] * x[j];
+  row_sums<R::LPR>(s, sh, turn);
+  const float rstd = rsqrtf(s[0] * inv + eps);
+#pragma unroll
+  for (int j = 0; j < R::E; ++j) x[j] *= rstd;
+  return rstd;
+}
+
+// g, the gradient of the normalised row n, becomes the row's own.
+template <typename R>
+__device__ __forceinline__ void normalize_grad(float* g, const float* n, float rstd, int width, int center, float* sh,
+                                               int& turn) {
+  const float inv = 1.f / width;
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < R::E; ++j) {
+    s[0] += g[j] * n[j];
+    s[1] += g[j];
+  }
+  row_sums<R::LPR>(s, sh, turn);
+  const float a = s[0] * inv, b = center ? s[1] * inv : 0.f;
+#pragma unroll
+  for (int j = 0; j < R::E; ++j) g[j] = rstd * (g[j] - b - n[j] * a);
+}
+
+// f(NormRow of the width's division) for rows of `width` elements
+template <typename T, typename F>
+hipError_t with_rows(int width, bool vec, F&& f) {
+#define RET_NORM_CASE(LIMIT, LPR, NV) \
+  if (width <= LIMIT) return vec ? f(NormRow<T, LPR, NV, true>{}) : f(NormRow<T, LPR, NV, false>{});
+  RET_NORM_CASE(64, 8, 1)
+  RET_NORM_CASE(128, 16, 1)
+  RET_NORM_CASE(256, 32, 1)
+  RET_NORM_CASE(512, 64, 1)
+  RET_NORM_CASE(1024, 128, 1)
+  RET_NORM_CASE(2048, 256, 1)
+  RET_NORM_CASE(4096, 512, 1)
+  RET_NORM_CASE(8192, 1024, 1)
+  RET_NORM_CASE(kMaxNormWidth, 1024, 2)
+#undef RET_NORM_CASE
+  return hipErrorInvalidValue;
+}
+
+}  // namespace ret
