@@ -21,9 +21,12 @@ struct DeltaParams {
   int batch, seqlen, k_heads, heads, total, blocks_max;
   float scale;
   int* ctrl;
-  // per (block, head): T = (I + A)^-1 and P (row-major 64 x 64, in planes), in
-  // the backward also their transposes; the decay vectors
-  void *t, *p, *tt, *pt;
+  // per (block, head): T = (I + A)^-1 diag(beta) and M = P T in planes, in the backward
+  // also the transposes of T and P; the decay vectors
+  void *t, *m, *tt, *pt;
+  // per (block, key head): keys by rows and by columns, queries by rows, in the
+  // backward also by columns, in the order the lanes take them
+  void *kf, *kc, *qf, *qc;
   float* vec;  // [4][64]: exp(G_r), exp(G_last - G_r), beta_r, unused
   // forward
   void* o;
@@ -38,7 +41,7 @@ struct DeltaParams {
   void *snap, *dsnap;  // per (block, head): the state at the block's start and the state's gradient at its end, [dv][dk]
   float* anchor;       // per (group, head): the fp32 state at the group's end
   void* u;             // the written values V', [tokens][heads][d] in planes
-  float *odo, *vdv, *xu;  // per (block, head, slice): row sums o.dO, v.dv, dX.V'
+  float *odo, *vdv, *udv;  // per (block, head, slice): row sums o.dO, v.dv, V'.dv
   float* adot;            // per (group, head, slice): <state, its gradient> at the group's end
 };
 

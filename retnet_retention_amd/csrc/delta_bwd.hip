@@ -1,7 +1,7 @@
 // Gradients of the gated delta rule's chunkwise form. The forward's walk is
 // run again (delta_fwd.hip, which keeps V', the state at each block's start and
 // the row sums o . dO); then, with dS+ the gradient of a block's final state,
-//     dV' = e^(G_last - G) K dS+ + P^T dO,   dX = T^T dV',   dv = beta dX,
+//     dV' = e^(G_last - G) K dS+ + P^T dO,   dv = T^T dV'  (X = V - e^G K S),
 //     dS = e^(G_last) dS+ + Q^T (scale e^G dO) - K^T (e^G dv)
 // goes through the blocks from the last to the first (delta_reverse_kernel),
 // and per block, with all of the above at hand (delta_qk_grad_kernel),
@@ -14,7 +14,8 @@
 //     d log_decay_t = sum over t' >= t of d_t' + <S_end, dS_end>,
 // summed inside groups of kDeltaGroup blocks from the product of the state and
 // its gradient at the group's end (a sum over a whole sequence would cancel);
-//     d beta_t = dX_t . V'_t / beta_t   (V' = beta times the prediction error).
+//     d beta_t = dv_t . V'_t / beta_t^2   (V' is beta times the prediction error,
+//     dv beta times what the write of it gains).
 #include "delta_common.hpp"
 
 namespace ret {
@@ -23,20 +24,16 @@ hipError_t launch_delta_forward(const DeltaParams& p, int d, int dtype, bool gra
 
 // The gradient of the state, from a sequence's last block to its first: the
 // same division of work and the same three exchanges as delta_chain_kernel.
-// The second four waves form P^T dO, put Q and scale e^G dO where the state
-// waves read them, and take the row sums.
+// The second four waves form P^T dO, put scale e^G dO where the state waves
+// read it, and take the row sums.
 template <typename T, int D>
 __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
-  using KT = KeyTile<T, CS::KR>;
   constexpr int NP = Planes<T>::N, SZ = sizeof(T);
   constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
-  // where LDS has no room for a second tile, Q's products follow K's in the same one
-  constexpr bool kTwoTiles = SZ == 2 || D == 128;
+  constexpr bool kAhead = SZ == 2;  // fp32 keys do not fit the registers a block ahead
   T* const tag = nullptr;
-  __shared__ __attribute__((aligned(16))) char kt[4 * KT::BYTES], qt[kTwoTiles ? 4 * KT::BYTES : 16];
   __shared__ __attribute__((aligned(16))) f32x4 part[4 * 512];
-  // each quarter's P^T dO on its way to the state wave, then its dX on the way back
   __shared__ __attribute__((aligned(16))) f32x4 quarter[16 * CT * 16];
   __shared__ __attribute__((aligned(16))) T od[OPLANE], oq[CS::OPND], ox[CS::OPND], ow[CS::OPND];
 
@@ -50,12 +47,13 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
   int len, base;
   seq_span(p, b, tok0, len, base);
   const int nblk = (len + kB - 1) / kB;
-  const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
-  const uint32_t qrow = (uint32_t)qs * SZ, vrow = (uint32_t)vs * SZ;
+  const int64_t vs = (int64_t)p.heads * D;
+  const uint32_t vrow = (uint32_t)vs * SZ;
   // descriptors of block blk (no rows: nothing is read)
   auto rows_of = [&](int blk) { return blk >= 0 ? min(kB, len - blk * kB) : 0; };
-  auto key_rsrc = [&](const void* x, int blk) {
-    return scalar_rsrc(reinterpret_cast<const T*>(x) + (tok0 + (int64_t)blk * kB) * qs + hk * D, rows_of(blk) * qrow);
+  auto key_rsrc = [&](const void* x, int blk) {  // keys or queries in the lanes' order
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + ((int64_t)(base + blk) * p.k_heads + hk) * (kB * D),
+                       blk >= 0 ? kB * D * SZ : 0);
   };
   auto value_rsrc = [&](const void* x, int blk) {
     return scalar_rsrc(reinterpret_cast<const T*>(x) + (tok0 + (int64_t)blk * kB) * vs + h * D, rows_of(blk) * vrow);
@@ -65,34 +63,33 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
     return scalar_rsrc(reinterpret_cast<const T*>(x) + slot_of(blk) * (NP * kB * kB), blk >= 0 ? NP * kB * kB * SZ : 0);
   };
   auto vec_rsrc = [&](int blk) { return scalar_rsrc(p.vec + slot_of(blk) * (4 * kB), blk >= 0 ? 4 * kB * 4 : 0); };
-  const uint32_t mat_off = ((16 * w + c) * kB + 8 * g16) * SZ;
+  const uint32_t lane_off = 8 * lane * SZ;
   uint32_t pair_off[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) pair_off[i] = (r4 + i) * vrow + (slice * CS::SL + 2 * c) * SZ;
   const int krow = CS::KR * (w % RG), cg = w / RG, vcol = slice * CS::SL + 32 * cg + n;
-  const uint32_t key_off[2] = {n * qrow + (krow + 8 * h2) * SZ, (32 + n) * qrow + (krow + 8 * h2) * SZ};
-  // rows 16 w .. of an upper triangular matrix
-  auto load_upper = [&](frag_t<T>(&f)[NP][2], const void* x, int blk) {
+  auto load_mat = [&](frag_t<T>(&f)[NP][2], const void* x, int blk) {
     const auto rs = mat_rsrc(x, blk);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (ks < (w >> 1)) continue;
+    for (int pl = 0; pl < NP; ++pl)
 #pragma unroll
-      for (int pl = 0; pl < NP; ++pl) f[pl][ks] = buf_frag(rs, mat_off + (pl * kB * kB + 32 * ks) * SZ, tag);
-    }
+      for (int ks = 0; ks < 2; ++ks)
+        if (ks >= (w >> 1)) f[pl][ks] = buf_frag(rs, lane_off + mat_frag(pl, w, ks) * SZ, tag);  // upper triangular
   };
-  auto load_keys = [&](frag_t<T>(&f)[2][CS::KS], const void* x, int blk) {
+  auto load_keys = [&](frag_t<T>(&f)[2][CS::KS], int blk) {
+    const auto rs = key_rsrc(p.kf, blk);
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int ks = 0; ks < CS::KS; ++ks)
+        f[rt][ks] = buf_frag(rs, lane_off + key_frag(krow / 16 + ks, rt) * SZ, tag);
+  };
+  auto load_columns = [&](frag_t<T>(&f)[TPW][4], const void* x, int blk) {
     const auto rs = key_rsrc(x, blk);
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
+    for (int t = 0; t < TPW; ++t)
 #pragma unroll
-      for (int ks = 0; ks < CS::KS; ++ks) f[rt][ks] = buf_frag(rs, key_off[rt] + 16 * ks * SZ, tag);
-  };
-  auto put_keys = [&](char* tile, const frag_t<T>(&f)[2][CS::KS]) {
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-      for (int ks = 0; ks < CS::KS; ++ks) KT::put(tile, 32 * rt + n, 16 * ks + 8 * h2, f[rt][ks]);
+      for (int ks = 0; ks < 4; ++ks) f[t][ks] = buf_frag(rs, lane_off + column_frag(krow / 32 + t, ks) * SZ, tag);
   };
   auto load_pairs = [&](PairOf<T>(&x)[CG][4], const void* from, int blk) {
     const auto rs = value_rsrc(from, blk);
@@ -101,6 +98,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
       for (int g = 0; g < CG; ++g) x[g][i] = buf_pair(rs, pair_off[i] + 32 * g * SZ, tag);
   };
+  // each quarter's P^T dO on its way to the state wave, then its dv back
   f32x4* my_quarter = quarter + (4 * w + g16) * (CT * 16) + c;
 
   if (wave < 4) {
@@ -114,25 +112,26 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[t][i] = si[(krow + 32 * t + state_row(i, h2)) * D + vcol];
     }
-    char* my_kt = kt + w * KT::BYTES;
-    const char* my_qt = kTwoTiles ? qt + w * KT::BYTES : my_kt;
-    frag_t<T> kf[2][CS::KS], tf[NP][2];
-    f32x4 eg, el, beta;
+    frag_t<T> kf[2][CS::KS], kc[TPW][4], qc[TPW][4], tf[NP][2];
+#pragma unroll
+    for (int pl = 0; pl < NP; ++pl) tf[pl][0] = zero_frag<T>();
+    f32x4 eg, el;
     float last;
     auto load_rest = [&](int blk) {
-      load_upper(tf, p.tt, blk);
+      load_mat(tf, p.tt, blk);
       const auto er = vec_rsrc(blk);
       eg = buf_f4(er, r4 * 4);
       el = buf_f4(er, (kB + r4) * 4);
-      beta = buf_f4(er, (2 * kB + r4) * 4);
       last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, (kB - 1) * 4, 0, 0));
     };
-    load_keys(kf, p.k, nblk - 1);
     load_rest(nblk - 1);
+    if constexpr (kAhead) {
+      load_keys(kf, nblk - 1);
+      load_columns(kc, p.kc, nblk - 1);
+    }
     lds_barrier();
 
     for (int blk = nblk - 1; blk >= 0; --blk) {
-      const int rows = min(kB, len - blk * kB);
       const int64_t slot = slot_of(blk);
       const bool group_end = (blk + 1) % kDeltaGroup == 0 || blk == nblk - 1;
       if (group_end && (blk != nblk - 1 || p.d_state_out)) {
@@ -152,6 +151,10 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         dot = sum64(dot);
         if (lane == 0) p.adot[at] = dot;
       }
+      if constexpr (kAhead)
+        load_columns(qc, p.qc, blk);
+      else
+        load_keys(kf, blk);
       f32x16 ksum[2] = {zero16(), zero16()};
 #pragma unroll
       for (int t = 0; t < TPW; ++t)
@@ -167,68 +170,57 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
           *reinterpret_cast<frag_t<T>*>(sn) = f.f[0];
         });
       put_partial(part, w, ksum, lane);
-      put_keys(my_kt, kf);
-      load_keys(kf, p.k, blk - 1);
       lds_barrier();
 
-      // dV' of the quarter
+      // dV' of the quarter (zero behind the sequence's end: K and dO are)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        f32x4 x = get_partial<RG>(part, ct, 4 * w + g16, c) * el + my_quarter[16 * ct];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = r4 + i < rows ? x[i] : 0.f;
-        put_opnd<PITCH, OPLANE>(ox, 16 * ct + c, r4, x);
-      }
+      for (int ct = 0; ct < CT; ++ct)
+        put_opnd<PITCH, OPLANE>(ox, row_of(ct, c), r4,
+                                get_partial<RG>(part, ct, 4 * w + g16, c) * el + my_quarter[16 * ct]);
+      if constexpr (kAhead) load_keys(kf, blk - 1);
       lds_barrier();
 
-      // dX = T^T dV'; the state takes -e^G beta dX
-      const f32x4 scale = eg * beta;
+      // dv = T^T dV'; the state takes -e^G dv
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        f32x4 dx = zero4();
+        f32x4 dv[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          if (ks < (w >> 1)) continue;
           frag_t<T> a[NP], x[NP];
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl) {
             a[pl] = tf[pl][ks];
-            x[pl] = lds_row8(ox + pl * OPLANE + (16 * ct + c) * PITCH + 32 * ks + 8 * g16);
+            x[pl] = lds_row8(ox + pl * OPLANE + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
           }
-          dx = mma_split2(a, x, dx, tag);
+          dv[ks] = mma_split2(a, x, zero4(), tag);
         }
-        put_opnd<PITCH, OPLANE>(ow, 16 * ct + c, 16 * w + quad_place(g16), -scale * dx);
-        my_quarter[16 * ct] = dx;
+        dv[0] += dv[1];
+        put_opnd<PITCH, OPLANE>(ow, row_of(ct, c), 16 * w + quad_place(g16), -eg * dv[0]);
+        my_quarter[16 * ct] = dv[0];
       }
       const float decay = last;
-      load_rest(blk - 1);
       lds_barrier();
-
-      auto add = [&](const char* tile, const T* opnd) {
+      auto add = [&](const frag_t<T>(&f)[TPW][4], const T* opnd) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          frag_t<T> f[NP];
+          frag_t<T> x[NP];
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl)
-            f[pl] = lds_row8(opnd + pl * OPLANE + (32 * cg + col_place(n)) * PITCH + 16 * ks + 8 * h2);
+            x[pl] = lds_row8(opnd + pl * OPLANE + (32 * cg + col_place(n)) * PITCH + 16 * ks + 8 * h2);
 #pragma unroll
-          for (int t = 0; t < TPW; ++t) {
-            const frag_t<T> a = KT::col(tile, 16 * ks, 32 * t, lane);
+          for (int t = 0; t < TPW; ++t)
 #pragma unroll
-            for (int pl = 0; pl < NP; ++pl) s[t] = mma32(a, f[pl], s[t]);
-          }
+            for (int pl = 0; pl < NP; ++pl) s[t] = mma32(f[t][ks], x[pl], s[t]);
         }
       };
 #pragma unroll
       for (int t = 0; t < TPW; ++t) s[t] *= decay;
-      add(my_kt, ow);
-      if constexpr (!kTwoTiles) {
-        frag_t<T> qf[2][CS::KS];
-        load_keys(qf, p.q, blk);
-        put_keys(my_kt, qf);
-        __builtin_amdgcn_wave_barrier();
-      }
-      add(my_qt, oq);
+      if constexpr (!kAhead) load_columns(qc, p.qc, blk);
+      add(qc, oq);
+      if constexpr (!kAhead) load_columns(kc, p.kc, blk);
+      add(kc, ow);
+      if constexpr (kAhead) load_columns(kc, p.kc, blk - 1);
+      load_rest(blk - 1);
     }
     if (p.d_state_in) {
       float* so = p.d_state_in + (int64_t)bh * D * D;
@@ -238,29 +230,28 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
     }
   } else {
-    frag_t<T> qf[2][CS::KS], pf[NP][2];
+    frag_t<T> pf[NP][2];
+#pragma unroll
+    for (int pl = 0; pl < NP; ++pl) pf[pl][0] = zero_frag<T>();
     PairOf<T> dout[CG][4], dnext[CG][4], v[CG][4], u[NP][CG][4];
-    f32x4 eg, beta;
+    f32x4 eg;
     auto put_dout = [&](const PairOf<T>(&x)[CG][4]) {  // exact in T
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         vec4_t<T> y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = (T)x[ct >> 1][i].get(ct & 1);
-        *reinterpret_cast<vec4_t<T>*>(od + (16 * ct + c) * PITCH + r4) = y;
+        *reinterpret_cast<vec4_t<T>*>(od + row_of(ct, c) * PITCH + r4) = y;
       }
     };
     auto load_values = [&](int blk) {
       load_pairs(v, p.v, blk);
 #pragma unroll
       for (int pl = 0; pl < NP; ++pl) load_pairs(u[pl], reinterpret_cast<const T*>(p.u) + pl * (int64_t)p.total * vs, blk);
-      const auto er = vec_rsrc(blk);
-      eg = buf_f4(er, r4 * 4);
-      beta = buf_f4(er, (2 * kB + r4) * 4);
     };
     load_pairs(dout, p.dout, nblk - 1);
-    load_upper(pf, p.pt, nblk - 1);
-    if constexpr (kTwoTiles) load_keys(qf, p.q, nblk - 1);
+    load_mat(pf, p.pt, nblk - 1);
+    eg = buf_f4(vec_rsrc(nblk - 1), r4 * 4);
     load_values(nblk - 1);
     load_pairs(dnext, p.dout, nblk - 2);
     put_dout(dout);
@@ -271,25 +262,21 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         f32x4 x = zero4();
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          if (ks < (w >> 1)) continue;
-          const frag_t<T> d = lds_row8(od + (16 * ct + c) * PITCH + 32 * ks + 8 * g16);
+          const frag_t<T> d = lds_row8(od + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl) x = mma(pf[pl][ks], d, x);
         }
         my_quarter[16 * ct] = x;
       }
-      load_upper(pf, p.pt, blk - 1);
+      load_mat(pf, p.pt, blk - 1);
       lds_barrier();
-      if constexpr (kTwoTiles) {
-        put_keys(qt + w * KT::BYTES, qf);
-        load_keys(qf, p.q, blk - 1);
-      }
+      // scale e^G dO, for the state waves after the third barrier
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         f32x4 x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = p.scale * eg[i] * dout[ct >> 1][i].get(ct & 1);
-        put_opnd<PITCH, OPLANE>(oq, 16 * ct + c, 16 * w + quad_place(g16), x);
+        put_opnd<PITCH, OPLANE>(oq, row_of(ct, c), 16 * w + quad_place(g16), x);
       }
       put_dout(dnext);
 #pragma unroll
@@ -297,25 +284,25 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) dout[g][i] = dnext[g][i];
       load_pairs(dnext, p.dout, blk - 2);
+      eg = buf_f4(vec_rsrc(blk - 1), r4 * 4);
       lds_barrier();
       lds_barrier();
       // dv and the row sums of the quarter
       const auto rs = value_rsrc(p.dv, blk);
-      f32x4 vdv = zero4(), xu = zero4();
+      f32x4 vdv = zero4(), uv = zero4();
 #pragma unroll
       for (int g = 0; g < CG; ++g) {
         f32x4 dv[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const f32x4 dx = my_quarter[16 * (2 * g + e)];
-          dv[e] = beta * dx;
+          dv[e] = my_quarter[16 * (2 * g + e)];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float y = 0.f;
 #pragma unroll
             for (int pl = 0; pl < NP; ++pl) y += u[pl][g][i].get(e);
             vdv[i] += dv[e][i] * v[g][i].get(e);
-            xu[i] += dx[i] * y;
+            uv[i] += dv[e][i] * y;
           }
         }
 #pragma unroll
@@ -324,11 +311,11 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         vdv[i] = sum16(vdv[i]);
-        xu[i] = sum16(xu[i]);
+        uv[i] = sum16(uv[i]);
       }
       if (c == 0) {
         *reinterpret_cast<f32x4*>(p.vdv + (slot_of(blk) * CS::NSL + slice) * kB + r4) = vdv;
-        *reinterpret_cast<f32x4*>(p.xu + (slot_of(blk) * CS::NSL + slice) * kB + r4) = xu;
+        *reinterpret_cast<f32x4*>(p.udv + (slot_of(blk) * CS::NSL + slice) * kB + r4) = uv;
       }
       load_values(blk - 1);
     }
@@ -553,7 +540,7 @@ __global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int 
     for (int s = 0; s < slices; ++s) {
       const int64_t at = (slot * slices + s) * kB + lane;
       d += p.odo[at] - p.vdv[at];
-      x += p.xu[at];
+      x += p.udv[at];
     }
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) {
@@ -568,7 +555,8 @@ __global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int 
       // with no state before it the first token's decay acts on nothing: the
       // sum over the whole sequence is zero but for its rounding
       p.d_log_decay[at] = r == 0 && !p.state_in ? 0.f : d;
-      p.d_beta[at] = x / p.vec[slot * (4 * kB) + 2 * kB + lane];
+      const float beta = p.vec[slot * (4 * kB) + 2 * kB + lane];
+      p.d_beta[at] = x / beta / beta;
     }
   }
 }

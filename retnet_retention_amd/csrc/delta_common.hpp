@@ -56,6 +56,23 @@ __device__ __forceinline__ C mma_split2(const A* a, const B* b, C c, float*) {
   return mma(a[0], b[0], c);
 }
 
+// ---------------------------------------------------------------------------
+// Operands laid out by delta_prep_kernel in the order the lanes take them, 64 x
+// 8 elements a fragment: a wave's load of one is 1 or 2 KiB in a row (rows of
+// the tensors are far apart, and a lane's 8 elements of its own row cost the
+// caches a request each).
+//   keys of a block and key head: [D / 16][2][64 lanes]   (32x32 row fragments)
+//   the same by columns (and of queries, backward): [D / 32][4][64 lanes]
+//   queries:                      [4][D / 32][64 lanes]   (16x16 row fragments)
+//   64 x 64 matrices, per plane:  [4][2][64 lanes]        (16x16 row fragments)
+// ---------------------------------------------------------------------------
+constexpr int kFrag = 64 * 8;
+__device__ __forceinline__ constexpr int key_frag(int ks, int rt) { return (2 * ks + rt) * kFrag; }
+__device__ __forceinline__ constexpr int column_frag(int tile, int ks) { return (4 * tile + ks) * kFrag; }
+template <int D>
+__device__ __forceinline__ constexpr int query_frag(int rb, int ks) { return (rb * (D / 32) + ks) * kFrag; }
+__device__ __forceinline__ constexpr int mat_frag(int plane, int rb, int ks) { return ((plane * 4 + rb) * 2 + ks) * kFrag; }
+
 // 8 consecutive elements of global memory as a fragment, zero unless `keep`
 template <typename T>
 __device__ __forceinline__ frag_t<T> global_row8(const T* p, bool keep) {
@@ -112,60 +129,43 @@ struct ChainShape {
   static constexpr int SPLANE = SL * SPITCH;
 };
 
-// A wave's 64 tokens x KR key columns in LDS, written by rows (8 elements of a
-// token's row) and read by columns. 16-byte chunks of a bf16 row are swapped
-// within the row by its number, so that 16 rows' writes of one chunk and the
-// transposed reads of 4 rows x 4 chunks meet distinct banks.
-template <typename T, int KR> struct KeyTile;
-template <int KR> struct KeyTile<bf16, KR> {
-  static constexpr int BYTES = kB * KR * 2;
-  __device__ static __forceinline__ int chunk(int r, int ch) {
-    const int f = KR == 64 ? ((((r >> 1) & 1) << 2) | ((r >> 2) & 3)) : ((r >> 2) & 3);
-    return r * (KR * 2) + ((ch ^ f) << 4);
-  }
-  __device__ static __forceinline__ void put(char* t, int r, int col, const bf16x8& x) {
-    *reinterpret_cast<bf16x8*>(t + chunk(r, col >> 3)) = x;
-  }
-  // Column fragment of tokens k0 .. k0 + 15 (k0 a multiple of 16, lane half h
-  // the tokens k0 + 4h .. and k0 + 8 + 4h ..) and of the 32 key columns from n0
-  // in the accumulator's order: inside 16 columns the groups of four come as
-  // 0, 2, 1, 3.
-  __device__ static __forceinline__ bf16x8 col(const char* t, int k0, int n0, int lane) {
-    const int grp = lane >> 4, m = lane & 15, h = grp >> 1;
-    const int q = m & 3, cg = ((q & 1) << 1) | (q >> 1);
-    const int c = n0 + 16 * (grp & 1) + 4 * cg, r = k0 + 4 * h + (m >> 2);
-    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(t + chunk(r, c >> 3) + 2 * (c & 7)));
-    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(t + chunk(r + 8, c >> 3) + 2 * (c & 7)));
-    typedef short i16x8 __attribute__((ext_vector_type(8)));
-    const i16x8 w = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    return __builtin_bit_cast(bf16x8, w);
-  }
-};
-template <int KR> struct KeyTile<float, KR> {
-  static constexpr int BYTES = kB * KR * 4;
-  __device__ static __forceinline__ void put(char* t, int r, int col, const f32x8& x) {
-    f32x4* p = reinterpret_cast<f32x4*>(t + (r * KR + col) * 4);
-    p[0] = f32x4{x[0], x[1], x[2], x[3]};
-    p[1] = f32x4{x[4], x[5], x[6], x[7]};
-  }
-  __device__ static __forceinline__ f32x8 col(const char* t, int k0, int n0, int lane) {
-    const int n = lane & 31, h = lane >> 5;
-    const int q = (n >> 2) & 3, cg = ((q & 1) << 1) | (q >> 1);
-    const float* p = reinterpret_cast<const float*>(t) + (k0 + 4 * h) * KR + n0 + (n & 16) + 4 * cg + (n & 3);
-    f32x8 f;
+// Column fragment of a row-major LDS array (`pitch` elements a row) as the state
+// products take it: tokens k0 .. k0 + 15 (lane half h the tokens k0 + 4h .. + 3
+// and k0 + 8 + 4h .. + 3) of the 32 key columns from n0 in the accumulator's
+// order: inside 16 columns the groups of four come as 0, 2, 1, 3.
+__device__ __forceinline__ bf16x8 state_col8(const bf16* m, int pitch, int k0, int n0, int lane) {
+  const int grp = lane >> 4, t = lane & 15, h = grp >> 1;
+  const int q = t & 3, cg = ((q & 1) << 1) | (q >> 1);
+  const bf16* p = m + (k0 + 4 * h + (t >> 2)) * pitch + n0 + 16 * (grp & 1) + 4 * cg;
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * pitch));
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x8 w = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ f32x8 state_col8(const float* m, int pitch, int k0, int n0, int lane) {
+  const int n = lane & 31, h = lane >> 5;
+  const int q = (n >> 2) & 3, cg = ((q & 1) << 1) | (q >> 1);
+  const float* p = m + (k0 + 4 * h) * pitch + n0 + (n & 16) + 4 * cg + (n & 3);
+  f32x8 f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = p[j * KR];
-      f[4 + j] = p[(8 + j) * KR];
-    }
-    return f;
+  for (int j = 0; j < 4; ++j) {
+    f[j] = p[j * pitch];
+    f[4 + j] = p[(8 + j) * pitch];
   }
-};
+  return f;
+}
 
 // A value column of a workgroup and its place: the quarter-row products take
 // column 32 (ct / 2) + 2 c + ct % 2 as column c of tile ct, so that a lane
-// holds neighbouring columns; operand copies keep it in row 16 ct + c.
-__device__ __forceinline__ constexpr int col_place(int n) { return ((n & 1) << 4) | (n >> 1); }  // within 32 columns
+// holds neighbouring columns. Copies in LDS keep it in row row_of(ct, c): odd
+// tiles in another order, so that 16 columns in a row meet distinct banks
+// whichever way they are numbered.
+__device__ __forceinline__ constexpr int row_of(int ct, int c) { return 16 * ct + (c ^ ((ct & 1) << 3)); }
+__device__ __forceinline__ constexpr int col_place(int n) { return row_of(n & 1, n >> 1); }  // within 32 columns
+__device__ __forceinline__ constexpr int col_at(int place) {                                // its inverse
+  return 2 * ((place & 15) ^ ((place >> 4) << 3)) + (place >> 4);
+}
 
 // Partial products of the waves, [wave][quad of rows][place of column] of 4
 // rows each.
@@ -180,9 +180,10 @@ __device__ __forceinline__ void put_partial(f32x4* buf, int wave, const f32x16* 
 }
 template <int RG>
 __device__ __forceinline__ f32x4 get_partial(const f32x4* buf, int ct, int quad, int c) {
-  f32x4 s = buf[((ct >> 1) * RG * 16 + quad) * 32 + (ct & 1) * 16 + c];
+  const f32x4* at = buf + ((ct >> 1) * RG * 16 + quad) * 32 + row_of(ct & 1, c);
+  f32x4 s = *at;
 #pragma unroll
-  for (int r = 1; r < RG; ++r) s += buf[(((ct >> 1) * RG + r) * 16 + quad) * 32 + (ct & 1) * 16 + c];
+  for (int r = 1; r < RG; ++r) s += at[r * 512];
   return s;
 }
 
