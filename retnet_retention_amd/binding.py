@@ -5,10 +5,13 @@ current HIP stream); every step of the computation runs in the library's
 kernels. It raises when the library has not been built: there is no fallback.
 """
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
+from torch._C import _cuda_getCurrentRawStream
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libretention.so")
 
@@ -231,13 +234,13 @@ def _dtype_code(t):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _on_device(name, t, like):
     """t (may be None) must be a GPU tensor on the device of `like`: its
     pointer goes to the kernels as a device address."""
-    if t is not None and (not t.is_cuda or t.device != like.device):
+    if t is not None and (not t.is_cuda or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be a GPU tensor on {like.device}")
 
 
@@ -278,7 +281,7 @@ def check_chunkwise(workspace):
 
 
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return _cuda_getCurrentRawStream(t.get_device())
 
 
 def _validate(q, k, v, g, out):
@@ -558,71 +561,75 @@ def recurrent_step(q, k, v, state, g=None, *, gammas=None, rotary_base=0.0, pos=
 # ---------------------------------------------------------------------------
 # Gated delta rule
 # ---------------------------------------------------------------------------
-def _delta_inputs(q, k, v, log_decay, beta, more, cu_seqlens, max_seqlen):
+# The decode calls' kernels take a few microseconds, so these checks read each
+# property once and build nothing they do not need.
+def _delta_inputs(q, k, v, log_decay, beta, name, other, cu_seqlens, max_seqlen):
     """Checks of the chunkwise calls' tensors; returns (batch, seqlen,
-    total_tokens). `more`: further tensors of v's shape and dtype, by name."""
+    total_tokens). `other` (called `name`): a further tensor like v."""
     packed = cu_seqlens is not None
     dims = 3 if packed else 4
-    if not q.is_cuda:
+    dev, dtype = q.get_device(), q.dtype
+    if dev < 0:
         raise ValueError("q must be a GPU tensor")
-    for name, t in (("q", q), ("k", k), ("v", v), *more):
-        _on_device(name, t, q)
+    for n, t in (("q", q), ("k", k), ("v", v), (name, other)):
+        if t.get_device() != dev:
+            raise ValueError(f"{n} must be a GPU tensor on {q.device}")
         if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.dtype != q.dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {q.dtype}")
+            raise ValueError(f"{n} must be contiguous")
+        if t.dtype != dtype:
+            raise ValueError(f"{n} has dtype {t.dtype}, expected {dtype}")
         if t.dim() != dims:
-            raise ValueError(f"{name} must be " + ("[total_tokens, heads, d]" if packed else
-                                                   "[batch, seqlen, heads, d]"))
-    if k.shape != q.shape:
+            raise ValueError(f"{n} must be " + ("[total_tokens, heads, d]" if packed else "[batch, seqlen, heads, d]"))
+    qs, vs = q.shape, v.shape
+    if k.shape != qs:
         raise ValueError("k must have the shape of q")
-    if v.shape[:-2] != q.shape[:-2]:
+    if vs[:-2] != qs[:-2]:
         raise ValueError("v must agree with q on its tokens")
-    for name, t in more:
-        if t.shape != v.shape:
-            raise ValueError(f"{name} must have the shape of v")
-    for name, t in (("log_decay", log_decay), ("beta", beta)):
-        _on_device(name, t, q)
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != v.shape[:-1]:
-            raise ValueError(f"{name} must be a contiguous fp32 tensor {list(v.shape[:-1])}")
+    if other.shape != vs:
+        raise ValueError(f"{name} must have the shape of v")
+    gates = vs[:-1]
+    for n, t in (("log_decay", log_decay), ("beta", beta)):
+        if t.get_device() != dev or t.dtype != torch.float32 or not t.is_contiguous() or t.shape != gates:
+            raise ValueError(f"{n} must be a contiguous fp32 tensor {list(gates)} on {q.device}")
     if not packed:
         if max_seqlen is not None:
             raise ValueError("max_seqlen goes with cu_seqlens")
-        return q.shape[0], q.shape[1], 0
-    _on_device("cu_seqlens", cu_seqlens, q)
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        return qs[0], qs[1], 0
+    if (cu_seqlens.get_device() != dev or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1
+            or not cu_seqlens.is_contiguous()):
         raise ValueError("cu_seqlens must be a contiguous GPU int32 tensor [batch + 1]")
     if max_seqlen is None:
         raise ValueError("max_seqlen (a bound on every length) goes with cu_seqlens")
-    return cu_seqlens.numel() - 1, int(max_seqlen), q.shape[0]
+    return cu_seqlens.numel() - 1, int(max_seqlen), qs[0]
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_desc_of(batch, seqlen, k_heads, v_heads, dk, dv, dtype, scale):
+    """(descriptor, reference to it): calls only read it."""
+    d = DeltaDesc(batch, seqlen, k_heads, v_heads, dk, dv, dtype, scale)
+    return d, ctypes.byref(d)
 
 
 def _delta_desc(batch, seqlen, q, v, scale):
-    return DeltaDesc(batch, seqlen, q.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1], _dtype_code(q), float(scale))
+    qs, vs = q.shape, v.shape
+    return _delta_desc_of(batch, seqlen, qs[-2], vs[-2], qs[-1], vs[-1], _dtype_code(q), float(scale))[1]
 
 
 def _delta_state(name, t, batch, q, v):
     if t is None:
         return
-    _on_device(name, t, q)
-    shape = (batch, v.shape[-2], q.shape[-1], v.shape[-1])
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous fp32 [batch, v_heads, dk, dv] tensor")
+    if (t.get_device() != q.get_device() or t.dtype != torch.float32 or not t.is_contiguous()
+            or t.shape != (batch, v.shape[-2], q.shape[-1], v.shape[-1])):
+        raise ValueError(f"{name} must be a contiguous fp32 [batch, v_heads, dk, dv] tensor on {q.device}")
 
 
-class _current:
+_here = contextlib.nullcontext()
+
+
+def _current(t):
     """The tensor's device as the current one (kernels launch there)."""
-
-    def __init__(self, t):
-        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *err):
-        if self.guard is not None:
-            self.guard.__exit__(*err)
+    dev = t.get_device()
+    return _here if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def delta_chunkwise_fwd(q, k, v, log_decay, beta, *, scale=1.0, state_in=None, state_out=None, cu_seqlens=None,
@@ -636,15 +643,15 @@ def delta_chunkwise_fwd(q, k, v, log_decay, beta, *, scale=1.0, state_in=None, s
     synchronize and raise RetentionError if cu_seqlens had to be clamped
     (check_chunkwise does the same later for a caller's workspace)."""
     out = torch.empty_like(v) if out is None else out
-    batch, seqlen, total = _delta_inputs(q, k, v, log_decay, beta, (("out", out),), cu_seqlens, max_seqlen)
+    batch, seqlen, total = _delta_inputs(q, k, v, log_decay, beta, "out", out, cu_seqlens, max_seqlen)
     _delta_state("state_in", state_in, batch, q, v)
     _delta_state("state_out", state_out, batch, q, v)
     desc = _delta_desc(batch, seqlen, q, v, scale)
     L = lib()
-    need = L.retention_delta_workspace_bytes(ctypes.byref(desc), int(cu_seqlens is not None), total)
+    need = L.retention_delta_workspace_bytes(desc, int(cu_seqlens is not None), total)
     workspace, ws_bytes, _ = _workspace(workspace, need, q)
     with _current(q):
-        _check(L.retention_delta_fwd(ctypes.byref(desc), _ptr(cu_seqlens), total, _ptr(q), _ptr(k), _ptr(v),
+        _check(L.retention_delta_fwd(desc, _ptr(cu_seqlens), total, _ptr(q), _ptr(k), _ptr(v),
                                      _ptr(log_decay), _ptr(beta), _ptr(out), _ptr(state_in), _ptr(state_out),
                                      _ptr(workspace), ws_bytes, _stream(q)))
     if check:
@@ -659,7 +666,7 @@ def delta_chunkwise_bwd(q, k, v, log_decay, beta, dout, *, scale=1.0, state_in=N
     (dq, dk, dv, dlog_decay, dbeta), and d_state_in after them when state_in
     is given. Packed sequences and check as in the forward; gradient rows
     outside every sequence are zero."""
-    batch, seqlen, total = _delta_inputs(q, k, v, log_decay, beta, (("dout", dout),), cu_seqlens, max_seqlen)
+    batch, seqlen, total = _delta_inputs(q, k, v, log_decay, beta, "dout", dout, cu_seqlens, max_seqlen)
     _delta_state("state_in", state_in, batch, q, v)
     _delta_state("d_state_out", d_state_out, batch, q, v)
     new = torch.empty_like if cu_seqlens is None else torch.zeros_like
@@ -668,10 +675,10 @@ def delta_chunkwise_bwd(q, k, v, log_decay, beta, dout, *, scale=1.0, state_in=N
         grads.append(torch.empty_like(state_in))
     desc = _delta_desc(batch, seqlen, q, v, scale)
     L = lib()
-    need = L.retention_delta_bwd_workspace_bytes(ctypes.byref(desc), int(cu_seqlens is not None), total)
+    need = L.retention_delta_bwd_workspace_bytes(desc, int(cu_seqlens is not None), total)
     workspace, ws_bytes, _ = _workspace(workspace, need, q)
     with _current(q):
-        _check(L.retention_delta_bwd(ctypes.byref(desc), _ptr(cu_seqlens), total, _ptr(q), _ptr(k), _ptr(v),
+        _check(L.retention_delta_bwd(desc, _ptr(cu_seqlens), total, _ptr(q), _ptr(k), _ptr(v),
                                      _ptr(log_decay), _ptr(beta), _ptr(dout), _ptr(state_in), _ptr(d_state_out),
                                      *(_ptr(t) for t in grads[:5]), _ptr(grads[5]) if state_in is not None else None,
                                      _ptr(workspace), ws_bytes, _stream(q)))
@@ -688,17 +695,17 @@ def delta_recurrent_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=No
     slots[b]; a slot that is negative, outside the pool or named by an earlier
     sequence is inactive (its output is zero)."""
     out = torch.empty_like(v) if out is None else out
-    batch, seqlen, _ = _delta_inputs(q, k, v, log_decay, beta, (("out", out),), None, None)
+    batch, seqlen, _ = _delta_inputs(q, k, v, log_decay, beta, "out", out, None, None)
     if seqlen != 1:
         raise ValueError("delta_recurrent_step takes one token per sequence (seqlen 1)")
     _delta_state("state", state, batch if slots is None else state.shape[0], q, v)
     if slots is not None:
-        _on_device("slots", slots, q)
-        if slots.dtype != torch.int32 or not slots.is_contiguous() or tuple(slots.shape) != (batch,):
+        if (slots.get_device() != q.get_device() or slots.dtype != torch.int32 or not slots.is_contiguous()
+                or slots.shape != (batch,)):
             raise ValueError("slots must be a contiguous GPU int32 tensor [batch]")
     desc = _delta_desc(batch, 1, q, v, scale)
     with _current(q):
-        _check(lib().retention_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
+        _check(lib().retention_delta_step(desc, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta),
                                           _ptr(out), _ptr(state), _ptr(slots), state.shape[0], _stream(q)))
     return out
 
@@ -708,25 +715,29 @@ def delta_recurrent_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=No
 # ---------------------------------------------------------------------------
 def _norm_inputs(x, rows, weights):
     """Checks of a norm call's tensors: `rows` like x, `weights` fp32 [width]."""
-    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    if dev < 0 or not x.is_contiguous() or x.dim() < 1:
         raise ValueError("x must be a contiguous GPU tensor [..., width]")
     for name, t in rows:
-        if t is None:
-            continue
-        _on_device(name, t, x)
-        if t.dtype != x.dtype or not t.is_contiguous() or t.shape != x.shape:
-            raise ValueError(f"{name} must be a contiguous tensor of x's shape and dtype")
+        if t is not None and (t.get_device() != dev or t.dtype != dtype or not t.is_contiguous() or t.shape != shape):
+            raise ValueError(f"{name} must be a contiguous tensor of x's shape and dtype on {x.device}")
+    width = shape[-1:]
     for name, t in weights:
-        if t is None:
-            continue
-        _on_device(name, t, x)
-        if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (x.shape[-1],):
-            raise ValueError(f"{name} must be a contiguous fp32 tensor [{x.shape[-1]}]")
+        if t is not None and (t.get_device() != dev or t.dtype != torch.float32 or not t.is_contiguous()
+                              or t.shape != width):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor [{shape[-1]}] on {x.device}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_desc_of(rows, width, dtype, center, eps):
+    """(descriptor, reference to it): calls only read it."""
+    d = NormDesc(rows, width, dtype, center, eps)
+    return d, ctypes.byref(d)
 
 
 def _norm_desc(x, center, eps):
     width = x.shape[-1]
-    return NormDesc(x.numel() // width if width else 0, width, _dtype_code(x), int(bool(center)), float(eps))
+    return _norm_desc_of(x.numel() // width if width else 0, width, _dtype_code(x), int(bool(center)), float(eps))[1]
 
 
 def head_norm_fwd(x, weight=None, gate=None, *, center=False, eps=1e-5, out=None):
@@ -737,7 +748,7 @@ def head_norm_fwd(x, weight=None, gate=None, *, center=False, eps=1e-5, out=None
     _norm_inputs(x, (("gate", gate), ("out", out)), (("weight", weight),))
     desc = _norm_desc(x, center, eps)
     with _current(x):
-        _check(lib().retention_head_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(gate), _ptr(out),
+        _check(lib().retention_head_norm_fwd(desc, _ptr(x), _ptr(weight), _ptr(gate), _ptr(out),
                                              _stream(x)))
     return out
 
@@ -751,10 +762,10 @@ def head_norm_bwd(x, dout, weight=None, gate=None, *, center=False, eps=1e-5, wo
     dgate = torch.empty_like(gate) if gate is not None else None
     desc = _norm_desc(x, center, eps)
     L = lib()
-    need = L.retention_head_norm_bwd_workspace_bytes(ctypes.byref(desc)) if weight is not None else 0
+    need = L.retention_head_norm_bwd_workspace_bytes(desc) if weight is not None else 0
     workspace, ws_bytes, _ = _workspace(workspace, need, x)
     with _current(x):
-        _check(L.retention_head_norm_bwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(gate), _ptr(dout), _ptr(dx),
+        _check(L.retention_head_norm_bwd(desc, _ptr(x), _ptr(weight), _ptr(gate), _ptr(dout), _ptr(dx),
                                          _ptr(dweight), _ptr(dgate), _ptr(workspace), ws_bytes, _stream(x)))
     return dx, dweight, dgate
 
@@ -771,7 +782,7 @@ def residual_norm_fwd(x, y, weight, *, post_weight=None, scale=None, skip=1.0, c
                  (("weight", weight), ("post_weight", post_weight), ("scale", scale)))
     desc = _norm_desc(x, center, eps)
     with _current(x):
-        _check(lib().retention_residual_norm_fwd(ctypes.byref(desc), float(skip), _ptr(x), _ptr(y), _ptr(weight),
+        _check(lib().retention_residual_norm_fwd(desc, float(skip), _ptr(x), _ptr(y), _ptr(weight),
                                                  _ptr(post_weight), _ptr(scale), _ptr(out), _ptr(residual), _stream(x)))
     return out, residual
 
@@ -789,10 +800,10 @@ def residual_norm_bwd(x, y, weight, dout, dresidual=None, *, post_weight=None, s
     dscale = torch.empty_like(scale) if scale is not None else None
     desc = _norm_desc(x, center, eps)
     L = lib()
-    need = L.retention_residual_norm_bwd_workspace_bytes(ctypes.byref(desc))
+    need = L.retention_residual_norm_bwd_workspace_bytes(desc)
     workspace, ws_bytes, _ = _workspace(workspace, need, x)
     with _current(x):
-        _check(L.retention_residual_norm_bwd(ctypes.byref(desc), float(skip), _ptr(x), _ptr(y), _ptr(weight),
+        _check(L.retention_residual_norm_bwd(desc, float(skip), _ptr(x), _ptr(y), _ptr(weight),
                                              _ptr(post_weight), _ptr(scale), _ptr(dout), _ptr(dresidual), _ptr(dx),
                                              _ptr(dy), _ptr(dweight), _ptr(dpost), _ptr(dscale), _ptr(workspace),
                                              ws_bytes, _stream(x)))

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
     for (int pl = 0; pl < NP; ++pl)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks >= (w >> 1)) f[pl][ks] = buf_frag(rs, lane_off + mat_frag(pl, w, ks) * SZ, tag);  // upper triangular
+        if (ks >= (w >> 1)) f[pl][ks] = buf_frag(rs, lane_off, mat_frag(pl, w, ks) * SZ, tag);  // upper triangular
   };
   auto load_keys = [&](frag_t<T>(&f)[2][CS::KS], int blk) {
     const auto rs = key_rsrc(p.kf, blk);
@@ -82,14 +82,17 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int ks = 0; ks < CS::KS; ++ks)
-        f[rt][ks] = buf_frag(rs, lane_off + key_frag(krow / 16 + ks, rt) * SZ, tag);
+        f[rt][ks] = buf_frag(rs, lane_off, key_frag(krow / 16 + ks, rt) * SZ, tag);
+  };
+  auto load_column = [&](frag_t<T>(&f)[TPW][4], __amdgpu_buffer_rsrc_t rs, int t, int ks) {
+    f[t][ks] = buf_frag(rs, lane_off, column_frag(krow / 32 + t, ks) * SZ, tag);
   };
   auto load_columns = [&](frag_t<T>(&f)[TPW][4], const void* x, int blk) {
     const auto rs = key_rsrc(x, blk);
 #pragma unroll
     for (int t = 0; t < TPW; ++t)
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) f[t][ks] = buf_frag(rs, lane_off + column_frag(krow / 32 + t, ks) * SZ, tag);
+      for (int ks = 0; ks < 4; ++ks) load_column(f, rs, t, ks);
   };
   auto load_pairs = [&](PairOf<T>(&x)[CG][4], const void* from, int blk) {
     const auto rs = value_rsrc(from, blk);
@@ -120,9 +123,9 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
     auto load_rest = [&](int blk) {
       load_mat(tf, p.tt, blk);
       const auto er = vec_rsrc(blk);
-      eg = buf_f4(er, r4 * 4);
-      el = buf_f4(er, (kB + r4) * 4);
-      last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, (kB - 1) * 4, 0, 0));
+      eg = buf_f4(er, r4 * 4, 0);
+      el = buf_f4(er, r4 * 4, kB * 4);
+      last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, 0, (kB - 1) * 4, 0));
     };
     load_rest(nblk - 1);
     if constexpr (kAhead) {
@@ -151,25 +154,33 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         dot = sum64(dot);
         if (lane == 0) p.adot[at] = dot;
       }
-      if constexpr (kAhead)
-        load_columns(qc, p.qc, blk);
-      else
-        load_keys(kf, blk);
+      if constexpr (!kAhead) load_keys(kf, blk);
+      const auto queries = key_rsrc(p.qc, blk);
+      Split<T> f[CS::KS];
       f32x16 ksum[2] = {zero16(), zero16()};
 #pragma unroll
       for (int t = 0; t < TPW; ++t)
         static_for<2>([&](auto sl) {
           constexpr int SLI = decltype(sl)::value;
-          const Split<T> f = split_acc<SLI>(s[t], tag);
           const int ks = 2 * t + SLI;
+          f[ks] = split_acc<SLI>(s[t], tag);
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl)
-#pragma unroll
-            for (int rt = 0; rt < 2; ++rt) ksum[rt] = mma32(kf[rt][ks], f.f[pl], ksum[rt]);
+          for (int pl = 0; pl < NP; ++pl) ksum[0] = mma32(kf[0][ks], f[ks].f[pl], ksum[0]);
+          if constexpr (kAhead) {
+            load_column(qc, queries, t, 2 * SLI);
+            load_column(qc, queries, t, 2 * SLI + 1);
+          }
           T* sn = reinterpret_cast<T*>(p.dsnap) + (slot * D + vcol) * D + krow + 16 * ks + 8 * h2;
-          *reinterpret_cast<frag_t<T>*>(sn) = f.f[0];
+          *reinterpret_cast<frag_t<T>*>(sn) = f[ks].f[0];
         });
-      put_partial(part, w, ksum, lane);
+      if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int ks = 0; ks < CS::KS; ++ks)
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) ksum[1] = mma32(kf[1][ks], f[ks].f[pl], ksum[1]);
+      put_partial(part, w, 0, ksum[0], lane);
+      if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
+      put_partial(part, w, 1, ksum[1], lane);
       lds_barrier();
 
       // dV' of the quarter (zero behind the sequence's end: K and dO are)
@@ -199,6 +210,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         my_quarter[16 * ct] = dv[0];
       }
       const float decay = last;
+      load_rest(blk - 1);
       lds_barrier();
       auto add = [&](const frag_t<T>(&f)[TPW][4], const T* opnd) {
 #pragma unroll
@@ -220,7 +232,6 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
       if constexpr (!kAhead) load_columns(kc, p.kc, blk);
       add(kc, ow);
       if constexpr (kAhead) load_columns(kc, p.kc, blk - 1);
-      load_rest(blk - 1);
     }
     if (p.d_state_in) {
       float* so = p.d_state_in + (int64_t)bh * D * D;
@@ -251,7 +262,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
     };
     load_pairs(dout, p.dout, nblk - 1);
     load_mat(pf, p.pt, nblk - 1);
-    eg = buf_f4(vec_rsrc(nblk - 1), r4 * 4);
+    eg = buf_f4(vec_rsrc(nblk - 1), r4 * 4, 0);
     load_values(nblk - 1);
     load_pairs(dnext, p.dout, nblk - 2);
     put_dout(dout);
@@ -284,7 +295,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) dout[g][i] = dnext[g][i];
       load_pairs(dnext, p.dout, blk - 2);
-      eg = buf_f4(vec_rsrc(blk - 1), r4 * 4);
+      eg = buf_f4(vec_rsrc(blk - 1), r4 * 4, 0);
       lds_barrier();
       lds_barrier();
       // dv and the row sums of the quarter

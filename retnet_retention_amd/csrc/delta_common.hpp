@@ -169,14 +169,12 @@ __device__ __forceinline__ constexpr int col_at(int place) {                    
 
 // Partial products of the waves, [wave][quad of rows][place of column] of 4
 // rows each.
-__device__ __forceinline__ void put_partial(f32x4* buf, int wave, const f32x16* acc, int lane) {
+__device__ __forceinline__ void put_partial(f32x4* buf, int wave, int rt, const f32x16& acc, int lane) {
   const int n = lane & 31, h = lane >> 5;
 #pragma unroll
-  for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      buf[(wave * 16 + 8 * rt + 2 * q + h) * 32 + col_place(n)] =
-          f32x4{acc[rt][4 * q], acc[rt][4 * q + 1], acc[rt][4 * q + 2], acc[rt][4 * q + 3]};
+  for (int q = 0; q < 4; ++q)
+    buf[(wave * 16 + 8 * rt + 2 * q + h) * 32 + col_place(n)] =
+        f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
 }
 template <int RG>
 __device__ __forceinline__ f32x4 get_partial(const f32x4* buf, int ct, int quad, int c) {
@@ -212,18 +210,21 @@ __device__ __forceinline__ constexpr int quad_place(int g) { return 4 * (((g & 1
 // Reads and writes through a buffer descriptor whose end is the end of what
 // exists: rows behind it read as zero and are not written, without a branch.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ u32x4b raw_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+// `at` is the part of the offset that is the same in all lanes (a scalar: a
+// vector register for each constant would cost more registers than the data).
+__device__ __forceinline__ u32x4b raw_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0);
 }
-__device__ __forceinline__ bf16x8 buf_frag(__amdgpu_buffer_rsrc_t rs, uint32_t off, bf16*) {
-  return __builtin_bit_cast(bf16x8, raw_load16(rs, off));
+__device__ __forceinline__ bf16x8 buf_frag(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at, bf16*) {
+  return __builtin_bit_cast(bf16x8, raw_load16(rs, off, at));
 }
-__device__ __forceinline__ f32x8 buf_frag(__amdgpu_buffer_rsrc_t rs, uint32_t off, float*) {
-  const f32x4 a = __builtin_bit_cast(f32x4, raw_load16(rs, off)), b = __builtin_bit_cast(f32x4, raw_load16(rs, off + 16));
+__device__ __forceinline__ f32x8 buf_frag(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at, float*) {
+  const f32x4 a = __builtin_bit_cast(f32x4, raw_load16(rs, off, at));
+  const f32x4 b = __builtin_bit_cast(f32x4, raw_load16(rs, off + 16, at));
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-__device__ __forceinline__ f32x4 buf_f4(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-  return __builtin_bit_cast(f32x4, raw_load16(rs, off));
+__device__ __forceinline__ f32x4 buf_f4(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t at) {
+  return __builtin_bit_cast(f32x4, raw_load16(rs, off, at));
 }
 // two neighbouring elements
 typedef uint32_t u32x2b __attribute__((ext_vector_type(2)));

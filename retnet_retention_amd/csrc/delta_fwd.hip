@@ -304,7 +304,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
 // for a block ahead, spread over the step: a wave that asks for much at once
 // waits until the caches have taken it.
 template <typename T, int D, bool GRAD>
-__global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
   constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1, SZ = sizeof(T);
   constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
@@ -376,28 +376,31 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
       const auto rs = key_rsrc(p.kf, blk);
 #pragma unroll
       for (int ks = 0; ks < CS::KS; ++ks)
-        kf[rt][ks] = buf_frag(rs, lane_off + key_frag(CS::KS * rg + ks, rt) * SZ, tag);
+        kf[rt][ks] = buf_frag(rs, lane_off, key_frag(CS::KS * rg + ks, rt) * SZ, tag);
     };
     auto load_column = [&](__amdgpu_buffer_rsrc_t rs, int t, int ks) {
-      kc[t][ks] = buf_frag(rs, lane_off + column_frag(TPW * rg + t, ks) * SZ, tag);
+      kc[t][ks] = buf_frag(rs, lane_off, column_frag(TPW * rg + t, ks) * SZ, tag);
     };
-    auto load_rest = [&](int blk) {
-      const auto tr = mat_rsrc(p.t, NP, blk);
-#pragma unroll
-      for (int pl = 0; pl < NP; ++pl)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-          if (ks <= (w >> 1)) tf[pl][ks] = buf_frag(tr, lane_off + mat_frag(pl, w, ks) * SZ, tag);  // lower triangular
+    auto load_values = [&](int blk) {  // what X takes
       const auto vr = value_rsrc(p.v, blk);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int g = 0; g < CG; ++g) v[g][i] = buf_pair(vr, pair_off[i] + 32 * g * SZ, tag);
-      const auto er = vec_rsrc(blk);
-      eg = buf_f4(er, r4 * 4);
-      el = buf_f4(er, (kB + r4) * 4);
-      last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, (kB - 1) * 4, 0, 0));
+      eg = buf_f4(vec_rsrc(blk), r4 * 4, 0);
     };
+    auto load_rest = [&](int blk) {  // what V' takes
+      const auto tr = mat_rsrc(p.t, NP, blk);
+#pragma unroll
+      for (int pl = 0; pl < NP; ++pl)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          if (ks <= (w >> 1)) tf[pl][ks] = buf_frag(tr, lane_off, mat_frag(pl, w, ks) * SZ, tag);  // lower triangular
+      const auto er = vec_rsrc(blk);
+      el = buf_f4(er, r4 * 4, kB * 4);
+      last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, 0, (kB - 1) * 4, 0));
+    };
+    load_values(0);
     load_rest(0);
     if constexpr (kAhead) {
       load_keys(0, 0);
@@ -410,28 +413,35 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
         load_keys(blk, 1);
       }
       const auto columns = key_rsrc(p.kc, blk);
-      f32x16 ksum[2] = {zero16(), zero16()};
       T* copy = my_os + (kTwoCopies ? (blk & 1) * COPY : 0);
+      // K S: the first 32 tokens' products follow the state's rounding, their
+      // sums go to LDS under the other 32 tokens' products
+      Split<T> f[CS::KS];
+      f32x16 ksum[2] = {zero16(), zero16()};
 #pragma unroll
       for (int t = 0; t < TPW; ++t)
         static_for<2>([&](auto sl) {
           constexpr int SLI = decltype(sl)::value;
-          const Split<T> f = split_acc<SLI>(s[t], tag);
           const int ks = 2 * t + SLI;
+          f[ks] = split_acc<SLI>(s[t], tag);
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl)
-#pragma unroll
-            for (int rt = 0; rt < 2; ++rt) ksum[rt] = mma32(kf[rt][ks], f.f[pl], ksum[rt]);
-          if constexpr (kAhead) {  // a load goes in the time of two products
+          for (int pl = 0; pl < NP; ++pl) ksum[0] = mma32(kf[0][ks], f[ks].f[pl], ksum[0]);
+          if constexpr (kAhead) {
             load_column(columns, t, 2 * SLI);
             load_column(columns, t, 2 * SLI + 1);
           }
 #pragma unroll
           for (int pl = 0; pl < PP; ++pl)
-            *reinterpret_cast<frag_t<T>*>(copy + pl * CS::SPLANE + 16 * ks) = f.f[pl];
-          __builtin_amdgcn_sched_barrier(0);
+            *reinterpret_cast<frag_t<T>*>(copy + pl * CS::SPLANE + 16 * ks) = f[ks].f[pl];
         });
-      put_partial(part, w, ksum, lane);
+      if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int ks = 0; ks < CS::KS; ++ks)
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) ksum[1] = mma32(kf[1][ks], f[ks].f[pl], ksum[1]);
+      put_partial(part, w, 0, ksum[0], lane);
+      if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
+      put_partial(part, w, 1, ksum[1], lane);
       if constexpr (GRAD) {
         if (blk && blk % kDeltaGroup == 0) {
           float* an = p.anchor + ((((int64_t)(base / kDeltaGroup + b + blk / kDeltaGroup - 1) * p.heads + h) * CS::NSL +
@@ -455,6 +465,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
         put_opnd<PITCH, OPLANE>(ox, row_of(ct, c), r4, x);
       }
       if constexpr (kAhead) load_keys(blk + 1, 0);
+      load_values(blk + 1);
       lds_barrier();
 
       // V' of the quarter (waves 0 and 1 multiply T's upper zeros too, rather than branch)
@@ -484,6 +495,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) load_column(columns, t, ks);
       }
+      load_rest(blk + 1);
       lds_barrier();
 
 #pragma unroll
@@ -499,7 +511,6 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl) s[t] = mma32(kc[t][ks], uf[pl], s[t]);
       }
-      load_rest(blk + 1);
     }
     if (p.state_out) {
       float* so = p.state_out + (int64_t)bh * D * D;
@@ -529,7 +540,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
     auto load_queries = [&](int blk) {
       const auto rs = key_rsrc(p.qf, blk);
 #pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) qf[ks] = buf_frag(rs, lane_off + query_frag<D>(w, ks) * SZ, tag);
+      for (int ks = 0; ks < D / 32; ++ks) qf[ks] = buf_frag(rs, lane_off, query_frag<D>(w, ks) * SZ, tag);
     };
     auto load_rest = [&](int blk) {
       const auto mr = mat_rsrc(p.m, PP, blk);
@@ -537,8 +548,8 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaParams p) {
       for (int pl = 0; pl < PP; ++pl)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks <= (w >> 1)) mf[pl][ks] = buf_frag(mr, lane_off + mat_frag(pl, w, ks) * SZ, tag);
-      eg = buf_f4(vec_rsrc(blk), r4 * 4);
+          if (ks <= (w >> 1)) mf[pl][ks] = buf_frag(mr, lane_off, mat_frag(pl, w, ks) * SZ, tag);
+      eg = buf_f4(vec_rsrc(blk), r4 * 4, 0);
       if constexpr (GRAD) {
         const auto dr = value_rsrc(p.dout, blk);
 #pragma unroll
