@@ -171,6 +171,10 @@ __device__ __forceinline__ void store8(float* p, const F8& v) {
 // clobber keeps the compiler from moving memory accesses across it.
 __device__ __forceinline__ void bare_barrier() { __asm__ volatile("s_barrier" ::: "memory"); }
 
+// Barrier of the waves' LDS traffic alone: loads and stores of global memory
+// stay in flight across it.
+__device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // a wave-uniform int held in a scalar register
 __device__ __forceinline__ int uniform_i(int x) { return __builtin_amdgcn_readfirstlane(x); }
 

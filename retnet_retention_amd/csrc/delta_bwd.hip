@@ -334,24 +334,24 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 }
 
 // d q and d k of one block and key head, summed over the value heads that
-// share it; wave w the key columns 32 w .. + 31.
-template <typename T, int D>
+// share it (GROUPED: more than one); wave w the key columns 32 w .. + 31. Bound
+// by the two states a block reads, D x D each: they pass through LDS by 32 value
+// columns, the next tile (two buffers, fp32 one) on its way while one is
+// multiplied, and each of dO, dv and V' is read once for all its products.
+template <typename T, int D, bool GROUPED>
 __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
-  constexpr int NW = D / 32;
-  constexpr int DV = 32;  // value rows of a state tile in LDS
+  constexpr int NW = D / 32, TW = 8 / NW;  // tasks of 16 rows of dP and dA a wave
+  constexpr int DV = 32;                   // value columns of a state tile in LDS
+  constexpr int BUFS = sizeof(T) == 2 ? 2 : 1;
   using ST = LTile<T, DV, D, kColTile>;
-  using QT = LTile<T, kB, D, kColTile>;
   constexpr int PA = sizeof(T) == 2 ? 40 : 36;  // pitch of the row operands
   constexpr int PM = sizeof(T) == 2 ? 72 : 68;  // pitch of the 64 x 64 matrices
-  constexpr int AROWS = 3 * kB * PA * (int)sizeof(T);
-  constexpr int TILES = 2 * ST::BYTES + AROWS > QT::BYTES ? 2 * ST::BYTES + AROWS : QT::BYTES;
-  __shared__ __attribute__((aligned(1024))) char buf[TILES];
+  constexpr int ROWS = 3 * kB * PA;
+  __shared__ __attribute__((aligned(1024))) char tiles[2 * BUFS * ST::BYTES];
+  __shared__ __attribute__((aligned(16))) T row_ops[BUFS * ROWS];  // [dO, dv, V'][64][PA]
   __shared__ __attribute__((aligned(16))) T mp[kB * PM], mpt[kB * PM], ms[kB * PM];
   __shared__ double sg[kB];
   T* const tag = nullptr;
-  char* st_s = buf;
-  char* st_d = buf + ST::BYTES;
-  T* rows_a = reinterpret_cast<T*>(buf + 2 * ST::BYTES);  // [dO, dv, V'][64][PA]
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform_i(tid >> 6);
   const int b = blockIdx.x / p.blocks_max, blk = blockIdx.x % p.blocks_max, hk = blockIdx.y;
@@ -363,18 +363,37 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
   const int64_t row0 = tok0 + blk * kB;
   const int n = lane & 31, h2 = lane >> 5, g16 = lane >> 4, c = lane & 15;
   const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
-  const int group = p.heads / p.k_heads;
-  TileLoads<T, QT, NW> qloads;
-  qloads.init(qs, lane);
+  const int group = GROUPED ? p.heads / p.k_heads : 1;
+  // keys and queries by columns, the wave's 32
+  const int64_t key_slot = ((int64_t)(base + blk) * p.k_heads + hk) * (kB * D) + 8 * lane;
+  const T* KC = reinterpret_cast<const T*>(p.kc) + key_slot;
+  const T* QC = reinterpret_cast<const T*>(p.qc) + key_slot;
 
   f32x16 dq[2] = {zero16(), zero16()}, dk[2] = {zero16(), zero16()};
   for (int hh = 0; hh < group; ++hh) {
     const int h = hk * group + hh;
     const int64_t slot = (int64_t)(base + blk) * p.heads + h;
-    const T* DO = reinterpret_cast<const T*>(p.dout) + row0 * vs + h * D;
-    const T* DVp = reinterpret_cast<const T*>(p.dv) + row0 * vs + h * D;
-    const T* U = reinterpret_cast<const T*>(p.u) + row0 * vs + h * D;
-    __syncthreads();  // the last head's reads
+    const T* src[3] = {reinterpret_cast<const T*>(p.dout) + row0 * vs + h * D,
+                       reinterpret_cast<const T*>(p.dv) + row0 * vs + h * D,
+                       reinterpret_cast<const T*>(p.u) + row0 * vs + h * D};
+    const T* SN = reinterpret_cast<const T*>(p.snap) + slot * D * D;
+    const T* DN = reinterpret_cast<const T*>(p.dsnap) + slot * D * D;
+    TileLoads<T, ST, NW> sloads;
+    sloads.init(D, lane);
+    constexpr int RN = (3 * kB * (DV / 8) + 2 * D - 1) / (2 * D);  // row operands: chunks of 8 a thread
+    Raw8<T> raw[RN];
+    auto ask = [&](int d0) {
+      char* to = tiles + (d0 / DV % BUFS) * 2 * ST::BYTES;
+      sloads.issue(to, SN, D, d0, w);
+      sloads.issue(to + ST::BYTES, DN, D, d0, w);
+#pragma unroll
+      for (int i = 0; i < RN; ++i) {
+        const int at = tid + i * 2 * D, m = at / (kB * (DV / 8)), r = at / (DV / 8) % kB, j = at % (DV / 8) * 8;
+        raw[i] = Raw8<T>{};
+        if (m < 3 && r < rows) raw[i] = ld_raw8((m == 0 ? src[0] : m == 1 ? src[1] : src[2]) + r * vs + d0 + j);
+      }
+    };
+    if constexpr (GROUPED) __syncthreads();  // the last head's reads
     if (w == 0) {
       float g = lane < rows ? p.log_decay[(row0 + lane) * p.heads + h] : 0.f;
       if (g < kMinLogDecay) g = kMinLogDecay;
@@ -387,69 +406,41 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
       sg[lane] = s;
     }
     for (int i = tid; i < 3 * kB * PM; i += 2 * D) (i < kB * PM ? mp : i < 2 * kB * PM ? mpt : ms)[i % (kB * PM)] = (T)0.f;
-    __syncthreads();
-    // dP and dA: 8 tasks of 16 rows
-    for (int task = w; task < 8; task += NW) {
-      const int rb = task & 3, which = task >> 2;
-      const T* A = (which ? DVp : DO) + (16 * rb + c) * vs + 8 * g16;
-      const bool keep = 16 * rb + c < rows;
-      f32x4 acc[4] = {zero4(), zero4(), zero4(), zero4()};
-#pragma unroll 2
-      for (int ks = 0; ks < D / 32; ++ks) {
-        const frag_t<T> a = global_row8(A + 32 * ks, keep);
+
+    f32x4 acc[TW][4];
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) {
-          if (ct > rb) break;
-          const int r = 16 * ct + c;
-          acc[ct] = mma(a, global_row8(U + r * vs + 8 * g16 + 32 * ks, r < rows), acc[ct]);
-        }
-      }
+    for (int k = 0; k < TW; ++k)
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        if (ct > rb) break;
-        const int s = 16 * ct + c;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 16 * rb + 4 * g16 + i;
-          const float e = s <= r ? __builtin_amdgcn_exp2f((float)((sg[r] - sg[s]) * 1.4426950408889634)) : 0.f;
-          if (which == 0 && s <= r) {
-            const T x = (T)(p.scale * e * acc[ct][i]);
-            mp[r * PM + s] = x;
-            mpt[s * PM + r] = x;
-          }
-          if (which == 1 && s < r) {
-            const T x = (T)(-e * acc[ct][i]);
-            ms[r * PM + s] = x;
-            ms[s * PM + r] = x;
-          }
-        }
-      }
-    }
-    // dO S^T, V' dS^T and dv S^T over the value rows
+      for (int ct = 0; ct < 4; ++ct) acc[k][ct] = zero4();
+    // dO S^T, V' dS^T and dv S^T over the value columns
     f32x16 a0[2] = {zero16(), zero16()}, a1[2] = {zero16(), zero16()}, a2[2] = {zero16(), zero16()};
-    const T* SN = reinterpret_cast<const T*>(p.snap) + slot * D * D;
-    const T* DN = reinterpret_cast<const T*>(p.dsnap) + slot * D * D;
-    TileLoads<T, ST, NW> sloads;
-    sloads.init(D, lane);
+    ask(0);
     for (int d0 = 0; d0 < D; d0 += DV) {
-      __syncthreads();
-      sloads.issue(st_s, SN, D, d0, w);
-      sloads.issue(st_d, DN, D, d0, w);
-      for (int i = tid; i < 3 * kB * (DV / 8); i += 2 * D) {
-        const int m = i / (kB * (DV / 8)), r = i / (DV / 8) % kB, j = i % (DV / 8) * 8;
-        const T* src = (m == 0 ? DO : m == 1 ? DVp : U) + r * vs + d0 + j;
-        const frag_t<T> x = global_row8(src, r < rows);
-        *reinterpret_cast<frag_t<T>*>(rows_a + (m * kB + r) * PA + j) = x;
+      const char* tile = tiles + (d0 / DV % BUFS) * 2 * ST::BYTES;
+      T* ops = row_ops + (d0 / DV % BUFS) * ROWS;
+#pragma unroll
+      for (int i = 0; i < RN; ++i) {
+        const int at = tid + i * 2 * D, m = at / (kB * (DV / 8)), r = at / (DV / 8) % kB, j = at % (DV / 8) * 8;
+        if (m < 3) st_raw8(ops + (m * kB + r) * PA + j, raw[i], true);
       }
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
+      __builtin_amdgcn_s_waitcnt(0);  // the tiles (LDS loads run past the compiler's counting)
+      lds_barrier();
+      if (BUFS == 2 && d0 + DV < D) ask(d0 + DV);
+#pragma unroll
+      for (int k = 0; k < TW; ++k) {
+        const int task = w + k * NW, rb = task & 3, which = task >> 2;
+        const frag_t<T> a = lds_row8(ops + (which * kB + 16 * rb + c) * PA + 8 * g16);
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct)  // (all four: the upper ones are left out below)
+          acc[k][ct] = mma(a, lds_row8(ops + (2 * kB + 16 * ct + c) * PA + 8 * g16), acc[k][ct]);
+      }
 #pragma unroll
       for (int ks = 0; ks < DV / 16; ++ks) {
-        const frag_t<T> fs = tile_col8w<ST>(st_s, 16 * ks, 32 * w, lane, tag);
-        const frag_t<T> fd = tile_col8w<ST>(st_d, 16 * ks, 32 * w, lane, tag);
+        const frag_t<T> fs = state_tile_col8<ST>(tile, 16 * ks, 32 * w, lane, tag);
+        const frag_t<T> fd = state_tile_col8<ST>(tile + ST::BYTES, 16 * ks, 32 * w, lane, tag);
         // the column fragments' order of the contraction
         auto row = [&](int m, int rt) {
-          const T* at = rows_a + (m * kB + 32 * rt + n) * PA + 16 * ks + 4 * h2;
+          const T* at = ops + (m * kB + 32 * rt + n) * PA + 16 * ks + 4 * h2;
           const vec4_t<T> lo = *reinterpret_cast<const vec4_t<T>*>(at), hi = *reinterpret_cast<const vec4_t<T>*>(at + 8);
           frag_t<T> f;
 #pragma unroll
@@ -466,6 +457,40 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
           a1[rt] = mma32(row(2, rt), fd, a1[rt]);
         }
       }
+      if (BUFS == 1 && d0 + DV < D) {
+        lds_barrier();
+        ask(d0 + DV);
+      }
+    }
+    frag_t<T> fq[4], fk[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      fq[ks] = *reinterpret_cast<const frag_t<T>*>(QC + column_frag(w, ks));
+      fk[ks] = *reinterpret_cast<const frag_t<T>*>(KC + column_frag(w, ks));
+    }
+    // dP (both ways round) and dA + dA^T
+#pragma unroll
+    for (int k = 0; k < TW; ++k) {
+      const int task = w + k * NW, rb = task & 3, which = task >> 2;
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) {
+        const int s = 16 * ct + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * rb + 4 * g16 + i;
+          const float e = s <= r ? __builtin_amdgcn_exp2f((float)((sg[r] - sg[s]) * 1.4426950408889634)) : 0.f;
+          if (which == 0 && s <= r) {
+            const T x = (T)(p.scale * e * acc[k][ct][i]);
+            mp[r * PM + s] = x;
+            mpt[s * PM + r] = x;
+          }
+          if (which == 1 && s < r) {
+            const T x = (T)(-e * acc[k][ct][i]);
+            ms[r * PM + s] = x;
+            ms[s * PM + r] = x;
+          }
+        }
+      }
     }
     const float* vec = p.vec + slot * (4 * kB);
 #pragma unroll
@@ -476,11 +501,14 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
         const f32x4 el = *reinterpret_cast<const f32x4*>(vec + kB + 32 * rt + 8 * q + 4 * h2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          dq[rt][4 * q + i] += p.scale * eg[i] * a0[rt][4 * q + i];
-          dk[rt][4 * q + i] += el[i] * a1[rt][4 * q + i] - eg[i] * a2[rt][4 * q + i];
+          const float x = p.scale * eg[i] * a0[rt][4 * q + i];
+          const float y = el[i] * a1[rt][4 * q + i] - eg[i] * a2[rt][4 * q + i];
+          dq[rt][4 * q + i] = GROUPED ? dq[rt][4 * q + i] + x : x;
+          dk[rt][4 * q + i] = GROUPED ? dk[rt][4 * q + i] + y : y;
         }
       }
-    // dP^T Q, then dP K and (dA + dA^T) K
+    __syncthreads();
+    // dP^T Q, dP K and (dA + dA^T) K
     auto mrow = [&](const T* m, int rt, int ks) {
       const T* at = m + (32 * rt + n) * PM + 16 * ks + 4 * h2;
       const vec4_t<T> lo = *reinterpret_cast<const vec4_t<T>*>(at), hi = *reinterpret_cast<const vec4_t<T>*>(at + 8);
@@ -492,32 +520,17 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
       }
       return f;
     };
-    for (int pass = 0; pass < 2; ++pass) {
-      __syncthreads();
-      const T* src = reinterpret_cast<const T*>(pass ? p.k : p.q) + row0 * qs + hk * D;
-      if (rows == kB)
-        qloads.issue(buf, src, qs, 0, w);
-      else
-        qloads.issue_clamped(buf, src, qs, 0, rows - 1, w);
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const frag_t<T> f = tile_col8w<QT>(buf, 16 * ks, 32 * w, lane, tag);
+    for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-          if (pass == 0) {
-            dk[rt] = mma32(mrow(mpt, rt, ks), f, dk[rt]);
-          } else {
-            dq[rt] = mma32(mrow(mp, rt, ks), f, dq[rt]);
-            dk[rt] = mma32(mrow(ms, rt, ks), f, dk[rt]);
-          }
-        }
+      for (int rt = 0; rt < 2; ++rt) {
+        dk[rt] = mma32(mrow(mpt, rt, ks), fq[ks], dk[rt]);
+        dq[rt] = mma32(mrow(mp, rt, ks), fk[ks], dq[rt]);
+        dk[rt] = mma32(mrow(ms, rt, ks), fk[ks], dk[rt]);
       }
-    }
   }
-  T* DQ = reinterpret_cast<T*>(p.dq) + row0 * qs + hk * D + 32 * w + n;
-  T* DK = reinterpret_cast<T*>(p.dk) + row0 * qs + hk * D + 32 * w + n;
+  T* DQ = reinterpret_cast<T*>(p.dq) + row0 * qs + hk * D + 32 * w + state_col(n);
+  T* DK = reinterpret_cast<T*>(p.dk) + row0 * qs + hk * D + 32 * w + state_col(n);
 #pragma unroll
   for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
@@ -578,7 +591,11 @@ static hipError_t launch_backward(const DeltaParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((delta_reverse_kernel<T, D>), dim3(CS::NSL * p.batch * p.heads), dim3(512), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((delta_qk_grad_kernel<T, D>), dim3(p.batch * p.blocks_max, p.k_heads), dim3(2 * D), 0, stream, p);
+  const dim3 grid(p.batch * p.blocks_max, p.k_heads);
+  if (p.heads == p.k_heads)
+    hipLaunchKernelGGL((delta_qk_grad_kernel<T, D, false>), grid, dim3(2 * D), 0, stream, p);
+  else
+    hipLaunchKernelGGL((delta_qk_grad_kernel<T, D, true>), grid, dim3(2 * D), 0, stream, p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int groups = (p.blocks_max + kDeltaGroup - 1) / kDeltaGroup;
   hipLaunchKernelGGL(delta_gate_grad_kernel, dim3(p.batch * groups, p.heads), dim3(64), 0, stream, p, CS::NSL);

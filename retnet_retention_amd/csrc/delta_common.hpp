@@ -56,6 +56,33 @@ __device__ __forceinline__ C mma_split2(const A* a, const B* b, C c, float*) {
   return mma(a[0], b[0], c);
 }
 
+// the key column within 32 of position n in that order
+__device__ __forceinline__ constexpr int state_col(int n) {
+  return (n & 16) + 4 * ((((n >> 2) & 1) << 1) | ((n >> 3) & 1)) + (n & 3);
+}
+// the same fragment of a tile filled by direct loads (rows: value columns)
+template <typename TL>
+__device__ __forceinline__ bf16x8 state_tile_col8(const char* m, int k0, int n0, int lane, bf16*) {
+  const int grp = lane >> 4, t = lane & 15, h = grp >> 1;
+  const char* p = m + TL::off(k0 + 4 * h + (t >> 2), n0 + 16 * (grp & 1) + state_col(4 * (t & 3)));
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + TL::row_step(8)));
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x8 w = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, w);
+}
+template <typename TL>
+__device__ __forceinline__ f32x8 state_tile_col8(const char* m, int k0, int n0, int lane, float*) {
+  const int h = lane >> 5, col = n0 + state_col(lane & 31);
+  f32x8 f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[j] = *reinterpret_cast<const float*>(m + TL::off(k0 + 4 * h + j, col));
+    f[4 + j] = *reinterpret_cast<const float*>(m + TL::off(k0 + 8 + 4 * h + j, col));
+  }
+  return f;
+}
+
 // ---------------------------------------------------------------------------
 // Operands laid out by delta_prep_kernel in the order the lanes take them, 64 x
 // 8 elements a fragment: a wave's load of one is 1 or 2 KiB in a row (rows of
@@ -251,10 +278,6 @@ __device__ __forceinline__ void buf_put_pair(__amdgpu_buffer_rsrc_t rs, uint32_t
 __device__ __forceinline__ void buf_put_pair(__amdgpu_buffer_rsrc_t rs, uint32_t off, float a, float b, float*) {
   __builtin_amdgcn_raw_buffer_store_b64(u32x2b{__float_as_uint(a), __float_as_uint(b)}, rs, off, 0, 0);
 }
-
-// Barrier of the waves' LDS traffic alone: loads and stores of global memory
-// stay in flight across it.
-__device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ int xcd_swizzle(int id, int total) {
   // workgroups go round the 8 XCDs; neighbours in the result share an XCD's L2

@@ -55,7 +55,7 @@ __device__ __forceinline__ void store_matrix(const float (*m)[kPrepPitch], T* ou
 // bits: E is the exponential of a difference of two sums that may both be
 // large.
 template <typename T, int D, bool GRAD>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
+__global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaParams p) {
   constexpr int HALF = D < 128 ? D : 128;  // columns staged at a time
   constexpr int SP = HALF + 16 / (int)sizeof(T);
   struct Stage { T k[kB][SP], q[kB][SP]; };
@@ -126,19 +126,25 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
       }
       __syncthreads();
       if (c0 + HALF < D) load(c0 + HALF);
+      // (a loop for each wave's number of tiles: no branch stands between products)
+      auto products = [&](auto tiles) {
 #pragma unroll 2
-      for (int ks = 0; ks < HALF / 32; ++ks) {
-        const frag_t<T> fq = lds_row8(&sh.st.q[16 * w + c][32 * ks + 8 * g16]);
-        const frag_t<T> fk = lds_row8(&sh.st.k[16 * w + c][32 * ks + 8 * g16]);
-        *reinterpret_cast<frag_t<T>*>(QF + query_frag<D>(w, c0 / 32 + ks)) = fq;
+        for (int ks = 0; ks < HALF / 32; ++ks) {
+          const frag_t<T> fq = lds_row8(&sh.st.q[16 * w + c][32 * ks + 8 * g16]);
+          const frag_t<T> fk = lds_row8(&sh.st.k[16 * w + c][32 * ks + 8 * g16]);
+          *reinterpret_cast<frag_t<T>*>(QF + query_frag<D>(w, c0 / 32 + ks)) = fq;
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) {
-          if (ct > w) break;
-          const frag_t<T> fb = lds_row8(&sh.st.k[16 * ct + c][32 * ks + 8 * g16]);
-          kk[ct] = mma(fk, fb, kk[ct]);
-          qk[ct] = mma(fq, fb, qk[ct]);
+          for (int ct = 0; ct < decltype(tiles)::value; ++ct) {
+            const frag_t<T> fb = lds_row8(&sh.st.k[16 * ct + c][32 * ks + 8 * g16]);
+            kk[ct] = mma(fk, fb, kk[ct]);
+            qk[ct] = mma(fq, fb, qk[ct]);
+          }
         }
-      }
+      };
+      if (w == 0) products(std::integral_constant<int, 1>{});
+      else if (w == 1) products(std::integral_constant<int, 2>{});
+      else if (w == 2) products(std::integral_constant<int, 3>{});
+      else products(std::integral_constant<int, 4>{});
 #pragma unroll
       for (int f = w; f < 2 * (HALF / 16); f += 4)
         *reinterpret_cast<frag_t<T>*>(KF + key_frag(c0 / 16 + f / 2, f & 1)) =

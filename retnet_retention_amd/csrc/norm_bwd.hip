@@ -47,13 +47,23 @@ __global__ __launch_bounds__(R::THREADS) void head_norm_bwd_kernel(NormParams p)
     acc[j] = 0.f;
   }
   const int64_t step = (int64_t)gridDim.x * R::RPB;
+  typename R::Raw rx, rd, rg;
+  auto ask = [&](int64_t row) {
+    const int64_t at = row * p.width;
+    const bool keep = row < p.rows;
+    R::ask(rx, reinterpret_cast<const T*>(p.x) + at, p.width, l, keep);
+    R::ask(rd, reinterpret_cast<const T*>(p.dout) + at, p.width, l, keep);
+    if (p.gate) R::ask(rg, reinterpret_cast<const T*>(p.gate) + at, p.width, l, keep);
+  };
+  ask((int64_t)blockIdx.x * R::RPB + threadIdx.x / R::LPR);
   for (int64_t first = (int64_t)blockIdx.x * R::RPB; first < p.rows; first += step) {
     const int64_t row = first + threadIdx.x / R::LPR, at = row * p.width;
     const bool keep = row < p.rows;
     float n[R::E], g[R::E], d[R::E];
-    R::load(n, reinterpret_cast<const T*>(p.x) + at, p.width, l, keep);
-    R::load(d, reinterpret_cast<const T*>(p.dout) + at, p.width, l, keep);
-    if (p.gate) R::load(g, reinterpret_cast<const T*>(p.gate) + at, p.width, l, keep);
+    R::take(n, rx);
+    R::take(d, rd);
+    if (p.gate) R::take(g, rg);
+    ask(row + step);
     const float rstd = normalize<R>(n, p.width, p.center, p.eps, l, sh, turn);
     if (p.gate) {
 #pragma unroll
@@ -92,16 +102,27 @@ __global__ __launch_bounds__(R::THREADS) void residual_norm_bwd_kernel(NormParam
     aw[j] = ap[j] = as[j] = 0.f;
   }
   const int64_t step = (int64_t)gridDim.x * R::RPB;
+  typename R::Raw rx, ry, rd, rr;
+  auto ask = [&](int64_t row) {
+    const int64_t at = row * p.width;
+    const bool keep = row < p.rows;
+    R::ask(rx, reinterpret_cast<const T*>(p.x) + at, p.width, l, keep);
+    R::ask(ry, reinterpret_cast<const T*>(p.y) + at, p.width, l, keep);
+    R::ask(rd, reinterpret_cast<const T*>(p.dout) + at, p.width, l, keep);
+    if (p.dresidual) R::ask(rr, reinterpret_cast<const T*>(p.dresidual) + at, p.width, l, keep);
+  };
+  ask((int64_t)blockIdx.x * R::RPB + threadIdx.x / R::LPR);
   for (int64_t first = (int64_t)blockIdx.x * R::RPB; first < p.rows; first += step) {
     const int64_t row = first + threadIdx.x / R::LPR, at = row * p.width;
     const bool keep = row < p.rows;
     float h[R::E], y[R::E], g[R::E], r[R::E];
-    R::load(h, reinterpret_cast<const T*>(p.x) + at, p.width, l, keep);
-    R::load(y, reinterpret_cast<const T*>(p.y) + at, p.width, l, keep);
-    R::load(g, reinterpret_cast<const T*>(p.dout) + at, p.width, l, keep);
-    if (p.dresidual) R::load(r, reinterpret_cast<const T*>(p.dresidual) + at, p.width, l, keep);
-    float ry = 0.f;
-    if (p.post) ry = normalize<R>(y, p.width, p.center, p.eps, l, sh, turn);
+    R::take(h, rx);
+    R::take(y, ry);
+    R::take(g, rd);
+    if (p.dresidual) R::take(r, rr);
+    ask(row + step);
+    float rstd_y = 0.f;
+    if (p.post) rstd_y = normalize<R>(y, p.width, p.center, p.eps, l, sh, turn);
 #pragma unroll
     for (int j = 0; j < R::E; ++j) h[j] = p.skip * h[j] + scale[j] * (p.post ? y[j] * post[j] : y[j]);
     const float rh = normalize<R>(h, p.width, p.center, p.eps, l, sh, turn);
@@ -129,7 +150,7 @@ __global__ __launch_bounds__(R::THREADS) void residual_norm_bwd_kernel(NormParam
         ap[j] += g[j] * y[j];
         g[j] *= post[j];
       }
-      normalize_grad<R>(g, y, ry, p.width, p.center, sh, turn);
+      normalize_grad<R>(g, y, rstd_y, p.width, p.center, sh, turn);
     }
     if (keep) R::store(reinterpret_cast<T*>(p.dy) + at, g, p.width, l);
   }
@@ -166,7 +187,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
 // each that their sums' traffic stays small beside the rows'.
 int norm_bwd_blocks(int64_t rows, int width) {
   int threads = 256, rpb = 1;
-  if (width > 4096) threads = 1024;
+  if (width > 8192) threads = 1024;
   else if (width > 2048) threads = 512;
   else for (rpb = 32; rpb > 1 && 2048 / rpb < width;) rpb /= 2;
   const int64_t most = 256 * (1024 / threads), need = (rows + rpb - 1) / rpb;
@@ -176,7 +197,7 @@ int norm_bwd_blocks(int64_t rows, int width) {
 template <typename T>
 static hipError_t launch_bwd(const NormParams& p, bool residual, hipStream_t stream) {
   const int blocks = norm_bwd_blocks(p.rows, p.width);
-  const hipError_t e = with_rows<T>(p.width, p.width % 8 == 0, [&](auto r) {
+  const hipError_t e = with_rows<T, true>(p.width, p.width % 8 == 0, [&](auto r) {
     using R = decltype(r);
     if (residual)
       hipLaunchKernelGGL((residual_norm_bwd_kernel<T, R>), dim3(blocks), dim3(R::THREADS), 0, stream, p);

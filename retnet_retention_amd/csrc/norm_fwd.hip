@@ -71,7 +71,7 @@ __global__ __launch_bounds__(R::THREADS) void residual_norm_fwd_kernel(NormParam
 
 template <typename T>
 static hipError_t launch_fwd(const NormParams& p, bool residual, hipStream_t stream) {
-  return with_rows<T>(p.width, p.width % 8 == 0, [&](auto r) {
+  return with_rows<T, false>(p.width, p.width % 8 == 0, [&](auto r) {
     using R = decltype(r);
     const dim3 grid((unsigned)((p.rows + R::RPB - 1) / R::RPB));
     if (residual)

@@ -33,6 +33,35 @@ struct NormRow {
       for (int j = 0; j < E; ++j) x[j] = keep && j * LPR + l < width ? (float)row[j * LPR + l] : 0.f;
     }
   }
+  // the lane's part of a row as it lies in memory, so that a row can be on its
+  // way while another is worked on
+  struct Raw { Raw8<T> v[VEC ? NV : 1]; T e[VEC ? 1 : E]; };
+  __device__ static __forceinline__ void ask(Raw& r, const T* row, int width, int l, bool keep) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = 8 * (v * LPR + l);
+        r.v[v] = Raw8<T>{};
+        if (keep && at < width) r.v[v] = ld_raw8(row + at);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) r.e[j] = keep && j * LPR + l < width ? row[j * LPR + l] : (T)0.f;
+    }
+  }
+  __device__ static __forceinline__ void take(float* x, const Raw& r) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const F8 y = unpack8(r.v[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[8 * v + e] = y.x[e];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = (float)r.e[j];
+    }
+  }
   template <typename U>
   __device__ static __forceinline__ void store(U* row, const float* x, int width, int l) {
     if constexpr (VEC) {
@@ -71,12 +100,12 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float* sh, int& turn) {
     float* at = sh + turn * 32;
     turn ^= 1;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = sum64(s[i]);
+    for (int i = 0; i < N; ++i) s[i] = sum_lanes<64>(s[i]);
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) at[wave * N + i] = s[i];
     }
-    __syncthreads();
+    lds_barrier();  // (rows on their way from memory stay so)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       s[i] = 0.f;
@@ -126,8 +155,10 @@ __device__ __forceinline__ void normalize_grad(float* g, const float* n, float r
   for (int j = 0; j < R::E; ++j) g[j] = rstd * (g[j] - b - n[j] * a);
 }
 
-// f(NormRow of the width's division) for rows of `width` elements
-template <typename T, typename F>
+// f(NormRow of the width's division) for rows of `width` elements. The backward
+// (BWD) holds a dozen rows' worth of registers, so its rows of up to 8192 are
+// spread over 512 lanes (256 registers each), not 1024 (128).
+template <typename T, bool BWD, typename F>
 hipError_t with_rows(int width, bool vec, F&& f) {
 #define RET_NORM_CASE(LIMIT, LPR, NV) \
   if (width <= LIMIT) return vec ? f(NormRow<T, LPR, NV, true>{}) : f(NormRow<T, LPR, NV, false>{});
@@ -138,7 +169,7 @@ hipError_t with_rows(int width, bool vec, F&& f) {
   RET_NORM_CASE(1024, 128, 1)
   RET_NORM_CASE(2048, 256, 1)
   RET_NORM_CASE(4096, 512, 1)
-  RET_NORM_CASE(8192, 1024, 1)
+  RET_NORM_CASE(8192, (BWD ? 512 : 1024), (BWD ? 2 : 1))
   RET_NORM_CASE(kMaxNormWidth, 1024, 2)
 #undef RET_NORM_CASE
   return hipErrorInvalidValue;
