@@ -9,7 +9,7 @@
 namespace ret {
 
 constexpr int kDeltaBlock = 64;  // tokens of a block
-constexpr int kDeltaGroup = 4;   // blocks between two fp32 copies of the state (backward)
+constexpr int kDeltaGroup = 2;   // blocks between two fp32 copies of the state (backward)
 
 // Pointers into one call's workspace and the caller's tensors. Blocks are
 // numbered over the whole batch: block i of sequence b is b * blocks_max + i,
@@ -51,6 +51,7 @@ struct DeltaLayout {
   size_t groups;
   size_t mat_plane;  // bytes of one 64 x 64 plane
   int planes;        // planes that hold an fp32 operand: 2 bf16 values, or 1 fp32
+  int mat_planes;    // the same for the backward's matrices: 3, or 1
   int slices;        // workgroups that share a head's value columns
 };
 DeltaLayout delta_layout(int batch, int seqlen, int d, int dtype, bool packed, int total);

@@ -29,13 +29,13 @@ hipError_t launch_delta_forward(const DeltaParams& p, int d, int dtype, bool gra
 template <typename T, int D>
 __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
-  constexpr int NP = Planes<T>::N, SZ = sizeof(T);
+  constexpr int NP = Planes<T>::N, NM = MatPlanes<T, true>::N, SZ = sizeof(T);
   constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
   constexpr bool kAhead = SZ == 2;  // fp32 keys do not fit the registers a block ahead
   T* const tag = nullptr;
   __shared__ __attribute__((aligned(16))) f32x4 part[4 * 512];
   __shared__ __attribute__((aligned(16))) f32x4 quarter[16 * CT * 16];
-  __shared__ __attribute__((aligned(16))) T od[OPLANE], oq[CS::OPND], ox[CS::OPND], ow[CS::OPND];
+  __shared__ __attribute__((aligned(16))) T od[OPLANE], oq[CS::OPND], ox[OPLANE * NM], ow[CS::OPND];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i(tid >> 6), w = wave & 3;
   const int id = xcd_swizzle(blockIdx.x, gridDim.x);
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
   };
   auto slot_of = [&](int blk) { return (int64_t)(base + blk) * p.heads + h; };
   auto mat_rsrc = [&](const void* x, int blk) {
-    return scalar_rsrc(reinterpret_cast<const T*>(x) + slot_of(blk) * (NP * kB * kB), blk >= 0 ? NP * kB * kB * SZ : 0);
+    return scalar_rsrc(reinterpret_cast<const T*>(x) + slot_of(blk) * (NM * kB * kB), blk >= 0 ? NM * kB * kB * SZ : 0);
   };
   auto vec_rsrc = [&](int blk) { return scalar_rsrc(p.vec + slot_of(blk) * (4 * kB), blk >= 0 ? 4 * kB * 4 : 0); };
   const uint32_t lane_off = 8 * lane * SZ;
@@ -68,13 +68,13 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) pair_off[i] = (r4 + i) * vrow + (slice * CS::SL + 2 * c) * SZ;
   const int krow = CS::KR * (w % RG), cg = w / RG, vcol = slice * CS::SL + 32 * cg + n;
-  auto load_mat = [&](frag_t<T>(&f)[NP][2], const void* x, int blk) {
+  auto load_mat = [&](frag_t<T>(&f)[2][NM], const void* x, int blk) {
     const auto rs = mat_rsrc(x, blk);
 #pragma unroll
-    for (int pl = 0; pl < NP; ++pl)
+    for (int pl = 0; pl < NM; ++pl)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks >= (w >> 1)) f[pl][ks] = buf_frag(rs, lane_off, mat_frag(pl, w, ks) * SZ, tag);  // upper triangular
+        if (ks >= (w >> 1)) f[ks][pl] = buf_frag(rs, lane_off, mat_frag(pl, w, ks) * SZ, tag);  // upper triangular
   };
   auto load_keys = [&](frag_t<T>(&f)[2][CS::KS], int blk) {
     const auto rs = key_rsrc(p.kf, blk);
@@ -115,9 +115,9 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[t][i] = si[(krow + 32 * t + state_row(i, h2)) * D + vcol];
     }
-    frag_t<T> kf[2][CS::KS], kc[TPW][4], qc[TPW][4], tf[NP][2];
+    frag_t<T> kf[2][CS::KS], kc[TPW][4], qc[TPW][4], tf[2][NM];
 #pragma unroll
-    for (int pl = 0; pl < NP; ++pl) tf[pl][0] = zero_frag<T>();
+    for (int pl = 0; pl < NM; ++pl) tf[0][pl] = zero_frag<T>();
     f32x4 eg, el;
     float last;
     auto load_rest = [&](int blk) {
@@ -186,8 +186,8 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
       // dV' of the quarter (zero behind the sequence's end: K and dO are)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        put_opnd<PITCH, OPLANE>(ox, row_of(ct, c), r4,
-                                get_partial<RG>(part, ct, 4 * w + g16, c) * el + my_quarter[16 * ct]);
+        put_opnd<PITCH, OPLANE, NM>(ox, row_of(ct, c), r4,
+                                    get_partial<RG>(part, ct, 4 * w + g16, c) * el + my_quarter[16 * ct]);
       if constexpr (kAhead) load_keys(kf, blk - 1);
       lds_barrier();
 
@@ -197,16 +197,14 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         f32x4 dv[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          frag_t<T> a[NP], x[NP];
+          frag_t<T> x[NM];
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl) {
-            a[pl] = tf[pl][ks];
+          for (int pl = 0; pl < NM; ++pl)
             x[pl] = lds_row8(ox + pl * OPLANE + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
-          }
-          dv[ks] = mma_split2(a, x, zero4(), tag);
+          dv[ks] = mma_planes(tf[ks], x, zero4());
         }
         dv[0] += dv[1];
-        put_opnd<PITCH, OPLANE>(ow, row_of(ct, c), 16 * w + quad_place(g16), -eg * dv[0]);
+        put_opnd<PITCH, OPLANE, NP>(ow, row_of(ct, c), 16 * w + quad_place(g16), -eg * dv[0]);
         my_quarter[16 * ct] = dv[0];
       }
       const float decay = last;
@@ -241,9 +239,9 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
     }
   } else {
-    frag_t<T> pf[NP][2];
+    frag_t<T> pf[2][NM];
 #pragma unroll
-    for (int pl = 0; pl < NP; ++pl) pf[pl][0] = zero_frag<T>();
+    for (int pl = 0; pl < NM; ++pl) pf[0][pl] = zero_frag<T>();
     PairOf<T> dout[CG][4], dnext[CG][4], v[CG][4], u[NP][CG][4];
     f32x4 eg;
     auto put_dout = [&](const PairOf<T>(&x)[CG][4]) {  // exact in T
@@ -275,7 +273,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         for (int ks = 0; ks < 2; ++ks) {
           const frag_t<T> d = lds_row8(od + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl) x = mma(pf[pl][ks], d, x);
+          for (int pl = NM - 1; pl >= 0; --pl) x = mma(pf[ks][pl], d, x);
         }
         my_quarter[16 * ct] = x;
       }
@@ -287,7 +285,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         f32x4 x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = p.scale * eg[i] * dout[ct >> 1][i].get(ct & 1);
-        put_opnd<PITCH, OPLANE>(oq, row_of(ct, c), 16 * w + quad_place(g16), x);
+        put_opnd<PITCH, OPLANE, NP>(oq, row_of(ct, c), 16 * w + quad_place(g16), x);
       }
       put_dout(dnext);
 #pragma unroll

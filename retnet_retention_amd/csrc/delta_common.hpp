@@ -44,16 +44,23 @@ __device__ __forceinline__ Split<float> split_acc(const f32x16& c, float*) {
   return s;
 }
 
-// a * b with the products of two roundings' rests left out (2^-18)
-template <typename A, typename B, typename C>
-__device__ __forceinline__ C mma_split2(const A* a, const B* b, C c, bf16*) {
-  c = mma(a[0], b[1], c);
-  c = mma(a[1], b[0], c);
-  return mma(a[0], b[0], c);
-}
-template <typename A, typename B, typename C>
-__device__ __forceinline__ C mma_split2(const A* a, const B* b, C c, float*) {
-  return mma(a[0], b[0], c);
+// The 64 x 64 matrices T, M and P and what they multiply (X, dV') pass every
+// value on: their roundings outweigh the others' in the decays' gradients, which
+// are differences of row sums. The backward takes three values for these (24
+// bits); with two, d log decay was up to 6e-5 off where three give 6e-6.
+template <typename T, bool GRAD> struct MatPlanes {
+  static constexpr int N = sizeof(T) == 4 ? 1 : GRAD ? 3 : 2;
+};
+
+// a * b, both in planes: products of rests smaller than 2^-24 are left out
+template <int NA, int NB, typename F>
+__device__ __forceinline__ f32x4 mma_planes(const F (&a)[NA], const F (&b)[NB], f32x4 c) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j <= 2) c = mma(a[i], b[j], c);
+  return c;
 }
 
 // the key column within 32 of position n in that order
@@ -212,19 +219,21 @@ __device__ __forceinline__ f32x4 get_partial(const f32x4* buf, int ct, int quad,
   return s;
 }
 
-// Four tokens' values of one column into an operand copy, in planes.
-template <int PITCH, int OPLANE>
-__device__ __forceinline__ void put_opnd(bf16* m, int row, int at, const f32x4& x) {
-  bf16x4 hi, lo;
+// Four tokens' values of one column into an operand copy, in N planes.
+template <int PITCH, int OPLANE, int N>
+__device__ __forceinline__ void put_opnd(bf16* m, int row, int at, f32x4 x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = (bf16)x[i];
-    lo[i] = (bf16)(x[i] - (float)hi[i]);
+  for (int pl = 0; pl < N; ++pl) {
+    bf16x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = (bf16)x[i];
+      x[i] -= (float)y[i];
+    }
+    *reinterpret_cast<bf16x4*>(m + pl * OPLANE + row * PITCH + at) = y;
   }
-  *reinterpret_cast<bf16x4*>(m + row * PITCH + at) = hi;
-  *reinterpret_cast<bf16x4*>(m + OPLANE + row * PITCH + at) = lo;
 }
-template <int PITCH, int OPLANE>
+template <int PITCH, int OPLANE, int N>
 __device__ __forceinline__ void put_opnd(float* m, int row, int at, const f32x4& x) {
   *reinterpret_cast<f32x4*>(m + row * PITCH + at) = x;
 }

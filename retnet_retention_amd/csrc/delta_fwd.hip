@@ -280,17 +280,17 @@ __global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaParams p) {
         block(3, 3);
       }
     }
-    constexpr int NP = Planes<T>::N;
-    store_matrix<T, false>(st, reinterpret_cast<T*>(p.t) + slot * (NP * kB * kB), NP, tid);
+    constexpr int NM = MatPlanes<T, GRAD>::N;
+    store_matrix<T, false>(st, reinterpret_cast<T*>(p.t) + slot * (NM * kB * kB), NM, tid);
     if constexpr (GRAD) {
-      store_matrix<T, true>(st, reinterpret_cast<T*>(p.tt) + slot * (NP * kB * kB), NP, tid);
-      store_matrix<T, true>(sp, reinterpret_cast<T*>(p.pt) + slot * (NP * kB * kB), NP, tid);
+      store_matrix<T, true>(st, reinterpret_cast<T*>(p.tt) + slot * (NM * kB * kB), NM, tid);
+      store_matrix<T, true>(sp, reinterpret_cast<T*>(p.pt) + slot * (NM * kB * kB), NM, tid);
     }
     __syncthreads();
     // the forward's outputs are of type T: one plane of M (an error of 2^-9 of
     // the rounding that the output itself takes); the backward's row sums are
-    // fp32 and take both
-    constexpr int MP = GRAD ? NP : 1;
+    // fp32 and take all
+    constexpr int MP = GRAD ? NM : 1;
     store_matrix<T, false>(sa, reinterpret_cast<T*>(p.m) + slot * (MP * kB * kB), MP, tid);
   }
 }
@@ -313,6 +313,7 @@ template <typename T, int D, bool GRAD>
 __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
   constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1, SZ = sizeof(T);
+  constexpr int NM = MatPlanes<T, GRAD>::N, MP = GRAD ? NM : 1;
   constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
   // Two copies of the state let Q S wait until the state waves are back at
   // their products; fp32 has no room for the second and takes it between.
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
   constexpr int COPY = CS::SPLANE * PP;
   T* const tag = nullptr;
   __shared__ __attribute__((aligned(16))) f32x4 part[4 * 512];
-  __shared__ __attribute__((aligned(16))) T ox[CS::OPND], ow[CS::OPND], ov[GRAD ? CS::OPND : 16];
+  __shared__ __attribute__((aligned(16))) T ox[OPLANE * NM], ow[CS::OPND], ov[GRAD ? CS::OPND : 16];
   __shared__ __attribute__((aligned(16))) T os[COPY * (kTwoCopies ? 2 : 1)];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i(tid >> 6), w = wave & 3;
@@ -372,9 +373,9 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
     }
     T* my_os = os + (32 * cg + col_place(n)) * CS::SPITCH + krow + 8 * h2;
 
-    frag_t<T> kf[2][CS::KS], kc[TPW][4], tf[NP][2];
+    frag_t<T> kf[2][CS::KS], kc[TPW][4], tf[2][NM];
 #pragma unroll
-    for (int pl = 0; pl < NP; ++pl) tf[pl][1] = zero_frag<T>();
+    for (int pl = 0; pl < NM; ++pl) tf[1][pl] = zero_frag<T>();
     PairOf<T> v[CG][4];
     f32x4 eg, el;
     float last;
@@ -396,12 +397,12 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
       eg = buf_f4(vec_rsrc(blk), r4 * 4, 0);
     };
     auto load_rest = [&](int blk) {  // what V' takes
-      const auto tr = mat_rsrc(p.t, NP, blk);
+      const auto tr = mat_rsrc(p.t, NM, blk);
 #pragma unroll
-      for (int pl = 0; pl < NP; ++pl)
+      for (int pl = 0; pl < NM; ++pl)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks <= (w >> 1)) tf[pl][ks] = buf_frag(tr, lane_off, mat_frag(pl, w, ks) * SZ, tag);  // lower triangular
+          if (ks <= (w >> 1)) tf[ks][pl] = buf_frag(tr, lane_off, mat_frag(pl, w, ks) * SZ, tag);  // lower triangular
       const auto er = vec_rsrc(blk);
       el = buf_f4(er, r4 * 4, kB * 4);
       last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(er, 0, (kB - 1) * 4, 0));
@@ -468,7 +469,7 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
         f32x4 x = -eg * get_partial<RG>(part, ct, 4 * w + g16, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] += v[ct >> 1][i].get(ct & 1);
-        put_opnd<PITCH, OPLANE>(ox, row_of(ct, c), r4, x);
+        put_opnd<PITCH, OPLANE, NM>(ox, row_of(ct, c), r4, x);
       }
       if constexpr (kAhead) load_keys(blk + 1, 0);
       load_values(blk + 1);
@@ -480,17 +481,15 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
         f32x4 u[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          frag_t<T> a[NP], x[NP];
+          frag_t<T> x[NM];
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl) {
-            a[pl] = tf[pl][ks];
+          for (int pl = 0; pl < NM; ++pl)
             x[pl] = lds_row8(ox + pl * OPLANE + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
-          }
-          u[ks] = mma_split2(a, x, zero4(), tag);
+          u[ks] = mma_planes(tf[ks], x, zero4());
         }
         u[0] += u[1];
-        put_opnd<PITCH, OPLANE>(ow, row_of(ct, c), 16 * w + quad_place(g16), u[0] * el);
-        if constexpr (GRAD) put_opnd<PITCH, OPLANE>(ov, row_of(ct, c), r4, u[0]);
+        put_opnd<PITCH, OPLANE, NP>(ow, row_of(ct, c), 16 * w + quad_place(g16), u[0] * el);
+        if constexpr (GRAD) put_opnd<PITCH, OPLANE, NP>(ov, row_of(ct, c), r4, u[0]);
       }
       const float decay = last;
       if constexpr (kAhead) {
@@ -538,9 +537,9 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
       }
     }
   } else {
-    frag_t<T> qf[D / 32], mf[PP][2];
+    frag_t<T> qf[D / 32], mf[2][MP];
 #pragma unroll
-    for (int pl = 0; pl < PP; ++pl) mf[pl][1] = zero_frag<T>();
+    for (int pl = 0; pl < MP; ++pl) mf[1][pl] = zero_frag<T>();
     PairOf<T> dout[CG][4];
     f32x4 eg;
     auto load_queries = [&](int blk) {
@@ -549,12 +548,12 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
       for (int ks = 0; ks < D / 32; ++ks) qf[ks] = buf_frag(rs, lane_off, query_frag<D>(w, ks) * SZ, tag);
     };
     auto load_rest = [&](int blk) {
-      const auto mr = mat_rsrc(p.m, PP, blk);
+      const auto mr = mat_rsrc(p.m, MP, blk);
 #pragma unroll
-      for (int pl = 0; pl < PP; ++pl)
+      for (int pl = 0; pl < MP; ++pl)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks <= (w >> 1)) mf[pl][ks] = buf_frag(mr, lane_off, mat_frag(pl, w, ks) * SZ, tag);
+          if (ks <= (w >> 1)) mf[ks][pl] = buf_frag(mr, lane_off, mat_frag(pl, w, ks) * SZ, tag);
       eg = buf_f4(vec_rsrc(blk), r4 * 4, 0);
       if constexpr (GRAD) {
         const auto dr = value_rsrc(p.dout, blk);
@@ -599,18 +598,10 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
         o[ct] *= in;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          frag_t<T> x[NP];
+          frag_t<T> x[NM];
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl) x[pl] = lds_row8(ox + pl * OPLANE + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
-          if constexpr (GRAD) {
-            frag_t<T> a[NP];
-#pragma unroll
-            for (int pl = 0; pl < NP; ++pl) a[pl] = mf[pl][ks];
-            o[ct] = mma_split2(a, x, o[ct], tag);
-          } else {
-#pragma unroll
-            for (int pl = 0; pl < NP; ++pl) o[ct] = mma(mf[0][ks], x[pl], o[ct]);
-          }
+          for (int pl = 0; pl < NM; ++pl) x[pl] = lds_row8(ox + pl * OPLANE + row_of(ct, c) * PITCH + 32 * ks + 8 * g16);
+          o[ct] = mma_planes(mf[ks], x, o[ct]);
         }
       }
       if constexpr (!GRAD) {
@@ -689,6 +680,7 @@ template <typename T, int D>
 static void chain_layout(DeltaLayout& l) {
   l.slices = ChainShape<T, D>::NSL;
   l.planes = Planes<T>::N;
+  l.mat_planes = MatPlanes<T, true>::N;
   l.mat_plane = kB * kB * sizeof(T);
 }
 
