@@ -382,3 +382,41 @@ def test_binding_refusals():
         rr.delta_recurrent_step(*a, x["s0"])
     with pytest.raises(TypeError):
         rr.delta_chunkwise_fwd(*(t.half() if i < 3 else t for i, t in enumerate(a)))
+
+
+def test_offsets_past_32_bits():
+    """The last of two packed sequences starts behind 2^31 elements of v: the
+    same bits as that sequence alone."""
+    h, d, first, last = 128, 256, 66000, 100
+    g = torch.Generator(device=DEV).manual_seed(3)
+    n = first + last
+    assert first * h * d > 2 ** 31
+    v = torch.randn(n, h, d, generator=g, device=DEV, dtype=torch.bfloat16)
+    k = torch.randn(n, 1, d, generator=g, device=DEV, dtype=torch.bfloat16) / 16
+    ld = -torch.rand(n, h, generator=g, device=DEV)
+    beta = torch.rand(n, h, generator=g, device=DEV)
+    cu = torch.tensor([0, first, n], dtype=torch.int32, device=DEV)
+    s = torch.empty(2, h, d, d, device=DEV)
+    o = rr.delta_chunkwise_fwd(k, k, v, ld, beta, state_out=s, cu_seqlens=cu, max_seqlen=first, check=True)
+    tail = [t[first:][None].contiguous() for t in (k, k, v, ld, beta)]
+    s1 = torch.empty(1, h, d, d, device=DEV)
+    o1 = rr.delta_chunkwise_fwd(*tail, state_out=s1)
+    assert torch.equal(o[first:], o1[0]) and torch.equal(s[1], s1[0])
+    assert torch.isfinite(o[first - 64:first].float()).all()
+
+
+def test_single_tokens_and_masked_batches():
+    """One token a sequence, without and with a state; a batch whose padding
+    has beta 0 and no decay leaves each state where its last real token did."""
+    x = make(16, 3, 1, 1, 2, 64, "f32")
+    y = dev(x)
+    got = rr.delta_chunkwise_bwd(*(y[k] for k in ("q", "k", "v", "g", "beta", "dout")))
+    assert (got[3] == 0).all()  # a first token's decay acts on nothing
+    x = make(17, 2, 130, 1, 2, 64, "f32")
+    x["beta"][0, 50:], x["g"][0, 50:] = 0.0, 0.0
+    y = dev(x)
+    _, s = forward(y, 1.0)
+    short = {k: (t[:1, :50].contiguous() if t.dim() > 2 and k not in ("s0", "ds") else t[:1]) for k, t in y.items()}
+    _, s50 = forward(short, 1.0)
+    # the same products in another order of decays (factors of exactly 1)
+    close(s[0], f64(s50[0]), bars("f32", 64)[1], "state", 2)

@@ -220,3 +220,17 @@ def test_binding_refusals():
         rr.head_norm_fwd(t["x"], eps=0.0)
     with pytest.raises(TypeError):
         rr.head_norm_fwd(t["x"].half())
+
+
+def test_offsets_past_32_bits():
+    """Rows behind 2^31 elements: the same bits as those rows alone."""
+    rows, width = 131200, 16384
+    assert (rows - 64) * width > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(rows, width, generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.ones(width, device=DEV)
+    out, res = rr.residual_norm_fwd(x, x, w)
+    o2, r2 = rr.residual_norm_fwd(x[-64:].contiguous(), x[-64:].contiguous(), w)
+    assert torch.equal(out[-64:], o2) and torch.equal(res[-64:], r2)
+    y = rr.head_norm_fwd(x, w)
+    assert torch.equal(y[-64:], rr.head_norm_fwd(x[-64:].contiguous(), w))
