@@ -304,12 +304,14 @@ ret_status_t retention_chunkwise_error(const void *workspace, size_t workspace_b
  * it from these workspaces too). With cu_seqlens NULL total_tokens is ignored.
  *
  * Supported: dk == dv in {64, 128, 256}; fp32 or bf16; v_heads <= 128 and a
- * multiple of k_heads; at most 2^31 - 1 tokens. bf16 tensors are multiplied on
+ * multiple of k_heads; at most 2^31 - 1 tokens, batch * v_heads < 2^20 and
+ * batch * ceil(seqlen / 64) < 2^23. bf16 tensors are multiplied on
  * the matrix cores as they are; what the recurrence carries (state, written
  * values) enters the products as the sum of two bf16 values, so that the fp32
  * states and gradients a call returns are good to a few 1e-6. A NaN or
  * infinity in a token reaches no other sequence and no output of an earlier
- * block of 64 tokens.
+ * block of 64 tokens. A batch may be padded with tokens of log_decay 0 and
+ * beta 0, which leave the state as it is, if their keys and values are finite.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t batch;    /* >= 1: sequences                                         */
@@ -325,7 +327,8 @@ typedef struct {
  * carried from block to block. state_in NULL: zeros; state_out NULL: not
  * written; state_out == state_in is allowed. The two forms of the recurrence
  * are those of the retention calls ("Summary": parallel inside a chunk, the
- * recurrent state passed between chunks). */
+ * recurrent state passed between chunks). Workspace: per 64 tokens two 64 x 64
+ * matrices a value head, three copies of the keys or queries a key head. */
 size_t retention_delta_workspace_bytes(const ret_delta_desc_t *desc, int32_t packed, int64_t total_tokens);
 ret_status_t retention_delta_fwd(const ret_delta_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
                                  const void *q, const void *k, const void *v, const float *log_decay,
@@ -336,8 +339,11 @@ ret_status_t retention_delta_fwd(const ret_delta_desc_t *desc, const int32_t *cu
  * term only when d_state_out is given) with respect to q, k, v, log_decay,
  * beta and state_in (d_state_in non-NULL exactly when state_in is). Key heads
  * that several value heads share receive the sum. The forward's walk is run
- * again; its states take workspace: per 64 tokens and value head four times
- * dk dv elements of the dtype, and a quarter of dk dv fp32. */
+ * again; what the gradients need of it takes workspace: per 64 tokens and
+ * value head two states of dk dv elements of the dtype and half a state of
+ * dk dv fp32 (at dk 256 in bf16 384 KiB), four 64 x 64 matrices (96 KiB in
+ * bf16, 64 KiB in fp32) and v twice (bf16) or once (fp32). A log_decay whose
+ * factor is 0 in 32 bits has gradient 0. */
 size_t retention_delta_bwd_workspace_bytes(const ret_delta_desc_t *desc, int32_t packed, int64_t total_tokens);
 ret_status_t retention_delta_bwd(const ret_delta_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
                                  const void *q, const void *k, const void *v, const float *log_decay,

@@ -18,9 +18,11 @@ ret_status_t check_delta(const ret_delta_desc_t* d, bool packed, int64_t total) 
   if (d->batch < 1 || d->seqlen < 1 || d->k_heads < 1 || d->v_heads < 1 || d->v_heads > kMaxHeads ||
       d->v_heads % d->k_heads != 0)
     return RET_ERR_SHAPE;
-  // rows are numbered with 32 bits, and so is every launch grid
+  // rows are numbered with 32 bits, and so are the threads of a launch: 512 for
+  // each of a head's (up to 8) slices, or for each block of 64 tokens
   const int64_t tokens = (int64_t)d->batch * d->seqlen;
-  if (tokens > INT32_MAX || (int64_t)d->batch * d->v_heads * 8 > INT32_MAX) return RET_ERR_SHAPE;
+  const int64_t blocks = (int64_t)d->batch * ((d->seqlen + (int64_t)ret::kDeltaBlock - 1) / ret::kDeltaBlock);
+  if (tokens > INT32_MAX || (int64_t)d->batch * d->v_heads >= 1 << 20 || blocks >= 1 << 23) return RET_ERR_SHAPE;
   if (packed && (total < 0 || total > tokens)) return RET_ERR_SHAPE;
   if (d->dtype != RET_F32 && d->dtype != RET_BF16) return RET_ERR_UNSUPPORTED;
   if (d->dk != d->dv || (d->dk != 64 && d->dk != 128 && d->dk != 256)) return RET_ERR_UNSUPPORTED;

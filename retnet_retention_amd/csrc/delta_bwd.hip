@@ -574,9 +574,10 @@ __global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int 
     const int r = blk * kB + lane;
     if (r < len) {
       const int64_t at = (tok0 + r) * p.heads + h;
-      // with no state before it the first token's decay acts on nothing: the
-      // sum over the whole sequence is zero but for its rounding
-      p.d_log_decay[at] = r == 0 && !p.state_in ? 0.f : d;
+      // The gradient is the factor exp(log decay) times what the state before it
+      // gives: zero where that is zero. The sum would be its own rounding there.
+      const bool none = (r == 0 && !p.state_in) || p.log_decay[at] < kZeroLogDecay;
+      p.d_log_decay[at] = none ? 0.f : d;
       const float beta = p.vec[slot * (4 * kB) + 2 * kB + lane];
       p.d_beta[at] = x / beta / beta;
     }

@@ -11,6 +11,7 @@ constexpr int kB = kDeltaBlock;
 // Logarithmic decays below this are a reset (exp gives 0 either way); the
 // bound keeps differences of sums finite.
 constexpr float kMinLogDecay = -1e5f;
+constexpr float kZeroLogDecay = -104.f;  // exp of less is 0 in 32 bits (2^-149 = exp(-103.3))
 
 // An fp32 operand of the matrix cores: for bf16 tensors as the sum of two
 // bf16 values (the rounded value and the rounded rest, together 16 bits or
@@ -106,13 +107,6 @@ __device__ __forceinline__ constexpr int column_frag(int tile, int ks) { return 
 template <int D>
 __device__ __forceinline__ constexpr int query_frag(int rb, int ks) { return (rb * (D / 32) + ks) * kFrag; }
 __device__ __forceinline__ constexpr int mat_frag(int plane, int rb, int ks) { return ((plane * 4 + rb) * 2 + ks) * kFrag; }
-
-// 8 consecutive elements of global memory as a fragment, zero unless `keep`
-template <typename T>
-__device__ __forceinline__ frag_t<T> global_row8(const T* p, bool keep) {
-  if (!keep) return zero_frag<T>();
-  return __builtin_bit_cast(frag_t<T>, *reinterpret_cast<const frag_t<T>*>(p));
-}
 
 // Rows of sequence b (clamped into the tensors for packed bounds) and the
 // number of its first block over the batch.

@@ -26,7 +26,8 @@ template <typename T, bool TRANS>
 __device__ __forceinline__ void store_matrix(const float (*m)[kPrepPitch], T* out, int planes, int tid) {
   const int lane = tid & 63;
 #pragma unroll
-  for (int f = tid >> 6; f < 8; f += 4) {
+  for (int i = 0; i < 2; ++i) {
+    const int f = (tid >> 6) + 4 * i;
     const int r = 16 * (f >> 1) + (lane & 15), c = 32 * (f & 1) + 8 * (lane >> 4);
     F8 x, y;
     if constexpr (TRANS) {
@@ -55,7 +56,7 @@ __device__ __forceinline__ void store_matrix(const float (*m)[kPrepPitch], T* ou
 // bits: E is the exponential of a difference of two sums that may both be
 // large.
 template <typename T, int D, bool GRAD>
-__global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaParams p) {
+__global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_prep_kernel(DeltaParams p) {
   constexpr int HALF = D < 128 ? D : 128;  // columns staged at a time
   constexpr int SP = HALF + 16 / (int)sizeof(T);
   struct Stage { T k[kB][SP], q[kB][SP]; };
@@ -146,9 +147,11 @@ __global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaParams p) {
       else if (w == 2) products(std::integral_constant<int, 3>{});
       else products(std::integral_constant<int, 4>{});
 #pragma unroll
-      for (int f = w; f < 2 * (HALF / 16); f += 4)
+      for (int i = 0; i < HALF / 32; ++i) {
+        const int f = w + 4 * i;
         *reinterpret_cast<frag_t<T>*>(KF + key_frag(c0 / 16 + f / 2, f & 1)) =
             lds_row8(&sh.st.k[32 * (f & 1) + (lane & 31)][16 * (f / 2) + 8 * (lane >> 5)]);
+      }
 #pragma unroll
       for (int t = 0; t < HALF / 32; ++t) {
         *reinterpret_cast<frag_t<T>*>(KC + column_frag(c0 / 32 + t, w)) =

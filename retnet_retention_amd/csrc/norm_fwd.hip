@@ -10,12 +10,20 @@
 
 namespace ret {
 
+// A launch's threads along one axis are counted in 32 bits: workgroups in
+// lines of 2^21 (at most 1024 threads each).
+constexpr int kGridLine = 1 << 21;
+template <typename R>
+__device__ __forceinline__ int64_t first_row() {
+  return ((int64_t)blockIdx.y * kGridLine + blockIdx.x) * R::RPB;
+}
+
 template <typename T, typename R>
 __global__ __launch_bounds__(R::THREADS) void head_norm_fwd_kernel(NormParams p) {
   __shared__ float sh[64];
   int turn = 0;
   const int l = threadIdx.x % R::LPR;
-  const int64_t row = (int64_t)blockIdx.x * R::RPB + threadIdx.x / R::LPR;
+  const int64_t row = first_row<R>() + threadIdx.x / R::LPR;
   const bool keep = row < p.rows;
   const int64_t at = row * p.width;
   float x[R::E], y[R::E];
@@ -39,7 +47,7 @@ __global__ __launch_bounds__(R::THREADS) void residual_norm_fwd_kernel(NormParam
   __shared__ float sh[64];
   int turn = 0;
   const int l = threadIdx.x % R::LPR;
-  const int64_t row = (int64_t)blockIdx.x * R::RPB + threadIdx.x / R::LPR;
+  const int64_t row = first_row<R>() + threadIdx.x / R::LPR;
   const bool keep = row < p.rows;
   const int64_t at = row * p.width;
   float x[R::E], z[R::E], w[R::E];
@@ -73,7 +81,9 @@ template <typename T>
 static hipError_t launch_fwd(const NormParams& p, bool residual, hipStream_t stream) {
   return with_rows<T, false>(p.width, p.width % 8 == 0, [&](auto r) {
     using R = decltype(r);
-    const dim3 grid((unsigned)((p.rows + R::RPB - 1) / R::RPB));
+    const int64_t blocks = (p.rows + R::RPB - 1) / R::RPB;
+    const dim3 grid((unsigned)(blocks < kGridLine ? blocks : kGridLine),
+                    (unsigned)((blocks + kGridLine - 1) / kGridLine));
     if (residual)
       hipLaunchKernelGGL((residual_norm_fwd_kernel<T, R>), grid, dim3(R::THREADS), 0, stream, p);
     else

@@ -196,3 +196,13 @@ def test_block_numbers_of_packed_sequences_never_meet():
         assert len(set(blocks)) == len(blocks) and len(set(groups)) == len(groups)
         total = cu[-1] // 64 + len(lens)
         assert all(0 <= i < total for i in blocks) and all(0 <= g < total // 4 + len(lens) + 1 for g in groups)
+
+
+@pytest.mark.parametrize("kw", [dict(batch=2**18, seqlen=1, k_heads=1, v_heads=4),
+                                dict(batch=2**20, seqlen=512, k_heads=1, v_heads=1)])
+def test_more_threads_than_a_launch_counts(L, kw):
+    d = _desc(**kw)
+    assert _fwd(L, d) == 2 and _bwd(L, d) == 2
+    assert L.retention_delta_workspace_bytes(ctypes.byref(d), 0, 0) == 0
+    kw["batch"] -= 1 + kw["batch"] // 2**10
+    assert L.retention_delta_workspace_bytes(ctypes.byref(_desc(**kw)), 0, 0) > 0

@@ -420,3 +420,22 @@ def test_single_tokens_and_masked_batches():
     _, s50 = forward(short, 1.0)
     # the same products in another order of decays (factors of exactly 1)
     close(s[0], f64(s50[0]), bars("f32", 64)[1], "state", 2)
+
+
+def test_gradient_of_a_reset_is_zero():
+    """A factor that is 0 passes no gradient on, -infinity or not, in a block's
+    middle and at its start; the others' gradients are the formula's."""
+    x = make(18, 2, 200, 1, 2, 64, "f32")
+    at = [0, 33, 64, 150]
+    x["g"][:, at[:3]], x["g"][:, at[3]] = -np.inf, -150.0
+    y = dev(x)
+    names = ("q", "k", "v", "g", "beta", "dout")
+    got = rr.delta_chunkwise_bwd(*(y[k] for k in names), state_in=y["s0"], d_state_out=y["ds"])
+    assert (got[3][:, at] == 0).all() and torch.isfinite(got[3]).all()
+    # the formula's, with a finite log decay whose factor is 0 in 64 bits too
+    x["g"][:, at] = -1000.0
+    ref = oracle.delta_grad(*(f64(x[k]) for k in names), state=f64(x["s0"]), d_state=f64(x["ds"]))
+    assert (ref[3][:, at] == 0).all()
+    bar = bars("f32", 64)[2]
+    for what, a, r in zip(("dq", "dk", "dv", "dlog_decay", "dbeta", "d_state_in"), got, ref):
+        close(a, r, bar, what, 2)

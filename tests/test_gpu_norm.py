@@ -234,3 +234,12 @@ def test_offsets_past_32_bits():
     assert torch.equal(out[-64:], o2) and torch.equal(res[-64:], r2)
     y = rr.head_norm_fwd(x, w)
     assert torch.equal(y[-64:], rr.head_norm_fwd(x[-64:].contiguous(), w))
+
+
+def test_more_rows_than_one_line_of_workgroups():
+    """2^29 rows of one value take 2^32 lanes: the same bits as those rows alone."""
+    rows = 2 ** 29 + 100
+    x = torch.randn(rows, 1, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV, dtype=torch.bfloat16)
+    y = rr.head_norm_fwd(x)
+    for at in (0, 2 ** 26 - 64, 2 ** 29 - 64, rows - 128):
+        assert torch.equal(y[at:at + 128], rr.head_norm_fwd(x[at:at + 128].clone())), at
