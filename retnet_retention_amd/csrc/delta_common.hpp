@@ -17,8 +17,9 @@ constexpr float kZeroLogDecay = -104.f;  // exp of less is 0 in 32 bits (2^-149 
 // bf16 values (the rounded value and the rounded rest, together 16 bits or
 // more), for fp32 tensors as it is. The state, the inverse T and the written
 // values V' feed each other from block to block, so one bf16 rounding each
-// (2^-9) would reach the fp32 state a call returns; with the rest the state
-// is within a few 1e-6.
+// (2^-9) would reach the fp32 state a call returns; with the rest (2^-18 a
+// product) the state is within 5e-6 over 8192 tokens. A third value
+// would cost half as many products again on the way from block to block.
 template <typename T> struct Planes;
 template <> struct Planes<bf16> { static constexpr int N = 2; };
 template <> struct Planes<float> { static constexpr int N = 1; };

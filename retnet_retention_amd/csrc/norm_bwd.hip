@@ -4,7 +4,10 @@
 // the weights' gradients are sums over all rows: a workgroup sums its rows in
 // registers, writes one row of sums, and a second launch adds these up in a
 // fixed order. Everything the forward formed is formed again from its inputs,
-// so one pass reads each tensor once.
+// so one pass reads each tensor once, the next row on its way while one is
+// worked on. Head norm: 36 + 5 us for 8192 tokens of 10 heads of 256, bf16 (210
+// MB: 5.1 TB/s with the column sums); residual norm: 163 us for 16384 rows of 4096
+// with all weights (805 MB: 4.9 TB/s).
 #include "norm_rows.hpp"
 
 namespace ret {
