@@ -439,3 +439,31 @@ def test_gradient_of_a_reset_is_zero():
     bar = bars("f32", 64)[2]
     for what, a, r in zip(("dq", "dk", "dv", "dlog_decay", "dbeta", "d_state_in"), got, ref):
         close(a, r, bar, what, 2)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own tensors: the bits of calls in turn."""
+    sets = [dev(make(20 + i, 2, 300, 2, 4, 128, "bf16")) for i in range(2)]
+    names = ("q", "k", "v", "g", "beta")
+    w = torch.ones(128, device=DEV)
+
+    def run(y):
+        s = y["s0"].clone()
+        o = rr.delta_chunkwise_fwd(*(y[k] for k in names), state_in=s, state_out=s)
+        n = rr.head_norm_fwd(o, w, y["v"], center=True)
+        dx, dw, dg = rr.head_norm_bwd(o, y["dout"], w, y["v"], center=True)
+        grads = rr.delta_chunkwise_bwd(*(y[k] for k in names), dx, state_in=y["s0"], d_state_out=y["ds"])
+        return (o, s, n, dx, dw, dg, *grads)
+
+    ref = [run(y) for y in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(run(sets[i]))
+    torch.cuda.synchronize()
+    for r, runs in zip(ref, got):
+        for g in runs:
+            assert all(torch.equal(a, b) for a, b in zip(r, g))
