@@ -60,11 +60,11 @@ struct Carve {
 };
 
 // control block | T | M | decay vectors | keys and queries in the lanes' order
-void carve_fwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d, int t_planes, int m_planes) {
+void carve_fwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d, int planes) {
   const size_t n = l.blocks * d->v_heads;
   c.part(p.ctrl, 2 * sizeof(int32_t));
-  c.part(p.t, n * t_planes * l.mat_plane);
-  c.part(p.m, n * m_planes * l.mat_plane);
+  c.part(p.t, n * planes * l.mat_plane);
+  c.part(p.m, n * planes * l.mat_plane);
   c.part(p.vec, n * 4 * ret::kDeltaBlock * sizeof(float));
   const size_t keys = l.blocks * d->k_heads * ret::kDeltaBlock * d->dk * elem_size(d->dtype);
   c.part(p.kf, keys);
@@ -72,10 +72,10 @@ void carve_fwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_d
   c.part(p.qf, keys);
 }
 
-// the forward's parts (all planes of M) | queries by columns | T^T | P^T | states | gradients of
+// the forward's parts | queries by columns | T^T | P^T | states | gradients of
 // states | fp32 states of the groups | V' | row sums
 void carve_bwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d, const Sizes& s) {
-  carve_fwd(c, p, l, d, l.mat_planes, l.mat_planes);
+  carve_fwd(c, p, l, d, l.mat_planes);
   const size_t n = l.blocks * d->v_heads, dd = (size_t)d->dk * d->dv;
   c.part(p.qc, l.blocks * d->k_heads * ret::kDeltaBlock * d->dk * elem_size(d->dtype));
   c.part(p.tt, n * l.mat_planes * l.mat_plane);
@@ -99,7 +99,7 @@ size_t workspace_bytes_of(const ret_delta_desc_t* d, bool packed, int64_t total,
   if (grad)
     carve_bwd(c, p, l, d, sizes_of(d, packed, total));
   else
-    carve_fwd(c, p, l, d, l.planes, 1);
+    carve_fwd(c, p, l, d, l.planes);
   return c.used;
 }
 
@@ -160,7 +160,7 @@ ret_status_t retention_delta_fwd(const ret_delta_desc_t* desc, const int32_t* cu
   p.state_out = state_out;
   Carve c{static_cast<char*>(workspace)};
   const DeltaLayout l = layout_of(desc, packed, total_tokens);
-  carve_fwd(c, p, l, desc, l.planes, 1);
+  carve_fwd(c, p, l, desc, l.planes);
   return ret::launch_delta_fwd(p, desc->dk, desc->dtype, stream) == hipSuccess ? RET_OK : RET_ERR_HIP;
 }
 

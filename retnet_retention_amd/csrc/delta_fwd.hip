@@ -294,11 +294,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
       store_matrix<T, true>(sp, reinterpret_cast<T*>(p.pt) + slot * (NM * kB * kB), NM, tid);
     }
     __syncthreads();
-    // the forward's outputs are of type T: one plane of M (an error of 2^-9 of
-    // the rounding that the output itself takes); the backward's row sums are
-    // fp32 and take all
-    constexpr int MP = GRAD ? NM : 1;
-    store_matrix<T, false>(sa, reinterpret_cast<T*>(p.m) + slot * (MP * kB * kB), MP, tid);
+    // all planes of M, as of T: with one, its rounding (2^-9) and that of a state
+    // copied in one plane put o 2.4e-3 off where its own rounding gives 1.7e-3;
+    // with two o is at its rounding, for 6% of the call (519 -> 552 us for 2 x 8192
+    // tokens, 16 heads of 256)
+    store_matrix<T, false>(sa, reinterpret_cast<T*>(p.m) + slot * (NM * kB * kB), NM, tid);
   }
 }
 
@@ -326,14 +326,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
 template <typename T, int D, bool GRAD>
 __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_kernel(DeltaParams p) {
   using CS = ChainShape<T, D>;
-  constexpr int NP = Planes<T>::N, PP = GRAD ? NP : 1, SZ = sizeof(T);
-  constexpr int NM = MatPlanes<T, GRAD>::N, MP = GRAD ? NM : 1;
+  constexpr int NP = Planes<T>::N, SZ = sizeof(T);
+  constexpr int NM = MatPlanes<T, GRAD>::N;
   constexpr int RG = CS::RG, TPW = CS::TPW, CT = CS::CT, CG = CS::CG, PITCH = CS::PITCH, OPLANE = CS::OPLANE;
   // Two copies of the state let Q S wait until the state waves are back at
-  // their products; fp32 has no room for the second and takes it between.
-  constexpr bool kTwoCopies = SZ == 2;
+  // their products. fp32 has no room for the second, nor have two workgroups of
+  // 128 columns a CU: they take Q S between the first two exchanges.
+  constexpr bool kTwoCopies = SZ == 2 && !(D == 128 && !GRAD);
   constexpr bool kAhead = SZ == 2;  // fp32 keys do not fit the registers a block ahead
-  constexpr int COPY = CS::SPLANE * PP;
+  constexpr int COPY = CS::SPLANE * NP;
   T* const tag = nullptr;
   __shared__ __attribute__((aligned(16))) f32x4 part[4 * 512];
   __shared__ __attribute__((aligned(16))) T ox[OPLANE * NM], ow[CS::OPND], ov[GRAD ? CS::OPND : 16];
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
             load_column(columns, t, 2 * SLI + 1);
           }
 #pragma unroll
-          for (int pl = 0; pl < PP; ++pl)
+          for (int pl = 0; pl < NP; ++pl)
             *reinterpret_cast<frag_t<T>*>(copy + pl * CS::SPLANE + 16 * ks) = f[ks].f[pl];
         });
       if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
@@ -551,9 +552,9 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
       }
     }
   } else {
-    frag_t<T> qf[D / 32], mf[2][MP];
+    frag_t<T> qf[D / 32], mf[2][NM];
 #pragma unroll
-    for (int pl = 0; pl < MP; ++pl) mf[1][pl] = zero_frag<T>();
+    for (int pl = 0; pl < NM; ++pl) mf[1][pl] = zero_frag<T>();
     PairOf<T> dout[CG][4];
     f32x4 eg;
     auto load_queries = [&](int blk) {
@@ -562,9 +563,9 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
       for (int ks = 0; ks < D / 32; ++ks) qf[ks] = buf_frag(rs, lane_off, query_frag<D>(w, ks) * SZ, tag);
     };
     auto load_rest = [&](int blk) {
-      const auto mr = mat_rsrc(p.m, MP, blk);
+      const auto mr = mat_rsrc(p.m, NM, blk);
 #pragma unroll
-      for (int pl = 0; pl < MP; ++pl)
+      for (int pl = 0; pl < NM; ++pl)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           if (ks <= (w >> 1)) mf[ks][pl] = buf_frag(mr, lane_off, mat_frag(pl, w, ks) * SZ, tag);
@@ -587,7 +588,7 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int pl = 0; pl < PP; ++pl)
+          for (int pl = 0; pl < NP; ++pl)
             o[ct] = mma(qf[ks], lds_row8(copy + pl * CS::SPLANE + row_of(ct, c) * CS::SPITCH + 32 * ks + 8 * g16), o[ct]);
       if constexpr (GRAD) {
         // the state at the block's start, [dv][dk], for the gradients of q and k
