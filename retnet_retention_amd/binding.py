@@ -11,7 +11,6 @@ import functools
 import os
 
 import torch
-from torch._C import _cuda_getCurrentRawStream
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libretention.so")
 
@@ -265,9 +264,10 @@ def chunkwise_error(workspace):
     current stream first): 0 when the call that used it completed without an
     error, else bit 0 (1) a wait that gave up, bit 1 (2) clamped packed
     bounds; the outputs are then not valid."""
+    stream = _stream(workspace)
     word = ctypes.c_int32(0)
     _check(lib().retention_chunkwise_error(_ptr(workspace), workspace.numel() * workspace.element_size(),
-                                           ctypes.byref(word), _stream(workspace)))
+                                           ctypes.byref(word), stream))
     return int(word.value)
 
 
@@ -280,8 +280,19 @@ def check_chunkwise(workspace):
         raise RetentionError("control", f"chunkwise control word 1 = {w} ({why}); the outputs are not valid", w)
 
 
+# The stream's handle without a Stream object around it (a microsecond of a
+# decode call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(t):
-    return _cuda_getCurrentRawStream(t.get_device())
+    """The current stream of a GPU tensor's device. A CPU tensor is refused: its
+    device number, -1, would mean the current device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the call takes GPU tensors")
+    return _raw_stream(dev)
 
 
 def _validate(q, k, v, g, out):
