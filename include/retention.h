@@ -340,10 +340,12 @@ ret_status_t retention_delta_fwd(const ret_delta_desc_t *desc, const int32_t *cu
  * beta and state_in (d_state_in non-NULL exactly when state_in is). Key heads
  * that several value heads share receive the sum. The forward's walk is run
  * again; what the gradients need of it takes workspace: per 64 tokens and
- * value head two states of dk dv elements of the dtype and half a state of
- * dk dv fp32 (at dk 256 in bf16 384 KiB), four 64 x 64 matrices (96 KiB in
- * bf16, 64 KiB in fp32) and v twice (bf16) or once (fp32). A log_decay whose
- * factor is 0 in 32 bits has gradient 0. */
+ * value head two states of dk dv fp32 (at dk 256 512 KiB) and three 64 x 64
+ * matrices (72 KiB in bf16, 48 KiB in fp32), v three times (bf16) or once (fp32),
+ * and per 64 tokens and key head three copies of the keys or queries and 32 KiB.
+ * d_log_decay is summed from terms that each carry the token's own factor, so
+ * its error falls with the factor as it does. A log_decay whose factor is 0 in 32
+ * bits has gradient 0. */
 size_t retention_delta_bwd_workspace_bytes(const ret_delta_desc_t *desc, int32_t packed, int64_t total_tokens);
 ret_status_t retention_delta_bwd(const ret_delta_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
                                  const void *q, const void *k, const void *v, const float *log_decay,

@@ -44,7 +44,7 @@ Sizes sizes_of(const ret_delta_desc_t* d, bool packed, int64_t total) {
 }
 
 DeltaLayout layout_of(const ret_delta_desc_t* d, bool packed, int64_t total) {
-  return ret::delta_layout(d->batch, d->seqlen, d->dk, d->dtype, packed, (int)total);
+  return ret::delta_layout(d->batch, d->seqlen, d->dtype, packed, (int)total);
 }
 
 // Takes 256-byte aligned parts of a workspace in turn; with no workspace it
@@ -59,36 +59,39 @@ struct Carve {
   }
 };
 
-// control block | T | M | decay vectors | keys and queries in the lanes' order
-void carve_fwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d, int planes) {
+size_t key_bytes(const DeltaLayout& l, const ret_delta_desc_t* d) {
+  return l.blocks * d->k_heads * ret::kDeltaBlock * d->dk * elem_size(d->dtype);
+}
+
+// control block | T | decay vectors | keys in the lanes' order
+void carve_shared(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d, int planes) {
   const size_t n = l.blocks * d->v_heads;
   c.part(p.ctrl, 2 * sizeof(int32_t));
   c.part(p.t, n * planes * l.mat_plane);
-  c.part(p.m, n * planes * l.mat_plane);
   c.part(p.vec, n * 4 * ret::kDeltaBlock * sizeof(float));
-  const size_t keys = l.blocks * d->k_heads * ret::kDeltaBlock * d->dk * elem_size(d->dtype);
-  c.part(p.kf, keys);
-  c.part(p.kc, keys);
-  c.part(p.qf, keys);
+  c.part(p.kf, key_bytes(l, d));
+  c.part(p.kc, key_bytes(l, d));
 }
 
-// the forward's parts | queries by columns | T^T | P^T | states | gradients of
-// states | fp32 states of the groups | V' | row sums
+// the shared parts | M | queries
+void carve_fwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d) {
+  carve_shared(c, p, l, d, l.planes);
+  c.part(p.m, l.blocks * d->v_heads * l.planes * l.mat_plane);
+  c.part(p.qf, key_bytes(l, d));
+}
+
+// the shared parts | queries | q.k and k.k | T^T | P^T | states | gradients of states | V' | rest of dv
 void carve_bwd(Carve& c, DeltaParams& p, const DeltaLayout& l, const ret_delta_desc_t* d, const Sizes& s) {
-  carve_fwd(c, p, l, d, l.mat_planes);
-  const size_t n = l.blocks * d->v_heads, dd = (size_t)d->dk * d->dv;
-  c.part(p.qc, l.blocks * d->k_heads * ret::kDeltaBlock * d->dk * elem_size(d->dtype));
+  carve_shared(c, p, l, d, l.mat_planes);
+  const size_t n = l.blocks * d->v_heads, state = (size_t)d->dk * d->dv * l.planes * elem_size(d->dtype);
+  c.part(p.qc, key_bytes(l, d));
+  c.part(p.pairs, l.blocks * d->k_heads * 2 * ret::kDeltaBlock * ret::kDeltaBlock * sizeof(float));
   c.part(p.tt, n * l.mat_planes * l.mat_plane);
   c.part(p.pt, n * l.mat_planes * l.mat_plane);
-  c.part(p.snap, n * dd * elem_size(d->dtype));
-  c.part(p.dsnap, n * dd * elem_size(d->dtype));
-  c.part(p.anchor, l.groups * d->v_heads * dd * sizeof(float));
+  c.part(p.snap, n * state);
+  c.part(p.dsnap, n * state);
   c.part(p.u, s.v * l.planes);
-  const size_t sums = n * l.slices * ret::kDeltaBlock * sizeof(float);
-  c.part(p.odo, sums);
-  c.part(p.vdv, sums);
-  c.part(p.udv, sums);
-  c.part(p.adot, l.groups * d->v_heads * l.slices * 4 * sizeof(float));  // a value of each of the four waves
+  c.part(p.dv_rest, s.v * (l.planes - 1));
 }
 
 size_t workspace_bytes_of(const ret_delta_desc_t* d, bool packed, int64_t total, bool grad) {
@@ -99,7 +102,7 @@ size_t workspace_bytes_of(const ret_delta_desc_t* d, bool packed, int64_t total,
   if (grad)
     carve_bwd(c, p, l, d, sizes_of(d, packed, total));
   else
-    carve_fwd(c, p, l, d, l.planes);
+    carve_fwd(c, p, l, d);
   return c.used;
 }
 
@@ -159,8 +162,7 @@ ret_status_t retention_delta_fwd(const ret_delta_desc_t* desc, const int32_t* cu
   p.o = o;
   p.state_out = state_out;
   Carve c{static_cast<char*>(workspace)};
-  const DeltaLayout l = layout_of(desc, packed, total_tokens);
-  carve_fwd(c, p, l, desc, l.planes);
+  carve_fwd(c, p, layout_of(desc, packed, total_tokens), desc);
   return ret::launch_delta_fwd(p, desc->dk, desc->dtype, stream) == hipSuccess ? RET_OK : RET_ERR_HIP;
 }
 

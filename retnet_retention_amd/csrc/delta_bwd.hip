@@ -1,6 +1,6 @@
 // Gradients of the gated delta rule's chunkwise form. The forward's walk is
-// run again (delta_fwd.hip, which keeps V', the state at each block's start and
-// the row sums o . dO); then, with dS+ the gradient of a block's final state,
+// run again (delta_fwd.hip, which keeps V' and the state at each block's start);
+// then, with dS+ the gradient of a block's final state,
 //     dV' = e^(G_last - G) K dS+ + P^T dO,   dv = T^T dV'  (X = V - e^G K S),
 //     dS = e^(G_last) dS+ + Q^T (scale e^G dO) - K^T (e^G dv)
 // goes through the blocks from the last to the first (delta_reverse_kernel),
@@ -8,12 +8,15 @@
 //     dP = (dO V'^T) scale E  (s <= r),   dA = -(dv V'^T) E  (s < r),
 //     dq = scale e^G dO S^T + dP K,
 //     dk = e^(G_last - G) V' dS+^T - e^G dv S^T + dP^T Q + (dA + dA^T) K.
-// The decays and strengths take row sums only. Scaling the state's history up
-// to token t by a factor is the same as scaling every later output and
-// dividing every later value by it, so with d_t = o_t . dO_t - v_t . dv_t
-//     d log_decay_t = sum over t' >= t of d_t' + <S_end, dS_end>,
-// summed inside groups of kDeltaGroup blocks from the product of the state and
-// its gradient at the group's end (a sum over a whole sequence would cancel);
+// A log decay stands in every factor E and e^G that crosses its token, so
+//     d log_decay_t = sum over s < t <= r of W_rs + sum over r >= t of x_r
+//                     + sum over s < t of y_s + e^(G_last) <S, dS+>,
+//     W_rs = dP_rs (q_r . k_s) + dA_rs (k_r . k_s),
+//     x_r = q_r . (scale e^G dO S^T)_r - k_r . (e^G dv S^T)_r,
+//     y_s = k_s . (e^(G_last - G) V' dS+^T)_s,
+// each term with that factor. (The difference of row sums o . dO - v . dv gives
+// the same value, but terms without the factor cancel in it and leave their
+// roundings: where a token forgets much, more than the gradient itself.)
 //     d beta_t = dv_t . V'_t / beta_t^2   (V' is beta times the prediction error,
 //     dv beta times what the write of it gains).
 #include "delta_common.hpp"
@@ -25,9 +28,9 @@ hipError_t launch_delta_forward(const DeltaParams& p, int d, int dtype, bool gra
 // The gradient of the state, from a sequence's last block to its first: the
 // same division of work and the same three exchanges as delta_chain_kernel.
 // The second four waves form P^T dO, put scale e^G dO where the state waves
-// read it, and take the row sums. 333 us for 4 sequences of 32 blocks, 10 heads
+// read it, and write dv. 351 us for 4 sequences of 32 blocks, 10 heads
 // of 256 (320 workgroups on 256 CUs: two rounds, the second a quarter full), and
-// the forward's walk before it 335; 171 and 193 us for 63 blocks, 16 heads of
+// the forward's walk before it 241; 170 and 132 us for 63 blocks, 16 heads of
 // 128 (64 workgroups, 2.7 us a block). With 128 registers a lane, for two
 // workgroups a CU at 128, both spill: 720 us for a backward that took 407.
 template <typename T, int D>
@@ -140,24 +143,6 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
 
     for (int blk = nblk - 1; blk >= 0; --blk) {
       const int64_t slot = slot_of(blk);
-      const bool group_end = (blk + 1) % kDeltaGroup == 0 || blk == nblk - 1;
-      if (group_end && (blk != nblk - 1 || p.d_state_out)) {
-        // <state, its gradient> at the group's end, this wave's part
-        const int64_t at =
-            (((int64_t)(base / kDeltaGroup + b + blk / kDeltaGroup) * p.heads + h) * CS::NSL + slice) * 4 + w;
-        const float* an = p.anchor + at * (TPW * 1024) + lane * 4;
-        float dot = 0.f;
-#pragma unroll
-        for (int t = 0; t < TPW; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(an + (4 * t + q) * 256);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dot += x[i] * s[t][4 * q + i];
-          }
-        dot = sum64(dot);
-        if (lane == 0) p.adot[at] = dot;
-      }
       if constexpr (!kAhead) load_keys(kf, blk);
       const auto queries = key_rsrc(p.qc, blk);
       Split<T> f[CS::KS];
@@ -174,8 +159,9 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
             load_column(qc, queries, t, 2 * SLI);
             load_column(qc, queries, t, 2 * SLI + 1);
           }
-          T* sn = reinterpret_cast<T*>(p.dsnap) + (slot * D + vcol) * D + krow + 16 * ks + 8 * h2;
-          *reinterpret_cast<frag_t<T>*>(sn) = f[ks].f[0];
+          T* sn = reinterpret_cast<T*>(p.dsnap) + (slot * NP * D + vcol) * D + krow + 16 * ks + 8 * h2;
+#pragma unroll
+          for (int pl = 0; pl < NP; ++pl) *reinterpret_cast<frag_t<T>*>(sn + pl * D * D) = f[ks].f[pl];
         });
       if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -246,7 +232,7 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
     frag_t<T> pf[2][NM];
 #pragma unroll
     for (int pl = 0; pl < NM; ++pl) pf[0][pl] = zero_frag<T>();
-    PairOf<T> dout[CG][4], dnext[CG][4], v[CG][4], u[NP][CG][4];
+    PairOf<T> dout[CG][4], dnext[CG][4];
     f32x4 eg;
     auto put_dout = [&](const PairOf<T>(&x)[CG][4]) {  // exact in T
 #pragma unroll
@@ -257,15 +243,9 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
         *reinterpret_cast<vec4_t<T>*>(od + row_of(ct, c) * PITCH + r4) = y;
       }
     };
-    auto load_values = [&](int blk) {
-      load_pairs(v, p.v, blk);
-#pragma unroll
-      for (int pl = 0; pl < NP; ++pl) load_pairs(u[pl], reinterpret_cast<const T*>(p.u) + pl * (int64_t)p.total * vs, blk);
-    };
     load_pairs(dout, p.dout, nblk - 1);
     load_mat(pf, p.pt, nblk - 1);
     eg = buf_f4(vec_rsrc(nblk - 1), r4 * 4, 0);
-    load_values(nblk - 1);
     load_pairs(dnext, p.dout, nblk - 2);
     put_dout(dout);
     lds_barrier();
@@ -300,65 +280,89 @@ __global__ __launch_bounds__(512) void delta_reverse_kernel(DeltaParams p) {
       eg = buf_f4(vec_rsrc(blk - 1), r4 * 4, 0);
       lds_barrier();
       lds_barrier();
-      // dv and the row sums of the quarter
+      // dv of the quarter, and what its type leaves of it
       const auto rs = value_rsrc(p.dv, blk);
-      f32x4 vdv = zero4(), uv = zero4();
 #pragma unroll
       for (int g = 0; g < CG; ++g) {
-        f32x4 dv[2];
+        const f32x4 x = my_quarter[16 * (2 * g)], y = my_quarter[16 * (2 * g + 1)];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          dv[e] = my_quarter[16 * (2 * g + e)];
+        for (int i = 0; i < 4; ++i) buf_put_pair(rs, pair_off[i] + 32 * g * SZ, x[i], y[i], tag);
+        if constexpr (NP > 1) {
+          const auto rest = value_rsrc(p.dv_rest, blk);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y = 0.f;
-#pragma unroll
-            for (int pl = 0; pl < NP; ++pl) y += u[pl][g][i].get(e);
-            vdv[i] += dv[e][i] * v[g][i].get(e);
-            uv[i] += dv[e][i] * y;
-          }
+          for (int i = 0; i < 4; ++i)
+            buf_put_pair(rest, pair_off[i] + 32 * g * SZ, x[i] - (float)(T)x[i], y[i] - (float)(T)y[i], tag);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) buf_put_pair(rs, pair_off[i] + 32 * g * SZ, dv[0][i], dv[1][i], tag);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vdv[i] = sum16(vdv[i]);
-        uv[i] = sum16(uv[i]);
-      }
-      if (c == 0) {
-        *reinterpret_cast<f32x4*>(p.vdv + (slot_of(blk) * CS::NSL + slice) * kB + r4) = vdv;
-        *reinterpret_cast<f32x4*>(p.udv + (slot_of(blk) * CS::NSL + slice) * kB + r4) = uv;
-      }
-      load_values(blk - 1);
     }
   }
 }
 
-// d q and d k of one block and key head, summed over the value heads that
-// share it (GROUPED: more than one); wave w the key columns 32 w .. + 31. Bound
-// by the two states a block reads, D x D each: they pass through LDS by 32 value
-// columns, the next tile (two buffers, fp32 one) on its way while one is
-// multiplied, and each of dO, dv and V' is read once for all its products. 161
-// us for 1280 blocks of 256 x 256 (336 MB of states, 294 MB of rows: 3.9 TB/s);
-// 70 us with two value heads of 128 a key head.
+// sum of a_j b_j over a fragment's elements
+__device__ __forceinline__ float dot_frag(const bf16x8& a, const bf16x8& b, float c) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int j = 0; j < 8; j += 2)
+    c = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a[j], a[j + 1]}, bf16x2{b[j], b[j + 1]}, c, false);
+  return c;
+}
+__device__ __forceinline__ float dot_frag(const f32x8& a, const f32x8& b, float c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = fmaf(a[j], b[j], c);
+  return c;
+}
+
+// Sum over the lanes up to this one. Only lower lanes are added, so a lane's sum
+// takes no rounding from what it leaves out.
+__device__ __forceinline__ float scan64(float x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const float y = __shfl_up(x, o, 64);
+    x += lane >= o ? y : 0.f;
+  }
+  return x;
+}
+
+// Gradients of one block and key head: dq and dk, summed over the value heads
+// that share it (GROUPED: more than one), and each value head's d log decay and
+// d beta. Wave w takes the key columns 32 w .. + 31. The two states of a block
+// pass through LDS by 16 value columns, the next ones on their way while some are
+// multiplied; each of dO, dv and V' is read once for all its products. States,
+// dv and V' come as their planes (bf16: two values, so that dq and dk are at
+// their own rounding and the decays' gradients good to a few 1e-6).
+// A log decay's gradient is the sum of every term that its factor stands in:
+// weights between tokens on both sides of it (w: the products of dP with Q K^T and
+// of dA with K K^T), what later tokens read of the state before the block (x),
+// what earlier ones leave in the state after it (y), and what passes through the
+// block (z). Nothing cancels that lacks the factor, so the error carries it too.
+// Bound by the states' way into LDS: 324 us for 1280 blocks of 256 x 256 (671 MB
+// of states, 210 MB of rows), where one bf16 value a state took 161 and left dq
+// 2.9e-3 and dk 3.2e-3 off (now 1.7e-3, their own rounding); 135 us with two value
+// heads of 128 a key head. Shared key heads keep dq and dk beside the sums of a
+// head: 40 (bf16) and 79 (fp32) vector registers of a lane spill at 256, 57 and 36
+// at 64, written and read once a value head.
 // Products of a wave are straight lines of matrix instructions with no branch
-// among them. Operands are one bf16 value here (2^-9 each, a sum of independent
-// roundings below that of the bf16 result): dq and dk are off by 2.7e-3 and
-// 3.0e-3 where their own rounding gives 1.7e-3.
+// among them.
 template <typename T, int D, bool GROUPED>
-__global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
-  constexpr int NW = D / 32, TW = 8 / NW;  // tasks of 16 rows of dP and dA a wave
-  constexpr int DV = 32;                   // value columns of a state tile in LDS
-  constexpr int BUFS = sizeof(T) == 2 ? 2 : 1;
+__global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_grad_kernel(DeltaParams p) {
+  constexpr int NP = Planes<T>::N, SZ = sizeof(T);
+  constexpr int NW = D / 32, TW = 8 / NW;  // 32 x 32 tiles of dP and dA a wave
+  constexpr int DV = 16;                   // value columns of a state tile in LDS
   using ST = LTile<T, DV, D, kColTile>;
-  constexpr int PA = sizeof(T) == 2 ? 40 : 36;  // pitch of the row operands
-  constexpr int PM = sizeof(T) == 2 ? 72 : 68;  // pitch of the 64 x 64 matrices
-  constexpr int ROWS = 3 * kB * PA;
-  __shared__ __attribute__((aligned(1024))) char tiles[2 * BUFS * ST::BYTES];
-  __shared__ __attribute__((aligned(16))) T row_ops[BUFS * ROWS];  // [dO, dv, V'][64][PA]
-  __shared__ __attribute__((aligned(16))) T mp[kB * PM], mpt[kB * PM], ms[kB * PM];
+  constexpr int PA = SZ == 2 ? 24 : 20;  // pitch of the row operands
+  constexpr int PM = SZ == 2 ? 72 : 68;  // pitch of the 64 x 64 operands
+  constexpr int PW = 68;                 // pitch of the weights
+  constexpr int NR = 1 + 2 * NP;         // row operands: dO, dv and V' in planes
+  // in LDS dO has as many planes as the others (zeros), so that the tiles of dP
+  // and dA are the same products
+  constexpr int ROWS = 3 * NP * kB * PA;
+  struct Stage { char tiles[2][2 * NP][ST::BYTES]; T rows[2][ROWS]; };
+  struct Weights { float w[2][kB][PW]; };
+  struct Mats { T p[NP][kB * PM], pt[NP][kB * PM], s[NP][kB * PM]; };
+  union Shared { Stage st; Weights wt; Mats m; __device__ Shared() {} };
+  __shared__ __attribute__((aligned(1024))) Shared sh;
   __shared__ double sg[kB];
+  __shared__ float sx[NW][kB], sy[NW][kB], sw[NW][kB], sz[NW], sbeta[kB];
   T* const tag = nullptr;
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform_i(tid >> 6);
@@ -369,36 +373,50 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
   if (blk * kB >= len) return;
   const int rows = min(kB, len - blk * kB);
   const int64_t row0 = tok0 + blk * kB;
-  const int n = lane & 31, h2 = lane >> 5, g16 = lane >> 4, c = lane & 15;
+  const int n = lane & 31, h2 = lane >> 5;
   const int64_t qs = (int64_t)p.k_heads * D, vs = (int64_t)p.heads * D;
   const int group = GROUPED ? p.heads / p.k_heads : 1;
-  // keys and queries by columns, the wave's 32
-  const int64_t key_slot = ((int64_t)(base + blk) * p.k_heads + hk) * (kB * D) + 8 * lane;
-  const T* KC = reinterpret_cast<const T*>(p.kc) + key_slot;
-  const T* QC = reinterpret_cast<const T*>(p.qc) + key_slot;
+  const int64_t key_slot = (int64_t)(base + blk) * p.k_heads + hk;
 
   f32x16 dq[2] = {zero16(), zero16()}, dk[2] = {zero16(), zero16()};
   for (int hh = 0; hh < group; ++hh) {
     const int h = hk * group + hh;
     const int64_t slot = (int64_t)(base + blk) * p.heads + h;
-    const T* src[3] = {reinterpret_cast<const T*>(p.dout) + row0 * vs + h * D,
-                       reinterpret_cast<const T*>(p.dv) + row0 * vs + h * D,
-                       reinterpret_cast<const T*>(p.u) + row0 * vs + h * D};
-    const T* SN = reinterpret_cast<const T*>(p.snap) + slot * D * D;
-    const T* DN = reinterpret_cast<const T*>(p.dsnap) + slot * D * D;
+    const T* SN = reinterpret_cast<const T*>(p.snap) + slot * (NP * D * D);
+    const T* DN = reinterpret_cast<const T*>(p.dsnap) + slot * (NP * D * D);
     TileLoads<T, ST, NW> sloads;
     sloads.init(D, lane);
-    constexpr int RN = (3 * kB * (DV / 8) + 2 * D - 1) / (2 * D);  // row operands: chunks of 8 a thread
+    constexpr int CHUNKS = kB * (DV / 8);  // of 8 elements in a row operand, a whole number of waves
+    constexpr int RN = (NR * CHUNKS + 2 * D - 1) / (2 * D);
+    const int cr = (tid % CHUNKS) / 2, cj = tid % 2 * 8;  // row and column of the thread's chunks
     Raw8<T> raw[RN];
-    auto ask = [&](int d0) {
-      char* to = tiles + (d0 / DV % BUFS) * 2 * ST::BYTES;
-      sloads.issue(to, SN, D, d0, w);
-      sloads.issue(to + ST::BYTES, DN, D, d0, w);
+    auto operand_of = [&](int i) { return uniform_i((tid + i * 2 * D) / CHUNKS); };
+    auto ask = [&](int d0, int buf) {
+#pragma unroll
+      for (int pl = 0; pl < NP; ++pl) {
+        sloads.issue(sh.st.tiles[buf][pl], SN + pl * D * D, D, d0, w);
+        sloads.issue(sh.st.tiles[buf][NP + pl], DN + pl * D * D, D, d0, w);
+      }
 #pragma unroll
       for (int i = 0; i < RN; ++i) {
-        const int at = tid + i * 2 * D, m = at / (kB * (DV / 8)), r = at / (DV / 8) % kB, j = at % (DV / 8) * 8;
-        raw[i] = Raw8<T>{};
-        if (m < 3 && r < rows) raw[i] = ld_raw8((m == 0 ? src[0] : m == 1 ? src[1] : src[2]) + r * vs + d0 + j);
+        const int m = operand_of(i);
+        const T* src = reinterpret_cast<const T*>(m == 0 ? p.dout : m == 1 ? p.dv : NP > 1 && m == 2 ? p.dv_rest : p.u);
+        if (m > NP) src += (m - 1 - NP) * (int64_t)p.total * vs;
+        const auto rs = scalar_rsrc(src + row0 * vs + h * D, m < NR ? rows * (uint32_t)vs * SZ : 0);
+        raw[i] = __builtin_bit_cast(Raw8<T>, buf_frag(rs, (cr * (uint32_t)vs + cj) * SZ, d0 * SZ, tag));
+      }
+    };
+    // columns within 16 in the order of the column fragments: 0-3, 8-11, 4-7, 12-15
+    auto put_rows = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < RN; ++i) {
+        const int m = operand_of(i);
+        if (m < NR) {
+          const frag_t<T> x = __builtin_bit_cast(frag_t<T>, raw[i]);
+          T* to = sh.st.rows[buf] + ((m ? NP + m - 1 : 0) * kB + cr) * PA + cj / 2;
+          *reinterpret_cast<vec4_t<T>*>(to) = vec4_t<T>{x[0], x[1], x[2], x[3]};
+          *reinterpret_cast<vec4_t<T>*>(to + 8) = vec4_t<T>{x[4], x[5], x[6], x[7]};
+        }
       }
     };
     if constexpr (GROUPED) __syncthreads();  // the last head's reads
@@ -413,91 +431,91 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
       }
       sg[lane] = s;
     }
-    for (int i = tid; i < 3 * kB * PM; i += 2 * D) (i < kB * PM ? mp : i < 2 * kB * PM ? mpt : ms)[i % (kB * PM)] = (T)0.f;
+    if constexpr (NP > 1) {
+      for (int i = tid; i < 2 * kB * PA / 8; i += 2 * D)
+        store8_zero(sh.st.rows[i / (kB * PA / 8)] + kB * PA + i % (kB * PA / 8) * 8);
+    }
 
-    f32x4 acc[TW][4];
+    f32x16 acc[TW];  // [s][r]: V' dO^T and V' dv^T
 #pragma unroll
-    for (int k = 0; k < TW; ++k)
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) acc[k][ct] = zero4();
-    // dO S^T, V' dS^T and dv S^T over the value columns
+    for (int k = 0; k < TW; ++k) acc[k] = zero16();
+    // dO S^T, V' dS^T and dv S^T over the value columns, and <S, dS>
     f32x16 a0[2] = {zero16(), zero16()}, a1[2] = {zero16(), zero16()}, a2[2] = {zero16(), zero16()};
-    ask(0);
+    float z = 0.f;
+    ask(0, 0);
     for (int d0 = 0; d0 < D; d0 += DV) {
-      const char* tile = tiles + (d0 / DV % BUFS) * 2 * ST::BYTES;
-      T* ops = row_ops + (d0 / DV % BUFS) * ROWS;
-#pragma unroll
-      for (int i = 0; i < RN; ++i) {
-        const int at = tid + i * 2 * D, m = at / (kB * (DV / 8)), r = at / (DV / 8) % kB, j = at % (DV / 8) * 8;
-        if (m < 3) st_raw8(ops + (m * kB + r) * PA + j, raw[i], true);
-      }
+      const int buf = d0 / DV % 2;
+      put_rows(buf);
       __builtin_amdgcn_s_waitcnt(0);  // the tiles (LDS loads run past the compiler's counting)
       lds_barrier();
-      if (BUFS == 2 && d0 + DV < D) ask(d0 + DV);
+      if (d0 + DV < D) ask(d0 + DV, buf ^ 1);
+      auto row = [&](int plane, int rt) {
+        return lds_row8(sh.st.rows[buf] + (plane * kB + 32 * rt + n) * PA + 8 * h2);
+      };
+      frag_t<T> fs[NP], fd[NP];
+#pragma unroll
+      for (int pl = 0; pl < NP; ++pl) {
+        fs[pl] = state_tile_col8<ST>(sh.st.tiles[buf][pl], 0, 32 * w, lane, tag);
+        fd[pl] = state_tile_col8<ST>(sh.st.tiles[buf][NP + pl], 0, 32 * w, lane, tag);
+      }
+      // (products of two rests are below 2^-17 of the first and left out)
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        const frag_t<T> x = row(0, rt);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const frag_t<T> dv = row(NP + i, rt), u = row(2 * NP + i, rt);
+          a0[rt] = mma32(x, fs[i], a0[rt]);
+#pragma unroll
+          for (int j = 0; i + j < NP; ++j) {
+            a2[rt] = mma32(dv, fs[j], a2[rt]);
+            a1[rt] = mma32(u, fd[j], a1[rt]);
+          }
+        }
+      }
 #pragma unroll
       for (int k = 0; k < TW; ++k) {
-        const int task = w + k * NW, rb = task & 3, which = task >> 2;
-        const frag_t<T> a = lds_row8(ops + (which * kB + 16 * rb + c) * PA + 8 * g16);
+        const int task = w + k * NW, which = task >> 2, rt = task >> 1 & 1, st = task & 1;
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct)  // (all four: the upper ones are left out below)
-          acc[k][ct] = mma(a, lds_row8(ops + (2 * kB + 16 * ct + c) * PA + 8 * g16), acc[k][ct]);
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int j = 0; i + j < NP; ++j)
+            acc[k] = mma32(row(2 * NP + i, st), row(which * NP + j, rt), acc[k]);
       }
 #pragma unroll
-      for (int ks = 0; ks < DV / 16; ++ks) {
-        const frag_t<T> fs = state_tile_col8<ST>(tile, 16 * ks, 32 * w, lane, tag);
-        const frag_t<T> fd = state_tile_col8<ST>(tile + ST::BYTES, 16 * ks, 32 * w, lane, tag);
-        // the column fragments' order of the contraction
-        auto row = [&](int m, int rt) {
-          const T* at = ops + (m * kB + 32 * rt + n) * PA + 16 * ks + 4 * h2;
-          const vec4_t<T> lo = *reinterpret_cast<const vec4_t<T>*>(at), hi = *reinterpret_cast<const vec4_t<T>*>(at + 8);
-          frag_t<T> f;
+      for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[j] = lo[j];
-            f[4 + j] = hi[j];
-          }
-          return f;
-        };
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-          a0[rt] = mma32(row(0, rt), fs, a0[rt]);
-          a2[rt] = mma32(row(1, rt), fs, a2[rt]);
-          a1[rt] = mma32(row(2, rt), fd, a1[rt]);
-        }
-      }
-      if (BUFS == 1 && d0 + DV < D) {
-        lds_barrier();
-        ask(d0 + DV);
-      }
+        for (int j = 0; i + j < NP; ++j) z = dot_frag(fs[i], fd[j], z);
     }
-    frag_t<T> fq[4], fk[4];
+    frag_t<T> fq[4], fk[4];  // queries and keys by columns, the wave's 32
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      fq[ks] = *reinterpret_cast<const frag_t<T>*>(QC + column_frag(w, ks));
-      fk[ks] = *reinterpret_cast<const frag_t<T>*>(KC + column_frag(w, ks));
+      const int64_t at = key_slot * (kB * D) + 8 * lane + column_frag(w, ks);
+      fq[ks] = *reinterpret_cast<const frag_t<T>*>(reinterpret_cast<const T*>(p.qc) + at);
+      fk[ks] = *reinterpret_cast<const frag_t<T>*>(reinterpret_cast<const T*>(p.kc) + at);
     }
-    // dP (both ways round) and dA + dA^T
+    __syncthreads();  // the stage has been read
+    // dP and dA in place of the sums, and their weights
 #pragma unroll
     for (int k = 0; k < TW; ++k) {
-      const int task = w + k * NW, rb = task & 3, which = task >> 2;
+      const int task = w + k * NW, which = task >> 2, r = 32 * (task >> 1 & 1) + n, s0 = 32 * (task & 1) + 4 * h2;
+      const float* pairs = p.pairs + (key_slot * 2 + which) * (kB * kB) + r * kB + s0;
+      const double gr = sg[r];
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        const int s = 16 * ct + c;
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 pair = *reinterpret_cast<const f32x4*>(pairs + 8 * q);
+        f32x4 wt;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 16 * rb + 4 * g16 + i;
-          const float e = s <= r ? __builtin_amdgcn_exp2f((float)((sg[r] - sg[s]) * 1.4426950408889634)) : 0.f;
-          if (which == 0 && s <= r) {
-            const T x = (T)(p.scale * e * acc[k][ct][i]);
-            mp[r * PM + s] = x;
-            mpt[s * PM + r] = x;
-          }
-          if (which == 1 && s < r) {
-            const T x = (T)(-e * acc[k][ct][i]);
-            ms[r * PM + s] = x;
-            ms[s * PM + r] = x;
-          }
+          const int s = s0 + 8 * q + i;
+          const float e = __builtin_amdgcn_exp2f((float)((gr - sg[s]) * 1.4426950408889634));
+          float x = acc[k][4 * q + i];
+          if (which && s == r) sbeta[r] = x;
+          x = which ? -e * x : p.scale * e * x;
+          wt[i] = s < r ? pair[i] * x : 0.f;
+          acc[k][4 * q + i] = s < r || (s == r && !which) ? x : 0.f;
         }
+        *reinterpret_cast<f32x4*>(&sh.wt.w[which][r][s0 + 8 * q]) = wt;
       }
     }
     const float* vec = p.vec + slot * (4 * kB);
@@ -505,16 +523,98 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 eg = *reinterpret_cast<const f32x4*>(vec + 32 * rt + 8 * q + 4 * h2);
-        const f32x4 el = *reinterpret_cast<const f32x4*>(vec + kB + 32 * rt + 8 * q + 4 * h2);
+        const int r = 32 * rt + 8 * q + 4 * h2;
+        const f32x4 eg = *reinterpret_cast<const f32x4*>(vec + r), el = *reinterpret_cast<const f32x4*>(vec + kB + r);
+        f32x4 xs, ys;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = p.scale * eg[i] * a0[rt][4 * q + i];
-          const float y = el[i] * a1[rt][4 * q + i] - eg[i] * a2[rt][4 * q + i];
-          dq[rt][4 * q + i] = GROUPED ? dq[rt][4 * q + i] + x : x;
-          dk[rt][4 * q + i] = GROUPED ? dk[rt][4 * q + i] + y : y;
+          const int e = 4 * q + i;
+          const float x = p.scale * eg[i] * a0[rt][e], y = el[i] * a1[rt][e], v = eg[i] * a2[rt][e];
+          const float key = (float)fk[2 * rt + e / 8][e % 8];
+          xs[i] = (float)fq[2 * rt + e / 8][e % 8] * x - key * v;
+          ys[i] = key * y;
+          dq[rt][e] = GROUPED ? dq[rt][e] + x : x;
+          dk[rt][e] = GROUPED ? dk[rt][e] + (y - v) : y - v;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          xs[i] = sum_lanes<32>(xs[i]);
+          ys[i] = sum_lanes<32>(ys[i]);
+        }
+        if (n == 0) {
+          *reinterpret_cast<f32x4*>(&sx[w][r]) = xs;
+          *reinterpret_cast<f32x4*>(&sy[w][r]) = ys;
         }
       }
+    z = sum64(z);
+    if (lane == 0) sz[w] = z;
+    __syncthreads();
+    // weights between tokens before t and tokens from t on, for t = lane
+    {
+      float sum = 0.f;
+#pragma unroll 4
+      for (int r = w; r < kB; r += NW) {
+        const int s = lane > 0 ? lane - 1 : 0;
+        const float x = scan64(lane > 0 ? sh.wt.w[0][r][s] + sh.wt.w[1][r][s] : 0.f, lane);
+        sum += lane <= r ? x : 0.f;
+      }
+      sw[w][lane] = sum;
+    }
+    __syncthreads();
+    if (w == 0) {
+      float x = 0.f, y = 0.f, sum = 0.f, zs = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        x += sx[i][63 - lane];  // tokens from t on: summed from the last, in reversed lanes
+        y += lane ? sy[i][lane - 1] : 0.f;
+        sum += sw[i][lane];
+        zs += sz[i];
+      }
+      x = __shfl(scan64(x, lane), 63 - lane, 64);
+      const float through = vec[kB - 1];  // exp(G_last)
+      sum += x + scan64(y, lane) + (through == 0.f ? 0.f : through * zs);
+      if (lane < rows) {
+        const int64_t at = (row0 + lane) * p.heads + h;
+        // a factor of 0 in 32 bits: no term is left, but those that are not finite
+        const bool none = (blk + lane == 0 && !p.state_in) || p.log_decay[at] < kZeroLogDecay;
+        p.d_log_decay[at] = none ? 0.f : sum;
+        const float beta = vec[2 * kB + lane];
+        p.d_beta[at] = sbeta[lane] / beta / beta;
+      }
+    }
+    // dP (both ways round) and dA + dA^T as operands, in planes
+#pragma unroll
+    for (int k = 0; k < TW; ++k) {
+      const int task = w + k * NW, which = task >> 2, rt = task >> 1 & 1, st = task & 1;
+      const int r = 32 * rt + n, s0 = 32 * st + 4 * h2;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 x = {acc[k][4 * q], acc[k][4 * q + 1], acc[k][4 * q + 2], acc[k][4 * q + 3]};
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) {
+          vec4_t<T> y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = (T)x[i];
+            x[i] -= (float)y[i];
+          }
+          if (which == 0) {
+            *reinterpret_cast<vec4_t<T>*>(&sh.m.p[pl][r * PM + s0 + 8 * q]) = y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sh.m.pt[pl][(s0 + 8 * q + i) * PM + r] = y[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int s = s0 + 8 * q + i;
+              if (s <= r) {
+                sh.m.s[pl][r * PM + s] = y[i];
+                sh.m.s[pl][s * PM + r] = y[i];
+              }
+            }
+          }
+        }
+      }
+    }
     __syncthreads();
     // dP^T Q, dP K and (dA + dA^T) K
     auto mrow = [&](const T* m, int rt, int ks) {
@@ -531,11 +631,13 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        dk[rt] = mma32(mrow(mpt, rt, ks), fq[ks], dk[rt]);
-        dq[rt] = mma32(mrow(mp, rt, ks), fk[ks], dq[rt]);
-        dk[rt] = mma32(mrow(ms, rt, ks), fk[ks], dk[rt]);
-      }
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int pl = 0; pl < NP; ++pl) {
+          dk[rt] = mma32(mrow(sh.m.pt[pl], rt, ks), fq[ks], dk[rt]);
+          dq[rt] = mma32(mrow(sh.m.p[pl], rt, ks), fk[ks], dq[rt]);
+          dk[rt] = mma32(mrow(sh.m.s[pl], rt, ks), fk[ks], dk[rt]);
+        }
   }
   T* DQ = reinterpret_cast<T*>(p.dq) + row0 * qs + hk * D + 32 * w + state_col(n);
   T* DK = reinterpret_cast<T*>(p.dk) + row0 * qs + hk * D + 32 * w + state_col(n);
@@ -551,50 +653,6 @@ __global__ __launch_bounds__(2 * D) void delta_qk_grad_kernel(DeltaParams p) {
     }
 }
 
-// d log decay and d beta from the row sums, one wave per (group of blocks,
-// head): 14 us for 640 groups, the latency of its loads.
-__global__ __launch_bounds__(64) void delta_gate_grad_kernel(DeltaParams p, int slices) {
-  const int groups = (p.blocks_max + kDeltaGroup - 1) / kDeltaGroup;
-  const int b = blockIdx.x / groups, grp = blockIdx.x % groups, h = blockIdx.y, lane = threadIdx.x;
-  int64_t tok0;
-  int len, base;
-  seq_span(p, b, tok0, len, base);
-  const int nblk = (len + kB - 1) / kB;
-  if (grp * kDeltaGroup >= nblk) return;
-  const int last = min(nblk, (grp + 1) * kDeltaGroup) - 1;
-  float carry = 0.f;
-  if (last != nblk - 1 || p.d_state_out) {
-    const float* ad = p.adot + ((int64_t)(base / kDeltaGroup + b + grp) * p.heads + h) * slices * 4;
-    for (int i = 0; i < slices * 4; ++i) carry += ad[i];
-  }
-  for (int blk = last; blk >= grp * kDeltaGroup; --blk) {
-    const int64_t slot = (int64_t)(base + blk) * p.heads + h;
-    float d = 0.f, x = 0.f;
-    for (int s = 0; s < slices; ++s) {
-      const int64_t at = (slot * slices + s) * kB + lane;
-      d += p.odo[at] - p.vdv[at];
-      x += p.udv[at];
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-      const float y = __shfl_down(d, o, 64);
-      if (lane + o < 64) d += y;
-    }
-    d += carry;
-    carry = __shfl(d, 0, 64);
-    const int r = blk * kB + lane;
-    if (r < len) {
-      const int64_t at = (tok0 + r) * p.heads + h;
-      // The gradient is the factor exp(log decay) times what the state before it
-      // gives: zero where that is zero. The sum would be its own rounding there.
-      const bool none = (r == 0 && !p.state_in) || p.log_decay[at] < kZeroLogDecay;
-      p.d_log_decay[at] = none ? 0.f : d;
-      const float beta = p.vec[slot * (4 * kB) + 2 * kB + lane];
-      p.d_beta[at] = x / beta / beta;
-    }
-  }
-}
-
 template <typename T, int D>
 static hipError_t launch_backward(const DeltaParams& p, hipStream_t stream) {
   using CS = ChainShape<T, D>;
@@ -606,9 +664,6 @@ static hipError_t launch_backward(const DeltaParams& p, hipStream_t stream) {
     hipLaunchKernelGGL((delta_qk_grad_kernel<T, D, false>), grid, dim3(2 * D), 0, stream, p);
   else
     hipLaunchKernelGGL((delta_qk_grad_kernel<T, D, true>), grid, dim3(2 * D), 0, stream, p);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int groups = (p.blocks_max + kDeltaGroup - 1) / kDeltaGroup;
-  hipLaunchKernelGGL(delta_gate_grad_kernel, dim3(p.batch * groups, p.heads), dim3(64), 0, stream, p, CS::NSL);
   return hipGetLastError();
 }
 

@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
         for (int ks = 0; ks < HALF / 32; ++ks) {
           const frag_t<T> fq = lds_row8(&sh.st.q[16 * w + c][32 * ks + 8 * g16]);
           const frag_t<T> fk = lds_row8(&sh.st.k[16 * w + c][32 * ks + 8 * g16]);
-          *reinterpret_cast<frag_t<T>*>(QF + query_frag<D>(w, c0 / 32 + ks)) = fq;
+          if constexpr (!GRAD) *reinterpret_cast<frag_t<T>*>(QF + query_frag<D>(w, c0 / 32 + ks)) = fq;
 #pragma unroll
           for (int ct = 0; ct < decltype(tiles)::value; ++ct) {
             const frag_t<T> fb = lds_row8(&sh.st.k[16 * ct + c][32 * ks + 8 * g16]);
@@ -165,6 +165,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
               state_col8(&sh.st.q[0][0], SP, 16 * w, 32 * t, lane);
       }
     }
+  }
+
+  if constexpr (GRAD) {
+    float* pairs = p.pairs + ((int64_t)(base + blk) * p.k_heads + hk) * (2 * kB * kB);
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = (16 * w + 4 * g16 + i) * kB + 16 * ct + c;
+        pairs[at] = qk[ct][i];
+        pairs[kB * kB + at] = kk[ct][i];
+      }
   }
 
   const int group = p.heads / p.k_heads;
@@ -258,7 +270,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
       *at *= *reinterpret_cast<const f32x4*>(&sbeta[i % 16 * 4]);
     }
     __syncthreads();
-    {
+    if constexpr (!GRAD) {
       // M = P T, five products of 16x16 blocks a wave
       auto block = [&](int ib, int jb) {
         f32x4 m = zero4();
@@ -292,19 +304,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
     if constexpr (GRAD) {
       store_matrix<T, true>(st, reinterpret_cast<T*>(p.tt) + slot * (NM * kB * kB), NM, tid);
       store_matrix<T, true>(sp, reinterpret_cast<T*>(p.pt) + slot * (NM * kB * kB), NM, tid);
+    } else {
+      __syncthreads();
+      // all planes of M, as of T: with one, its rounding (2^-9) and that of a state
+      // copied in one plane put o 2.4e-3 off where its own rounding gives 1.7e-3;
+      // with two o is at its rounding, for 6% of the call (519 -> 552 us for 2 x 8192
+      // tokens, 16 heads of 256)
+      store_matrix<T, false>(sa, reinterpret_cast<T*>(p.m) + slot * (NM * kB * kB), NM, tid);
     }
-    __syncthreads();
-    // all planes of M, as of T: with one, its rounding (2^-9) and that of a state
-    // copied in one plane put o 2.4e-3 off where its own rounding gives 1.7e-3;
-    // with two o is at its rounding, for 6% of the call (519 -> 552 us for 2 x 8192
-    // tokens, 16 heads of 256)
-    store_matrix<T, false>(sa, reinterpret_cast<T*>(p.m) + slot * (NM * kB * kB), NM, tid);
   }
 }
 
 // The state's way through one sequence's blocks, for SL value columns of one
-// head; GRAD: the same walk for the backward, which keeps V', the states and
-// the row sums o . dO in place of the output.
+// head; GRAD: the same walk for the backward, which keeps V' and the states in
+// place of the output.
 // Bound by the way from one block's state to the next, which takes three
 // exchanges between the four state waves: each multiplies its key rows of S
 // into K S (partial sums of all 64 tokens); a quarter of the tokens each, they
@@ -464,18 +477,6 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
       put_partial(part, w, 0, ksum[0], lane);
       if constexpr (TPW > 1) __builtin_amdgcn_sched_barrier(0);
       put_partial(part, w, 1, ksum[1], lane);
-      if constexpr (GRAD) {
-        if (blk && blk % kDeltaGroup == 0) {
-          float* an = p.anchor + ((((int64_t)(base / kDeltaGroup + b + blk / kDeltaGroup - 1) * p.heads + h) * CS::NSL +
-                                   slice) * 4 + w) * (TPW * 1024) + lane * 4;
-#pragma unroll
-          for (int t = 0; t < TPW; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<f32x4*>(an + (4 * t + q) * 256) =
-                  f32x4{s[t][4 * q], s[t][4 * q + 1], s[t][4 * q + 2], s[t][4 * q + 3]};
-        }
-      }
       lds_barrier();
 
       // X of the quarter (zero behind the sequence's end: K and V are)
@@ -539,23 +540,41 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
 #pragma unroll
         for (int i = 0; i < 16; ++i) so[(krow + 32 * t + state_row(i, h2)) * D + vcol] = s[t][i];
     }
-    if constexpr (GRAD) {
-      if (nblk && p.d_state_out) {  // the last group's copy: only a gradient of the final state meets it
-        float* an = p.anchor + ((((int64_t)(base / kDeltaGroup + b + (nblk - 1) / kDeltaGroup) * p.heads + h) * CS::NSL +
-                                 slice) * 4 + w) * (TPW * 1024) + lane * 4;
+  } else if constexpr (GRAD) {
+    // the state at the block's start, [dv][dk] in planes
+    auto keep_state = [&](int blk) {
+      const T* copy = os + (kTwoCopies ? (blk & 1) * COPY : 0);
+      T* sn = reinterpret_cast<T*>(p.snap) + slot_of(blk) * (NP * D * D);
 #pragma unroll
-        for (int t = 0; t < TPW; ++t)
+      for (int pl = 0; pl < NP; ++pl)
+        for (int i = tid - 256; i < CS::SL * D / 8; i += 256) {
+          const int row = i / (D / 8), at = i % (D / 8) * 8, col = slice * CS::SL + (row & 32) + col_at(row & 31);
+          copy8(sn + pl * D * D + (int64_t)col * D + at, copy + pl * CS::SPLANE + row * CS::SPITCH + at);
+        }
+    };
+    for (int blk = 0; blk < nblk; ++blk) {
+      lds_barrier();
+      if constexpr (!kTwoCopies) keep_state(blk);
+      lds_barrier();
+      lds_barrier();
+      if constexpr (kTwoCopies) keep_state(blk);
+      // V' in planes of whole tensors
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4*>(an + (4 * t + q) * 256) =
-                f32x4{s[t][4 * q], s[t][4 * q + 1], s[t][4 * q + 2], s[t][4 * q + 3]};
+      for (int pl = 0; pl < NP; ++pl) {
+        const auto ur = value_rsrc(reinterpret_cast<const T*>(p.u) + pl * (int64_t)p.total * vs, blk);
+#pragma unroll
+        for (int g = 0; g < CG; ++g) {
+          const vec4_t<T> x = *reinterpret_cast<const vec4_t<T>*>(ov + pl * OPLANE + row_of(2 * g, c) * PITCH + r4);
+          const vec4_t<T> y = *reinterpret_cast<const vec4_t<T>*>(ov + pl * OPLANE + row_of(2 * g + 1, c) * PITCH + r4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) buf_put_pair(ur, pair_off[i] + 32 * g * SZ, (float)x[i], (float)y[i], tag);
+        }
       }
     }
   } else {
     frag_t<T> qf[D / 32], mf[2][NM];
 #pragma unroll
     for (int pl = 0; pl < NM; ++pl) mf[1][pl] = zero_frag<T>();
-    PairOf<T> dout[CG][4];
     f32x4 eg;
     auto load_queries = [&](int blk) {
       const auto rs = key_rsrc(p.qf, blk);
@@ -570,13 +589,6 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
         for (int ks = 0; ks < 2; ++ks)
           if (ks <= (w >> 1)) mf[ks][pl] = buf_frag(mr, lane_off, mat_frag(pl, w, ks) * SZ, tag);
       eg = buf_f4(vec_rsrc(blk), r4 * 4, 0);
-      if constexpr (GRAD) {
-        const auto dr = value_rsrc(p.dout, blk);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int g = 0; g < CG; ++g) dout[g][i] = buf_pair(dr, pair_off[i] + 32 * g * SZ, tag);
-      }
     };
     f32x4 o[CT];
     auto query_state = [&](int blk) {
@@ -590,14 +602,6 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl)
             o[ct] = mma(qf[ks], lds_row8(copy + pl * CS::SPLANE + row_of(ct, c) * CS::SPITCH + 32 * ks + 8 * g16), o[ct]);
-      if constexpr (GRAD) {
-        // the state at the block's start, [dv][dk], for the gradients of q and k
-        T* sn = reinterpret_cast<T*>(p.snap) + slot_of(blk) * D * D;
-        for (int i = tid - 256; i < CS::SL * D / 8; i += 256) {
-          const int row = i / (D / 8), at = i % (D / 8) * 8, col = slice * CS::SL + (row & 32) + col_at(row & 31);
-          copy8(sn + (int64_t)col * D + at, copy + row * CS::SPITCH + at);
-        }
-      }
     };
     load_queries(0);
     load_rest(0);
@@ -619,36 +623,11 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
           o[ct] = mma_planes(mf[ks], x, o[ct]);
         }
       }
-      if constexpr (!GRAD) {
-        const auto orsrc = value_rsrc(p.o, blk);
+      const auto orsrc = value_rsrc(p.o, blk);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int g = 0; g < CG; ++g)
-            buf_put_pair(orsrc, pair_off[i] + 32 * g * SZ, o[2 * g][i], o[2 * g + 1][i], tag);
-      } else {
-        f32x4 dot = zero4();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) dot[i] += o[ct][i] * dout[ct >> 1][i].get(ct & 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dot[i] = sum16(dot[i]);
-        if (c == 0) *reinterpret_cast<f32x4*>(p.odo + (slot_of(blk) * CS::NSL + slice) * kB + r4) = dot;
-        // V' in planes of whole tensors
-#pragma unroll
-        for (int pl = 0; pl < NP; ++pl) {
-          const auto ur = value_rsrc(reinterpret_cast<const T*>(p.u) + pl * (int64_t)p.total * vs, blk);
-#pragma unroll
-          for (int g = 0; g < CG; ++g) {
-            const vec4_t<T> x = *reinterpret_cast<const vec4_t<T>*>(ov + pl * OPLANE + row_of(2 * g, c) * PITCH + r4);
-            const vec4_t<T> y = *reinterpret_cast<const vec4_t<T>*>(ov + pl * OPLANE + row_of(2 * g + 1, c) * PITCH + r4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              buf_put_pair(ur, pair_off[i] + 32 * g * SZ, (float)x[i], (float)y[i], tag);
-          }
-        }
-      }
+        for (int g = 0; g < CG; ++g) buf_put_pair(orsrc, pair_off[i] + 32 * g * SZ, o[2 * g][i], o[2 * g + 1][i], tag);
       load_queries(blk + 1);
       load_rest(blk + 1);
     }
@@ -691,29 +670,21 @@ hipError_t launch_delta_fwd(const DeltaParams& p, int d, int dtype, hipStream_t 
   return launch_delta_forward(p, d, dtype, false, stream);
 }
 
-template <typename T, int D>
-static void chain_layout(DeltaLayout& l) {
-  l.slices = ChainShape<T, D>::NSL;
+template <typename T>
+static void plane_layout(DeltaLayout& l) {
   l.planes = Planes<T>::N;
   l.mat_planes = MatPlanes<T, true>::N;
   l.mat_plane = kB * kB * sizeof(T);
 }
 
-DeltaLayout delta_layout(int batch, int seqlen, int d, int dtype, bool packed, int total) {
+DeltaLayout delta_layout(int batch, int seqlen, int dtype, bool packed, int total) {
   DeltaLayout l;
   const size_t per = ((size_t)seqlen + kB - 1) / kB;
   l.blocks = packed ? (size_t)total / kB + batch : per * batch;
-  // group g of a sequence is numbered (its first block) / kDeltaGroup + its place in the batch + g
-  l.groups = l.blocks / kDeltaGroup + batch + 1;
-  if (dtype == 1) {
-    if (d == 64) chain_layout<bf16, 64>(l);
-    else if (d == 128) chain_layout<bf16, 128>(l);
-    else chain_layout<bf16, 256>(l);
-  } else {
-    if (d == 64) chain_layout<float, 64>(l);
-    else if (d == 128) chain_layout<float, 128>(l);
-    else chain_layout<float, 256>(l);
-  }
+  if (dtype == 1)
+    plane_layout<bf16>(l);
+  else
+    plane_layout<float>(l);
   return l;
 }
 
