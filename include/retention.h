@@ -293,7 +293,10 @@ ret_status_t retention_chunkwise_error(const void *workspace, size_t workspace_b
  *     state             [batch, v_heads, dk, dv]       fp32
  * log_decay is meant to be <= 0 (-infinity: the state is forgotten; values
  * below -1e5 count as that) and beta in [0, 2] with keys of length at most 1;
- * then no state grows. Other values are computed as they stand. There is no
+ * then no state grows. Other values are computed as they stand. A decode step
+ * and the first token of a chunkwise call whose factor is 0 in 32 bits forget
+ * whatever the given state holds, NaN and infinity too, so a slot can be used
+ * again without clearing it; at a later token the state has to be finite. There is no
  * rotation, GroupNorm or gate in these calls (retention_head_norm_fwd follows).
  *
  * Packed sequences: with cu_seqlens (DEVICE int32 [batch + 1], as in

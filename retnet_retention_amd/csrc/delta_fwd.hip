@@ -392,7 +392,9 @@ __global__ __launch_bounds__(512, D == 128 && !GRAD ? 4 : 2) void delta_chain_ke
     f32x16 s[TPW];
 #pragma unroll
     for (int t = 0; t < TPW; ++t) s[t] = zero16();
-    if (p.state_in) {
+    // A first token that forgets starts from zeros whatever the state holds (a factor
+    // of zero would keep a NaN or an infinity); an empty sequence passes it on.
+    if (p.state_in && (nblk == 0 || p.vec[slot_of(0) * (4 * kB)] != 0.f)) {
       const float* si = p.state_in + (int64_t)bh * D * D;
 #pragma unroll
       for (int t = 0; t < TPW; ++t)

@@ -60,7 +60,8 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
   const float a = expf(p.log_decay[bh]), beta = p.beta[bh];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    s[i] *= a;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[i][e] = a == 0.f ? 0.f : a * s[i][e];  // forgotten, NaN and infinity too
     ak += kr[i] * s[i];
     aq += qr[i] * s[i];
   }
