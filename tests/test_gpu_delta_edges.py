@@ -59,3 +59,124 @@ def test_an_empty_sequence_passes_any_state_on():
     o = rr.delta_chunkwise_fwd(*(y[k] for k in KEYS), state_in=s, state_out=out, cu_seqlens=cu, max_seqlen=40, check=True)
     assert torch.isfinite(o.float()).all() and torch.isfinite(out[1]).all()
     np.testing.assert_array_equal(f64(out[0]), f64(s[0]))
+
+
+def free_memory(need):
+    """Skips where the card holds less (a smaller device, or a shared one)."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+
+
+@pytest.mark.parametrize("slots", [False, True])
+def test_states_too_large_for_the_caches(slots):
+    """Pools above 512 MiB are streamed past the caches: the bits of smaller calls."""
+    b, h, d = 132, 16, 256
+    assert b * h * d * d * 4 > 512 << 20
+    g = torch.Generator(device=DEV).manual_seed(44)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    q, k, v = (r(b, 1, n, d).bfloat16() / 16 for n in (8, 8, h))
+    ld, beta = -torch.rand(b, 1, h, generator=g, device=DEV), torch.rand(b, 1, h, generator=g, device=DEV)
+    pool = r(b, h, d, d)
+    at = torch.randperm(b, generator=g, device=DEV).to(torch.int32) if slots else None
+    want, outs = pool.clone(), []
+    for i in range(0, b, 33):
+        part = [t[i:i + 33].contiguous() for t in (q, k, v, ld, beta)]
+        if slots:
+            outs.append(rr.delta_recurrent_step(*part, want, slots=at[i:i + 33].contiguous()))
+        else:
+            outs.append(rr.delta_recurrent_step(*part, want[i:i + 33]))
+    o = rr.delta_recurrent_step(q, k, v, ld, beta, pool, slots=at)
+    assert torch.equal(o, torch.cat(outs)) and torch.equal(pool, want)
+
+
+def test_a_slot_behind_2_31_elements():
+    h, d, n = 16, 256, 2060
+    assert (n - 2) * h * d * d > 2 ** 31
+    free_memory(12 << 30)
+    x = make(45, 2, 1, 2, h, d, "bf16")
+    y = dev(x)
+    pool = torch.zeros(n, h, d, d, device=DEV)
+    pool[n - 1], pool[n - 2] = y["s0"][0], y["s0"][1]
+    slots = torch.tensor([n - 1, n - 2], dtype=torch.int32, device=DEV)
+    o = rr.delta_recurrent_step(*(y[k] for k in KEYS), pool, slots=slots)
+    s = y["s0"].clone()
+    o1 = rr.delta_recurrent_step(*(y[k] for k in KEYS), s)
+    assert torch.equal(o, o1) and torch.equal(pool[n - 1], s[0]) and torch.equal(pool[n - 2], s[1])
+    assert (pool[:n - 2] == 0).all()
+
+
+def test_backward_behind_2_31_elements():
+    """The last of two packed sequences starts behind 2^31 elements of v and of its
+    gradient (and its states behind 2^33): the bits of that sequence alone."""
+    h, d, first, last = 128, 256, 66000, 100
+    n = first + last
+    assert first * h * d > 2 ** 31
+    free_memory(160 << 30)
+    g = torch.Generator(device=DEV).manual_seed(46)
+    v = torch.randn(n, h, d, generator=g, device=DEV, dtype=torch.bfloat16)
+    k = torch.randn(n, 1, d, generator=g, device=DEV, dtype=torch.bfloat16) / 16
+    ld, beta = -torch.rand(n, h, generator=g, device=DEV), torch.rand(n, h, generator=g, device=DEV)
+    cu = torch.tensor([0, first, n], dtype=torch.int32, device=DEV)
+    got = rr.delta_chunkwise_bwd(k, k, v, ld, beta, v, cu_seqlens=cu, max_seqlen=first, check=True)
+    tail = [t[first:][None].contiguous() for t in (k, k, v, ld, beta, v)]
+    for a, b in zip(got, rr.delta_chunkwise_bwd(*tail)):
+        assert torch.equal(a[first:], b[0])
+        assert torch.isfinite(a[first - 64:first].float()).all()
+    del got
+    torch.cuda.empty_cache()
+
+
+# With one key many times over a written value is beta times what the writes before it
+# left, a sum of up to thirty terms of its own size that each carry an error of their
+# own: sqrt(30) < 6 times the errors of other inputs.
+REPEATED = 6
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_strength_extremes_in_bf16(d):
+    """beta 0, 1 and 2, one key many times over: values replaced and reflected."""
+    from test_gpu_delta_accuracy import CARRIED, ROUNDED_ONCE, near_norm, rounded
+
+    x = make(47, 1, 140, 1, 2, d, "bf16")
+    x["beta"][0, 5:30] = 0.0
+    x["beta"][0, 30:70] = 1.0
+    x["beta"][0, 70:80] = 2.0
+    x["k"][0, 32:60] = x["k"][0, 31]
+    y, args = dev(x), [f64(x[k]) for k in KEYS]
+    s = torch.empty_like(y["s0"])
+    o = rr.delta_chunkwise_fwd(*(y[k] for k in KEYS), state_in=y["s0"], state_out=s)
+    ro, rs = oracle.delta(*args, state=f64(x["s0"]))
+    got = rr.delta_chunkwise_bwd(*(y[k] for k in KEYS), y["dout"], state_in=y["s0"], d_state_out=y["ds"])
+    ref = oracle.delta_grad(*args, f64(x["dout"]), state=f64(x["s0"]), d_state=f64(x["ds"]))
+    row = lambda t: (f64(t) if isinstance(t, torch.Tensor) else t).reshape(1, -1)  # noqa: E731
+    for name, a, r in (("o", o, ro), ("dq", got[0], ref[0]), ("dk", got[1], ref[1]), ("dv", got[2], ref[2])):
+        near_norm(row(a), row(rounded(r)), ROUNDED_ONCE * REPEATED ** 0.5, name)
+    for name, a, r in (("state", s, rs), ("dlog_decay", got[3], ref[3]), ("dbeta", got[4], ref[4]), ("ds", got[5], ref[5])):
+        near_norm(row(a), row(r), CARRIED * REPEATED, name)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_decay_extremes_in_bf16(d):
+    """-infinity forgets, 0 keeps, strong decays underflow, all in one block."""
+    from test_gpu_delta_accuracy import CARRIED, near_norm, near_rounded
+
+    x = make(48, 1, 150, 1, 2, d, "bf16")
+    for at, v in ((10, -np.inf), (70, -1e30), (71, -200.0)):
+        x["g"][0, at] = v
+    x["g"][0, 20:40] = 0.0
+    x["g"][0, 100:103, 0] = -3e4
+    y = dev(x)
+    s = torch.empty_like(y["s0"])
+    o = rr.delta_chunkwise_fwd(*(y[k] for k in KEYS), state_in=y["s0"], state_out=s)
+    ro, rs = oracle.delta(*(f64(x[k]) for k in KEYS), state=f64(x["s0"]))
+    near_rounded(o, ro, "o")
+    got = rr.delta_chunkwise_bwd(*(y[k] for k in KEYS), y["dout"], state_in=y["s0"], d_state_out=y["ds"])
+    x["g"] = x["g"].clamp(min=-2000.0)  # a factor of 0 in 64 bits too, and finite
+    ref = oracle.delta_grad(*(f64(x[k]) for k in KEYS), f64(x["dout"]), state=f64(x["s0"]), d_state=f64(x["ds"]))
+    for name, a, r in zip(("dq", "dk", "dv"), got, ref):
+        near_rounded(a, r, name)
+    row = lambda t: (f64(t) if isinstance(t, torch.Tensor) else t).reshape(1, -1)  # noqa: E731
+    near_norm(row(s), row(rs), CARRIED, "state")
+    for name, a, r in zip(("dlog_decay", "dbeta", "dstate"), got[3:], ref[3:]):
+        near_norm(row(a), row(r), CARRIED, name)
