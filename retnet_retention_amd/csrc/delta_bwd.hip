@@ -335,12 +335,14 @@ __device__ __forceinline__ float scan64(float x, int lane) {
 // of dA with K K^T), what later tokens read of the state before the block (x),
 // what earlier ones leave in the state after it (y), and what passes through the
 // block (z). Nothing cancels that lacks the factor, so the error carries it too.
-// Bound by the states' way into LDS: 324 us for 1280 blocks of 256 x 256 (671 MB
-// of states, 210 MB of rows), where one bf16 value a state took 161 and left dq
-// 2.9e-3 and dk 3.2e-3 off (now 1.7e-3, their own rounding); 135 us with two value
-// heads of 128 a key head. Shared key heads keep dq and dk beside the sums of a
-// head: 40 (bf16) and 79 (fp32) vector registers of a lane spill at 256, 57 and 36
-// at 64, written and read once a value head.
+// Bound by memory while the states pass (two thirds of a block's 49 us: 42 KB a
+// step of 2.1 us on each of 256 CUs), then by one workgroup a CU working alone on
+// what follows: 307 us for 1280 blocks of 256 x 256 (671 MB of states, 210 MB of
+// rows). One bf16 value a state took 161 and left dq 2.9e-3 and dk 3.2e-3 off (now
+// 1.7e-3, their own rounding). 126 us with two value heads of 128 a key head.
+// Shared key heads keep dq and dk beside the sums of a head: 39 (bf16) and 74
+// (fp32) vector registers of a lane spill at 256, 30 and 42 at 64, written and read
+// once a value head; fp32 at 128 without sharing spills 4 for two workgroups a CU.
 // Products of a wave are straight lines of matrix instructions with no branch
 // among them.
 template <typename T, int D, bool GROUPED>
@@ -356,11 +358,16 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
   // in LDS dO has as many planes as the others (zeros), so that the tiles of dP
   // and dA are the same products
   constexpr int ROWS = 3 * NP * kB * PA;
-  struct Stage { char tiles[2][2 * NP][ST::BYTES]; T rows[2][ROWS]; };
+  constexpr int TILES = 2 * NP * ST::BYTES, MAT = kB * PM;
+  constexpr int S_BYTES = NP * MAT * SZ;  // dA + dA^T, in the place of the first tiles
   struct Weights { float w[2][kB][PW]; };
-  struct Mats { T p[NP][kB * PM], pt[NP][kB * PM], s[NP][kB * PM]; };
-  union Shared { Stage st; Weights wt; Mats m; __device__ Shared() {} };
-  __shared__ __attribute__((aligned(1024))) Shared sh;
+  struct Mats { T p[NP][MAT], pt[NP][MAT]; };
+  union Rows { T rows[2][ROWS]; Weights wt; Mats m; __device__ Rows() {} };
+  // Objects of their own: the compiler lets reads of one pair of tiles pass the
+  // direct loads on their way into the other only where it knows them apart.
+  __shared__ __attribute__((aligned(1024))) char tiles0[TILES > S_BYTES ? TILES : S_BYTES];
+  __shared__ __attribute__((aligned(1024))) char tiles1[TILES];
+  __shared__ __attribute__((aligned(16))) Rows sh;
   __shared__ double sg[kB];
   __shared__ float sx[NW][kB], sy[NW][kB], sw[NW][kB], sz[NW], sbeta[kB];
   T* const tag = nullptr;
@@ -391,11 +398,11 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
     const int cr = (tid % CHUNKS) / 2, cj = tid % 2 * 8;  // row and column of the thread's chunks
     Raw8<T> raw[RN];
     auto operand_of = [&](int i) { return uniform_i((tid + i * 2 * D) / CHUNKS); };
-    auto ask = [&](int d0, int buf) {
+    auto ask = [&](int d0, char* tiles) {
 #pragma unroll
       for (int pl = 0; pl < NP; ++pl) {
-        sloads.issue(sh.st.tiles[buf][pl], SN + pl * D * D, D, d0, w);
-        sloads.issue(sh.st.tiles[buf][NP + pl], DN + pl * D * D, D, d0, w);
+        sloads.issue(tiles + pl * ST::BYTES, SN + pl * D * D, D, d0, w);
+        sloads.issue(tiles + (NP + pl) * ST::BYTES, DN + pl * D * D, D, d0, w);
       }
 #pragma unroll
       for (int i = 0; i < RN; ++i) {
@@ -413,7 +420,7 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
         const int m = operand_of(i);
         if (m < NR) {
           const frag_t<T> x = __builtin_bit_cast(frag_t<T>, raw[i]);
-          T* to = sh.st.rows[buf] + ((m ? NP + m - 1 : 0) * kB + cr) * PA + cj / 2;
+          T* to = sh.rows[buf] + ((m ? NP + m - 1 : 0) * kB + cr) * PA + cj / 2;
           *reinterpret_cast<vec4_t<T>*>(to) = vec4_t<T>{x[0], x[1], x[2], x[3]};
           *reinterpret_cast<vec4_t<T>*>(to + 8) = vec4_t<T>{x[4], x[5], x[6], x[7]};
         }
@@ -433,7 +440,7 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
     }
     if constexpr (NP > 1) {
       for (int i = tid; i < 2 * kB * PA / 8; i += 2 * D)
-        store8_zero(sh.st.rows[i / (kB * PA / 8)] + kB * PA + i % (kB * PA / 8) * 8);
+        store8_zero(sh.rows[i / (kB * PA / 8)] + kB * PA + i % (kB * PA / 8) * 8);
     }
 
     f32x16 acc[TW];  // [s][r]: V' dO^T and V' dv^T
@@ -442,21 +449,19 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
     // dO S^T, V' dS^T and dv S^T over the value columns, and <S, dS>
     f32x16 a0[2] = {zero16(), zero16()}, a1[2] = {zero16(), zero16()}, a2[2] = {zero16(), zero16()};
     float z = 0.f;
-    ask(0, 0);
-    for (int d0 = 0; d0 < D; d0 += DV) {
-      const int buf = d0 / DV % 2;
+    auto step = [&](int d0, const char* tiles, char* next, int buf) {
       put_rows(buf);
-      __builtin_amdgcn_s_waitcnt(0);  // the tiles (LDS loads run past the compiler's counting)
+      __builtin_amdgcn_s_waitcnt(0);  // the tiles
       lds_barrier();
-      if (d0 + DV < D) ask(d0 + DV, buf ^ 1);
+      if (d0 + DV < D) ask(d0 + DV, next);
       auto row = [&](int plane, int rt) {
-        return lds_row8(sh.st.rows[buf] + (plane * kB + 32 * rt + n) * PA + 8 * h2);
+        return lds_row8(sh.rows[buf] + (plane * kB + 32 * rt + n) * PA + 8 * h2);
       };
       frag_t<T> fs[NP], fd[NP];
 #pragma unroll
       for (int pl = 0; pl < NP; ++pl) {
-        fs[pl] = state_tile_col8<ST>(sh.st.tiles[buf][pl], 0, 32 * w, lane, tag);
-        fd[pl] = state_tile_col8<ST>(sh.st.tiles[buf][NP + pl], 0, 32 * w, lane, tag);
+        fs[pl] = state_tile_col8<ST>(tiles + pl * ST::BYTES, 0, 32 * w, lane, tag);
+        fd[pl] = state_tile_col8<ST>(tiles + (NP + pl) * ST::BYTES, 0, 32 * w, lane, tag);
       }
       // (products of two rests are below 2^-17 of the first and left out)
 #pragma unroll
@@ -486,6 +491,11 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
       for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int j = 0; i + j < NP; ++j) z = dot_frag(fs[i], fd[j], z);
+    };
+    ask(0, tiles0);
+    for (int d0 = 0; d0 < D; d0 += 2 * DV) {
+      step(d0, tiles0, tiles1, 0);
+      step(d0 + DV, tiles1, tiles0, 1);
     }
     frag_t<T> fq[4], fk[4];  // queries and keys by columns, the wave's 32
 #pragma unroll
@@ -583,6 +593,7 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
       }
     }
     // dP (both ways round) and dA + dA^T as operands, in planes
+    T* smat = reinterpret_cast<T*>(tiles0);
 #pragma unroll
     for (int k = 0; k < TW; ++k) {
       const int task = w + k * NW, which = task >> 2, rt = task >> 1 & 1, st = task & 1;
@@ -607,8 +618,8 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
             for (int i = 0; i < 4; ++i) {
               const int s = s0 + 8 * q + i;
               if (s <= r) {
-                sh.m.s[pl][r * PM + s] = y[i];
-                sh.m.s[pl][s * PM + r] = y[i];
+                smat[pl * MAT + r * PM + s] = y[i];
+                smat[pl * MAT + s * PM + r] = y[i];
               }
             }
           }
@@ -636,7 +647,7 @@ __global__ __launch_bounds__(2 * D, D > 64 && !GROUPED ? 2 : 1) void delta_qk_gr
         for (int pl = 0; pl < NP; ++pl) {
           dk[rt] = mma32(mrow(sh.m.pt[pl], rt, ks), fq[ks], dk[rt]);
           dq[rt] = mma32(mrow(sh.m.p[pl], rt, ks), fk[ks], dq[rt]);
-          dk[rt] = mma32(mrow(sh.m.s[pl], rt, ks), fk[ks], dk[rt]);
+          dk[rt] = mma32(mrow(smat + pl * MAT, rt, ks), fk[ks], dk[rt]);
         }
   }
   T* DQ = reinterpret_cast<T*>(p.dq) + row0 * qs + hk * D + 32 * w + state_col(n);
