@@ -28,9 +28,9 @@ hipError_t launch_delta_forward(const DeltaParams& p, int d, int dtype, bool gra
 // The gradient of the state, from a sequence's last block to its first: the
 // same division of work and the same three exchanges as delta_chain_kernel.
 // The second four waves form P^T dO, put scale e^G dO where the state waves
-// read it, and write dv. 351 us for 4 sequences of 32 blocks, 10 heads
+// read it, and write dv. 346 us for 4 sequences of 32 blocks, 10 heads
 // of 256 (320 workgroups on 256 CUs: two rounds, the second a quarter full), and
-// the forward's walk before it 241; 170 and 132 us for 63 blocks, 16 heads of
+// the forward's walk before it 235; 167 and 129 us for 63 blocks, 16 heads of
 // 128 (64 workgroups, 2.7 us a block). With 128 registers a lane, for two
 // workgroups a CU at 128, both spill: 720 us for a backward that took 407.
 template <typename T, int D>
@@ -337,9 +337,9 @@ __device__ __forceinline__ float scan64(float x, int lane) {
 // block (z). Nothing cancels that lacks the factor, so the error carries it too.
 // Bound by memory while the states pass (two thirds of a block's 49 us: 42 KB a
 // step of 2.1 us on each of 256 CUs), then by one workgroup a CU working alone on
-// what follows: 307 us for 1280 blocks of 256 x 256 (671 MB of states, 210 MB of
+// what follows: 297 us for 1280 blocks of 256 x 256 (671 MB of states, 210 MB of
 // rows). One bf16 value a state took 161 and left dq 2.9e-3 and dk 3.2e-3 off (now
-// 1.7e-3, their own rounding). 126 us with two value heads of 128 a key head.
+// 1.7e-3, their own rounding). 124 us with two value heads of 128 a key head.
 // Shared key heads keep dq and dk beside the sums of a head: 39 (bf16) and 74
 // (fp32) vector registers of a lane spill at 256, 30 and 42 at 64, written and read
 // once a value head; fp32 at 128 without sharing spills 4 for two workgroups a CU.

@@ -55,9 +55,9 @@ __device__ __forceinline__ void store_matrix(const float (*m)[kPrepPitch], T* ou
 // sum_k A_ik T_kj, in fp32 products; the columns take their beta at the end.
 // The cumulative decays are summed in 64 bits: E is the exponential of a
 // difference of two sums that may both be large.
-// All blocks at once, so bound by what passes: 157 us for 4096 blocks of bf16
-// keys of 256 (268 MB read, 507 MB written: 4.9 TB/s, where a large copy
-// reaches 5.2); 98 us for 32 value heads of 128 over 10287 packed tokens. A
+// All blocks at once, so bound by what passes: 158 us for 4096 blocks of bf16
+// keys of 256 (268 MB read, 540 MB written: 5.1 TB/s, where a large copy
+// reaches 5.2); 99 us for 32 value heads of 128 over 10287 packed tokens. A
 // short sequence sees one block's latency, 13 us.
 template <typename T, int D, bool GRAD>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_prep_kernel(DeltaParams p) {
@@ -329,8 +329,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && D > 64 ? 2 : 3) void delta_p
 // both ways round, not through a tile in LDS, and what a block reads is asked
 // for a block ahead, spread over the step: a wave that asks for much at once
 // waits until the caches have taken it.
-// Measured: 415 us for 128 blocks a sequence of 256 x 256 states, 3.2 us a
-// block; 256 workgroups of 32 columns, one a CU. 337 us for 65 blocks at most
+// Measured: 423 us for 128 blocks a sequence of 256 x 256 states, 3.3 us a
+// block; 256 workgroups of 32 columns, one a CU. 355 us for 65 blocks at most
 // of 128 x 128 states (two workgroups a CU, 128 registers a lane). A block's 6.8
 // MFLOP of a workgroup are 0.7 us at a CU's dense rate and its 124 KB 0.8 us at
 // the caches' 64 bytes a clock: the rest is latency at the exchanges. X and V'

@@ -156,8 +156,16 @@ __device__ __forceinline__ void normalize_grad(float* g, const float* n, float r
 }
 
 // f(NormRow of the width's division) for rows of `width` elements. The backward
-// (BWD) holds a dozen rows' worth of registers, so its rows of up to 8192 are
-// spread over 512 lanes (256 registers each), not 1024 (128).
+// (BWD) holds a dozen rows' worth of registers, so its rows of 4097 to 8192 are
+// spread over 512 lanes (256 registers each), not 1024 (128, of which 72 more
+// spill). That does not hold them all either: the residual norm's backward spills
+// 46 registers of a lane (bf16) or 109 (fp32) there, and above 8192, where a row
+// takes the 1024 lanes a workgroup has, 304 or 423; the head norm's 217 or 168
+// there. Measured with all weights: 5.3 and 4.2 TB/s (fp32, bf16) at 4096, 2.6 and
+// 2.8 at 8192, 0.8 and 0.7 at 16384; the head norm's backward 5.2 and 4.6 at
+// 8192, 2.1 and 1.6 at 16384. Widths that are no multiple of 8 take single
+// elements: the residual norm's forward 4.5 and 1.4 TB/s at 16380, 5.2 and 4.6 at
+// 16384.
 template <typename T, bool BWD, typename F>
 hipError_t with_rows(int width, bool vec, F&& f) {
 #define RET_NORM_CASE(LIMIT, LPR, NV) \

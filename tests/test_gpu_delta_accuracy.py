@@ -160,3 +160,29 @@ def test_decay_gradient_before_loud_gradients(at, dtype):
     err = np.abs(got[:, at] - ref[:, at]) / np.sqrt((terms ** 2).sum(1))
     print(f"  at: {err} (bar {gates_bar(dtype):.2e})", flush=True)
     assert (err <= gates_bar(dtype)).all()
+
+
+@pytest.mark.parametrize("dtype,hk,h,d", [("bf16", 2, 4, 128), ("f32", 1, 2, 64), ("bf16", 1, 2, 256)])
+def test_packed_gradients_by_head(dtype, hk, h, d):
+    lens = [130, 0, 1, 66, 64]
+    x = make(37, len(lens), max(lens), hk, h, d, dtype, lens=lens)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    got = grads(x, 0.25, cu_seqlens=cu, max_seqlen=max(lens), check=True)
+    ref, rs = oracle.packed(oracle.delta_grad, lens, [f64(x[k]) for k in (*KEYS, "dout")], state=f64(x["s0"]),
+                            d_state=f64(x["ds"]), scale=0.25)
+    if dtype == "bf16":
+        for name, g, r in zip(("dq", "dk", "dv"), got, ref):
+            near_rounded(g, r, name)
+    for name, g, r in zip(("dlog_decay", "dbeta"), got[3:5], ref[3:]):
+        near_norm(heads_first(g), heads_first(r), gates_bar(dtype), name)
+    near_norm(f64(got[5]).reshape(len(lens) * h, -1), rs.reshape(len(lens) * h, -1), gates_bar(dtype), "dstate")
+
+
+@pytest.mark.parametrize("b,n,hk,h,d", SIZES)
+def test_the_backward_takes_three_values_for_its_matrices(b, n, hk, h, d):
+    """d beta = dv . V' / beta^2. With the 64 x 64 matrices and what they multiply in
+    24 bits, the operands of two bf16 values on its way are the state, its gradient,
+    dv and V': sqrt(4) 2^-18.4, and the bar a third more, 2^-17 = 7.6e-6. With two values
+    for the matrices too, heads of these sizes were 6.8e-6 to 9.0e-6 off."""
+    x = make(38, b, n, hk, h, d, "bf16")
+    near_norm(heads_first(grads(x, 0.25)[4]), heads_first(reference(x, 0.25)[4]), 2.0 ** -17, "dbeta")

@@ -180,3 +180,41 @@ def test_decay_extremes_in_bf16(d):
     near_norm(row(s), row(rs), CARRIED, "state")
     for name, a, r in zip(("dlog_decay", "dbeta", "dstate"), got[3:], ref[3:]):
         near_norm(row(a), row(r), CARRIED, name)
+
+
+def workspace(call, fill):
+    """A workspace of `call`'s size with every byte `fill` (255: NaN in every type)."""
+    need = []
+    with pytest.raises(rr.RetentionError):
+        call(torch.empty(16, dtype=torch.uint8, device=DEV))
+    for size in (1 << i for i in range(16, 36)):
+        try:
+            call(torch.empty(size, dtype=torch.uint8, device=DEV))
+            need.append(size)
+            break
+        except rr.RetentionError:
+            continue
+    return torch.full((need[0],), fill, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hk,h,lens", [(2, 2, None), (1, 3, None), (2, 2, [65, 0, 1, 130]), (1, 2, [64, 63])])
+def test_nothing_of_the_workspace_is_read_before_it_is_written(dtype, d, hk, h, lens):
+    """The same bits whatever the workspace held, call after call, every variant of the kernels."""
+    b, n = (len(lens), max(lens)) if lens else (2, 130)
+    x = make(49, b, n, hk, h, d, dtype, lens=lens)
+    y, more = dev(x), {}
+    if lens:
+        more = dict(cu_seqlens=torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV), max_seqlen=n)
+    s = torch.empty_like(y["s0"])
+    fwd = lambda ws: [rr.delta_chunkwise_fwd(*(y[k] for k in KEYS), state_in=y["s0"], state_out=s, workspace=ws,  # noqa: E731
+                                             **more), s.clone()]
+    bwd = lambda ws: list(rr.delta_chunkwise_bwd(*(y[k] for k in KEYS), y["dout"], state_in=y["s0"],  # noqa: E731
+                                                 d_state_out=y["ds"], workspace=ws, **more))
+    for call in (fwd, bwd):
+        ref = call(workspace(call, 0))
+        ws = workspace(call, 255)
+        for _ in range(3):
+            for a, r in zip(call(ws), ref):
+                assert torch.isfinite(a.float()).all() and torch.equal(a, r)
