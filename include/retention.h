@@ -314,7 +314,8 @@ ret_status_t retention_chunkwise_error(const void *workspace, size_t workspace_b
  * states and gradients a call returns are good to a few 1e-6. A NaN or
  * infinity in a token reaches no other sequence and no output of an earlier
  * block of 64 tokens. A batch may be padded with tokens of log_decay 0 and
- * beta 0, which leave the state as it is, if their keys and values are finite.
+ * beta 0, which leave the state as it is, if their keys and values are finite
+ * and small enough that k . k is too.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t batch;    /* >= 1: sequences                                         */
