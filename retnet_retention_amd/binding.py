@@ -650,7 +650,8 @@ def delta_chunkwise_fwd(q, k, v, log_decay, beta, *, scale=1.0, state_in=None, s
     v_heads]; returns the output (v's shape) and fills state_out (fp32 [batch,
     v_heads, d, d], may be state_in itself) if it is given. Packed sequences:
     [total_tokens, heads, d] tensors with cu_seqlens (GPU int32 [batch + 1])
-    and max_seqlen; rows outside every sequence are left as they were. check:
+    and max_seqlen; rows outside every sequence are left as they were. A first
+    token with log decay -infinity forgets whatever state_in holds. check:
     synchronize and raise RetentionError if cu_seqlens had to be clamped
     (check_chunkwise does the same later for a caller's workspace)."""
     out = torch.empty_like(v) if out is None else out
@@ -704,7 +705,8 @@ def delta_recurrent_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=No
     output. state: fp32 [batch, v_heads, d, d], or with `slots` (GPU int32
     [batch]) a pool [num_slots, v_heads, d, d] of which sequence b uses slot
     slots[b]; a slot that is negative, outside the pool or named by an earlier
-    sequence is inactive (its output is zero)."""
+    sequence is inactive (its output is zero). Log decay -infinity forgets
+    whatever the slot holds."""
     out = torch.empty_like(v) if out is None else out
     batch, seqlen, _ = _delta_inputs(q, k, v, log_decay, beta, "out", out, None, None)
     if seqlen != 1:
