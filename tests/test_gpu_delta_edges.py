@@ -218,3 +218,65 @@ def test_nothing_of_the_workspace_is_read_before_it_is_written(dtype, d, hk, h, 
         for _ in range(3):
             for a, r in zip(call(ws), ref):
                 assert torch.isfinite(a.float()).all() and torch.equal(a, r)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_a_loose_bound_on_the_lengths(dtype, d):
+    """max_seqlen far above every length: the bits of the tight bound, both directions."""
+    lens = [70, 0, 200, 1]
+    x = make(50, len(lens), 200, 1, 2, d, dtype, lens=lens)
+    y = dev(x)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    outs = []
+    for bound in (200, 100000):
+        s = torch.empty_like(y["s0"])
+        o = rr.delta_chunkwise_fwd(*(y[k] for k in KEYS), state_in=y["s0"], state_out=s, cu_seqlens=cu, max_seqlen=bound,
+                                   check=True)
+        outs.append([o, s, *rr.delta_chunkwise_bwd(*(y[k] for k in KEYS), y["dout"], state_in=y["s0"],
+                                                   d_state_out=y["ds"], cu_seqlens=cu, max_seqlen=bound, check=True)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_the_largest_launch():
+    """8191 sequences of one token, 128 heads of 256: just below 2^32 threads."""
+    b, h, d = 8191, 128, 256
+    assert 8 * b * h * 512 > 2 ** 32 - 2 ** 20
+    free_memory(60 << 30)
+    g = torch.Generator(device=DEV).manual_seed(51)
+    k = torch.randn(b, 1, 1, d, generator=g, device=DEV, dtype=torch.bfloat16) / 16
+    v = torch.randn(b, 1, h, d, generator=g, device=DEV, dtype=torch.bfloat16)
+    ld, beta = -torch.rand(b, 1, h, generator=g, device=DEV), torch.rand(b, 1, h, generator=g, device=DEV)
+    o = rr.delta_chunkwise_fwd(k, k, v, ld, beta)
+    for at in (0, 4000, b - 3):
+        part = [t[at:at + 3].contiguous() for t in (k, k, v, ld, beta)]
+        assert torch.equal(o[at:at + 3], rr.delta_chunkwise_fwd(*part))
+    # one token and no state: o = beta (q . k) v
+    w = (k.double() ** 2).sum(-1, keepdim=True) * beta[..., None].double()
+    err = (o[-64:].double() - w[-64:] * v[-64:].double()).norm() / (w[-64:] * v[-64:].double()).norm()
+    assert err < 2.0 ** -8
+
+
+def test_packed_backward_in_a_graph():
+    """Captured on one stream with a workspace that held NaN, replayed on new inputs
+    between eager calls."""
+    lens = [130, 0, 66]
+    x = make(52, len(lens), 130, 1, 2, 64, "bf16", lens=lens)
+    y = dev(x)
+    more = dict(cu_seqlens=torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV), max_seqlen=130)
+    run = lambda ws=None: rr.delta_chunkwise_bwd(*(y[k] for k in KEYS), y["dout"], state_in=y["s0"],  # noqa: E731
+                                                 d_state_out=y["ds"], workspace=ws, **more)
+    ws = workspace(run, 255)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs = run(ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in range(4):
+        for k in ("v", "dout"):
+            y[k].copy_(torch.randn(y[k].shape, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, run()))
