@@ -417,6 +417,149 @@ ret_status_t retention_residual_norm_bwd(const ret_norm_desc_t *desc, float skip
                                          float *dpost_weight, float *dscale, void *workspace, size_t workspace_bytes,
                                          hipStream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Gated linear recurrence: a state of one value a channel, a factor of its own
+ * for each channel and token. Per channel c of `width`, with s() the sigmoid,
+ *     la_t = decay_t                      (rate NULL: log decays, fp32)
+ *     la_t = -rate_c s(decay_t)           (rate given; decay in the dtype)
+ *     a_t = exp(la_t),   m_t = sqrt(1 - a_t^2) with `normalize`, else 1
+ *     h_t = a_t h_(t-1) + m_t s(gate_t) x_t        (gate NULL: m_t x_t),  o_t = h_t
+ *     x, gate, o        [batch, seqlen, width]     dtype of the descriptor
+ *     decay             [batch, seqlen, width]     fp32, or with rate the dtype
+ *     rate              [width]                    fp32, >= 0
+ *     state             [batch, width]             fp32
+ * It is the recurrence that retention has ("Summary": a linear recurrence with
+ * exponential decay) without keys. Rows of x, decay and gate may stand further
+ * apart than `width` (columns of a wider projection): their strides count elements
+ * from a token to the next, over the whole batch, and they need no more than their
+ * element's alignment; o and all gradients are dense.
+ * Log decays are meant to be <= 0. At -infinity, as for every factor that is 0 in
+ * 32 bits, a token forgets whatever the state holds, NaN and infinity too. Other
+ * values are computed as they stand (normalize gives NaN for those above 0).
+ *
+ * Packed sequences: with cu_seqlens (DEVICE int32 [batch + 1]) the tensors are
+ * [total_tokens, width], sequence b holds rows cu_seqlens[b] .. cu_seqlens[b+1]-1,
+ * empty sequences are allowed (their state passes through), rows outside every
+ * sequence are not written, and bounds that have to be clamped set bit 1 of control
+ * word 1 (retention_chunkwise_error reads it from these workspaces too); seqlen only
+ * has to be >= 1. With cu_seqlens NULL total_tokens is ignored.
+ *
+ * Limits: width <= 65536, fewer than 2^31 - 2^16 tokens, and tokens * width small
+ * enough for a launch (below 2^34).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch;        /* >= 1: sequences                                         */
+  int32_t seqlen;       /* >= 1: tokens of each                                    */
+  int32_t width;        /* channels                                                */
+  int32_t dtype;        /* ret_dtype_t of x, gate, o and (with rate) decay         */
+  int32_t normalize;    /* nonzero: inputs times sqrt(1 - a^2)                     */
+  int32_t reserved;     /* 0                                                       */
+  int64_t x_stride;     /* elements from a token to the next; 0: width             */
+  int64_t decay_stride;
+  int64_t gate_stride;
+} ret_scan_desc_t;
+
+/* Forward. state_in NULL: zeros; state_out NULL: not written; state_out == state_in
+ * is allowed. kept (NULL: none): retention_scan_kept_bytes(...) bytes of states on
+ * the way, which save the backward a forward of its own. */
+size_t retention_scan_workspace_bytes(const ret_scan_desc_t *desc, int32_t packed, int64_t total_tokens);
+size_t retention_scan_kept_bytes(const ret_scan_desc_t *desc, int32_t packed, int64_t total_tokens);
+ret_status_t retention_scan_fwd(const ret_scan_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
+                                const void *x, const void *decay, const float *rate, const void *gate, void *o,
+                                const float *state_in, float *state_out, float *kept, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dout (.) o) + sum(d_state_out (.) state_out) (the second term
+ * only when d_state_out is given) with respect to x, decay, rate, gate and
+ * state_in; drate, dgate, d_state_in are non-NULL exactly when rate, gate, state_in
+ * are. kept: what a forward of the same inputs wrote there, or NULL. Rows before
+ * the first packed sequence and behind the last get gradient 0. Where a log decay is
+ * 0, normalize gives it the gradient of the recurrence alone (sqrt(1 - a^2) has
+ * none there; decay's gradient goes to this as its sigmoid goes to 0). A factor of 0
+ * in 32 bits has gradient 0. */
+size_t retention_scan_bwd_workspace_bytes(const ret_scan_desc_t *desc, int32_t packed, int64_t total_tokens,
+                                          int32_t has_kept);
+ret_status_t retention_scan_bwd(const ret_scan_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
+                                const void *x, const void *decay, const float *rate, const void *gate,
+                                const void *dout, const float *state_in, const float *d_state_out, const float *kept,
+                                void *dx, void *ddecay, float *drate, void *dgate, float *d_state_in, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* One decode step for a batch of single tokens (seqlen 1, batch <= 65535), the
+ * state in place: a pool [num_slots, width] with slots as in retention_delta_step. */
+ret_status_t retention_scan_step(const ret_scan_desc_t *desc, const void *x, const void *decay, const float *rate,
+                                 const void *gate, void *o, float *state, const int32_t *slots, int64_t num_slots,
+                                 hipStream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Short causal convolution before a mixer, a filter of its own for each channel:
+ *     z_t = bias + sum_(j < taps) weight[j] x_(t - taps + 1 + j),
+ *     o_t = z_t, or with `swish` z_t s(z_t).
+ *     x, o              [batch, seqlen, width]     dtype of the descriptor
+ *     weight, bias      [width, taps], [width]     fp32 (bias NULL: none)
+ *     state             [batch, taps - 1, width]   dtype: the last inputs, oldest first
+ * x's rows may stand apart, packed sequences and limits as for the recurrence
+ * above. The state before a sequence stands for its inputs at t < 0 (state_in NULL:
+ * zeros); state_out == state_in is allowed. Without cu_seqlens the forward needs no
+ * workspace (0 bytes). Gradients: as there, with dbias non-NULL exactly when bias
+ * is; the workspace holds partial sums of dweight and dbias.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch;     /* >= 1: sequences                                         */
+  int32_t seqlen;    /* >= 1: tokens of each                                    */
+  int32_t width;     /* channels                                                */
+  int32_t taps;      /* 2, 3 or 4                                               */
+  int32_t dtype;     /* ret_dtype_t                                             */
+  int32_t swish;     /* nonzero: swish of the sum                               */
+  int64_t x_stride;  /* elements from a token to the next; 0: width             */
+} ret_conv_desc_t;
+
+size_t retention_conv_workspace_bytes(const ret_conv_desc_t *desc, int32_t packed, int64_t total_tokens);
+ret_status_t retention_conv_fwd(const ret_conv_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
+                                const void *x, const float *weight, const float *bias, void *o, const void *state_in,
+                                void *state_out, void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t retention_conv_bwd_workspace_bytes(const ret_conv_desc_t *desc, int32_t packed, int64_t total_tokens);
+ret_status_t retention_conv_bwd(const ret_conv_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,
+                                const void *x, const float *weight, const float *bias, const void *dout,
+                                const void *state_in, const void *d_state_out, void *dx, float *dweight, float *dbias,
+                                void *d_state_in, void *workspace, size_t workspace_bytes, hipStream_t stream);
+/* One decode step (seqlen 1, batch <= 65535): the pool [num_slots, taps - 1, width]
+ * in place, slots as in retention_delta_step. */
+ret_status_t retention_conv_step(const ret_conv_desc_t *desc, const void *x, const float *weight, const float *bias,
+                                 void *o, void *state, const int32_t *slots, int64_t num_slots, hipStream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Cache of parked states: the states of sessions that wait (retention's, the delta
+ * rule's or the recurrence's, `values` fp32 each) in 8 bits. Every 64 values of a
+ * state, counted from its first, share a scale:
+ *     scale = max |x| (1 / 127) in fp32,   code = x / scale to the nearest, halves to
+ * even, and code scale is read back. A block that holds NaN or infinity reads back as NaN.
+ *     state    [num_slots, values]                 fp32
+ *     codes    [cache_slots, values]               int8
+ *     scales   [cache_slots, ceil(values / 64)]    fp32
+ * Sequence b of `batch` moves between slot slots[b] of state (slots NULL: b itself,
+ * then num_slots must equal batch) and slot cache_slots_of[b] of the cache (both
+ * DEVICE int32 [batch], 4-byte aligned). Write: a sequence with a slot outside
+ * either pool, or with a cache slot that an earlier one names, writes nothing.
+ * Read: several sequences may read one cache slot (a shared prefix); a cache slot
+ * outside the cache (-1) gives a state of zeros; a slot outside state, or named by an
+ * earlier sequence, is not written.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t batch;       /* 1 .. 65535                                              */
+  int32_t reserved;    /* 0                                                       */
+  int64_t values;      /* of a state, >= 1                                        */
+  int64_t num_slots;   /* of state                                                */
+  int64_t cache_slots; /* of codes and scales                                     */
+} ret_state_cache_desc_t;
+
+ret_status_t retention_state_cache_write(const ret_state_cache_desc_t *desc, const float *state, int8_t *codes,
+                                         float *scales, const int32_t *cache_slots_of, const int32_t *slots,
+                                         hipStream_t stream);
+ret_status_t retention_state_cache_read(const ret_state_cache_desc_t *desc, const int8_t *codes, const float *scales,
+                                        float *state, const int32_t *cache_slots_of, const int32_t *slots,
+                                        hipStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *retention_status_string(ret_status_t status);
 

@@ -14,6 +14,9 @@ gfx950 behind a C ABI (include/retention.h), with a thin ctypes binding.
     delta_recurrent_step  its decode step, state (or a pool of states) in place
     head_norm_fwd, head_norm_bwd          per-head norm with weight and swish gate, gradients
     residual_norm_fwd, residual_norm_bwd  norm after a block, scaled residual, norm before the next
+    gated_scan_fwd, gated_scan_bwd, gated_scan_step   gated linear recurrence, a state a channel
+    short_conv_fwd, short_conv_bwd, short_conv_step   short causal convolution before a mixer
+    state_cache_write, state_cache_read   states of parked sessions in 8 bits
     check_chunkwise  raise if a chunkwise call's control word reports an error
 """
 
@@ -30,6 +33,9 @@ from .binding import (  # noqa: F401
     delta_chunkwise_bwd,
     delta_chunkwise_fwd,
     delta_recurrent_step,
+    gated_scan_bwd,
+    gated_scan_fwd,
+    gated_scan_step,
     head_norm_bwd,
     head_norm_fwd,
     lib,
@@ -39,4 +45,9 @@ from .binding import (  # noqa: F401
     residual_norm_bwd,
     residual_norm_fwd,
     score_map,
+    short_conv_bwd,
+    short_conv_fwd,
+    short_conv_step,
+    state_cache_read,
+    state_cache_write,
 )

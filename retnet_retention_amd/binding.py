@@ -63,6 +63,19 @@ EXPORTS = (
     "retention_residual_norm_fwd",
     "retention_residual_norm_bwd_workspace_bytes",
     "retention_residual_norm_bwd",
+    "retention_scan_workspace_bytes",
+    "retention_scan_kept_bytes",
+    "retention_scan_fwd",
+    "retention_scan_bwd_workspace_bytes",
+    "retention_scan_bwd",
+    "retention_scan_step",
+    "retention_conv_workspace_bytes",
+    "retention_conv_fwd",
+    "retention_conv_bwd_workspace_bytes",
+    "retention_conv_bwd",
+    "retention_conv_step",
+    "retention_state_cache_write",
+    "retention_state_cache_read",
     "retention_status_string",
     "retention_abi_version",
 )
@@ -109,6 +122,48 @@ class NormDesc(ctypes.Structure):
         ("dtype", ctypes.c_int32),
         ("center", ctypes.c_int32),
         ("eps", ctypes.c_float),
+    ]
+
+
+class ScanDesc(ctypes.Structure):
+    """Mirror of ret_scan_desc_t."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("seqlen", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("normalize", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("decay_stride", ctypes.c_int64),
+        ("gate_stride", ctypes.c_int64),
+    ]
+
+
+class ConvDesc(ctypes.Structure):
+    """Mirror of ret_conv_desc_t."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("seqlen", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("taps", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("swish", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
+class StateCacheDesc(ctypes.Structure):
+    """Mirror of ret_state_cache_desc_t."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("values", ctypes.c_int64),
+        ("num_slots", ctypes.c_int64),
+        ("cache_slots", ctypes.c_int64),
     ]
 
 
@@ -199,6 +254,33 @@ def lib():
         h.retention_residual_norm_bwd_workspace_bytes.restype = sz
         h.retention_residual_norm_bwd.argtypes = [pnd, f32] + [vp] * 13 + [sz, vp]
         h.retention_residual_norm_bwd.restype = st
+        psd, pcd, pqd = (ctypes.POINTER(d) for d in (ScanDesc, ConvDesc, StateCacheDesc))
+        h.retention_scan_workspace_bytes.argtypes = [psd, i32, i64]
+        h.retention_scan_workspace_bytes.restype = sz
+        h.retention_scan_kept_bytes.argtypes = [psd, i32, i64]
+        h.retention_scan_kept_bytes.restype = sz
+        h.retention_scan_fwd.argtypes = [psd, vp, i64] + [vp] * 9 + [sz, vp]
+        h.retention_scan_fwd.restype = st
+        h.retention_scan_bwd_workspace_bytes.argtypes = [psd, i32, i64, i32]
+        h.retention_scan_bwd_workspace_bytes.restype = sz
+        h.retention_scan_bwd.argtypes = [psd, vp, i64] + [vp] * 14 + [sz, vp]
+        h.retention_scan_bwd.restype = st
+        h.retention_scan_step.argtypes = [psd] + [vp] * 7 + [i64, vp]
+        h.retention_scan_step.restype = st
+        h.retention_conv_workspace_bytes.argtypes = [pcd, i32, i64]
+        h.retention_conv_workspace_bytes.restype = sz
+        h.retention_conv_fwd.argtypes = [pcd, vp, i64] + [vp] * 7 + [sz, vp]
+        h.retention_conv_fwd.restype = st
+        h.retention_conv_bwd_workspace_bytes.argtypes = [pcd, i32, i64]
+        h.retention_conv_bwd_workspace_bytes.restype = sz
+        h.retention_conv_bwd.argtypes = [pcd, vp, i64] + [vp] * 11 + [sz, vp]
+        h.retention_conv_bwd.restype = st
+        h.retention_conv_step.argtypes = [pcd] + [vp] * 6 + [i64, vp]
+        h.retention_conv_step.restype = st
+        h.retention_state_cache_write.argtypes = [pqd] + [vp] * 6
+        h.retention_state_cache_write.restype = st
+        h.retention_state_cache_read.argtypes = [pqd] + [vp] * 6
+        h.retention_state_cache_read.restype = st
         h.retention_status_string.argtypes = [st]
         h.retention_status_string.restype = ctypes.c_char_p
         h.retention_abi_version.argtypes = []
@@ -821,3 +903,312 @@ def residual_norm_bwd(x, y, weight, dout, dresidual=None, *, post_weight=None, s
                                              _ptr(dy), _ptr(dweight), _ptr(dpost), _ptr(dscale), _ptr(workspace),
                                              ws_bytes, _stream(x)))
     return dx, dy, dweight, dpost, dscale
+
+
+# ---------------------------------------------------------------------------
+# Gated linear recurrence and the short convolution before it
+# ---------------------------------------------------------------------------
+def _token_stride(name, t):
+    """Elements from a token of [..., width] to the next, over all leading
+    dimensions alike (columns of a wider tensor are)."""
+    if t.is_contiguous():
+        return t.shape[-1]
+    sizes, strides = t.shape, t.stride()
+    if sizes[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    stride, tokens = None, 1
+    for n, s in zip(reversed(sizes[:-1]), reversed(strides[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif s != stride * tokens:
+            raise ValueError(f"{name}'s tokens must stand at one distance from each other")
+        tokens *= n
+    if stride is None:
+        return sizes[-1]
+    if stride < sizes[-1]:
+        raise ValueError(f"{name}'s tokens must not overlap")
+    return stride
+
+
+def _token_rows(rows, dense, cu_seqlens):
+    """Checks of tensors [batch, seqlen, width], or packed [total_tokens,
+    width]: `rows` may have a token stride, `dense` may not. Returns (batch,
+    seqlen, total_tokens, width, strides of `rows` (0 for None))."""
+    name, x = rows[0][:2]
+    dev, shape = x.get_device(), x.shape
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    packed = cu_seqlens is not None
+    if len(shape) != (2 if packed else 3):
+        raise ValueError(f"{name} must be " + ("[total_tokens, width]" if packed else "[batch, seqlen, width]"))
+    for n, t, dtype in rows + dense:
+        if t is not None and (t.get_device() != dev or t.dtype != dtype or t.shape != shape):
+            raise ValueError(f"{n} must be a {dtype} tensor {list(shape)} on {x.device}")
+    for n, t, _ in dense:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    strides = [0 if t is None else _token_stride(n, t) for n, t, _ in rows]
+    if not packed:
+        return shape[0], shape[1], 0, shape[2], strides
+    if (cu_seqlens.get_device() != dev or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1
+            or not cu_seqlens.is_contiguous()):
+        raise ValueError("cu_seqlens must be a contiguous GPU int32 tensor [batch + 1]")
+    return cu_seqlens.numel() - 1, 1, shape[0], shape[1], strides
+
+
+def _held(like, *tensors):
+    """Checks of (name, tensor or None, shape, dtype), contiguous on `like`'s device."""
+    for name, t, shape, dtype in tensors:
+        if t is not None and (t.get_device() != like.get_device() or t.dtype != dtype or not t.is_contiguous()
+                              or t.shape != shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {like.device}")
+
+
+def _slots(name, slots, batch, like):
+    if (slots.get_device() != like.get_device() or slots.dtype != torch.int32 or not slots.is_contiguous()
+            or slots.shape != (batch,)):
+        raise ValueError(f"{name} must be a contiguous GPU int32 tensor [batch]")
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_desc_of(*fields):
+    """(descriptor, reference to it): calls only read it."""
+    d = ScanDesc(*fields)
+    return d, ctypes.byref(d)
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_desc_of(*fields):
+    """(descriptor, reference to it): calls only read it."""
+    d = ConvDesc(*fields)
+    return d, ctypes.byref(d)
+
+
+def _scan_call(x, decay, gate, rate, normalize, cu_seqlens, *dense):
+    """Checks of a recurrence call; returns (descriptor, batch, total_tokens, width)."""
+    code = _dtype_code(x)
+    rows = (("x", x, x.dtype), ("decay", decay, torch.float32 if rate is None else x.dtype), ("gate", gate, x.dtype))
+    batch, seqlen, total, width, strides = _token_rows(rows, dense, cu_seqlens)
+    if rate is not None:
+        _held(x, ("rate", rate, (width,), torch.float32))
+    desc = _scan_desc_of(batch, seqlen, width, code, int(bool(normalize)), 0, *strides)[1]
+    return desc, batch, total, width
+
+
+def gated_scan_fwd(x, decay, gate=None, *, rate=None, normalize=False, state_in=None, state_out=None, cu_seqlens=None,
+                   out=None, keep=False, workspace=None, check=False):
+    """Gated linear recurrence h_t = a_t h_(t-1) + m_t sigmoid(gate_t) x_t over
+    whole sequences, a state a channel: x [batch, seqlen, width]; a_t =
+    exp(decay_t) (fp32 log decays), or with rate (fp32 [width], >= 0)
+    exp(-rate sigmoid(decay_t)) (decay in x's dtype); m_t = sqrt(1 - a_t^2)
+    with normalize, else 1; without gate its factor is 1. Returns the output
+    (every h_t) and fills state_out (fp32 [batch, width], may be state_in
+    itself) if it is given; with keep=True returns (output, kept): states on the
+    way for gated_scan_bwd. x, decay and gate may be columns of a wider
+    projection. Packed sequences: [total_tokens, width] tensors with cu_seqlens
+    (GPU int32 [batch + 1]); rows outside every sequence are left as they were.
+    A factor of 0 (log decay -infinity) forgets whatever the state holds. check:
+    as delta_chunkwise_fwd."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    desc, batch, total, width = _scan_call(x, decay, gate, rate, normalize, cu_seqlens, ("out", out, x.dtype))
+    state = (batch, width)
+    _held(x, ("state_in", state_in, state, torch.float32), ("state_out", state_out, state, torch.float32))
+    L = lib()
+    packed = int(cu_seqlens is not None)
+    kept = None
+    if keep:
+        kept = torch.empty(L.retention_scan_kept_bytes(desc, packed, total) // 4, device=x.device)
+    workspace, ws_bytes, _ = _workspace(workspace, L.retention_scan_workspace_bytes(desc, packed, total), x)
+    with _current(x):
+        _check(L.retention_scan_fwd(desc, _ptr(cu_seqlens), total, _ptr(x), _ptr(decay), _ptr(rate), _ptr(gate),
+                                    _ptr(out), _ptr(state_in), _ptr(state_out), _ptr(kept), _ptr(workspace), ws_bytes,
+                                    _stream(x)))
+    if check:
+        check_chunkwise(workspace)
+    return (out, kept) if keep else out
+
+
+def gated_scan_bwd(x, decay, dout, gate=None, *, rate=None, normalize=False, state_in=None, d_state_out=None,
+                   cu_seqlens=None, kept=None, workspace=None, check=False):
+    """Gradients of sum(dout * out) (+ sum(d_state_out * state_out)) with out,
+    state_out = gated_scan_fwd(x, decay, gate, ...). Returns (dx, ddecay, dgate,
+    drate), None where there is no such input, and d_state_in after them when
+    state_in is given. kept: what the forward of the same inputs returned with
+    keep=True (without it that forward is run again for its states). Packed
+    sequences and check as in the forward; gradient rows before the first
+    sequence and behind the last are zero."""
+    desc, batch, total, width = _scan_call(x, decay, gate, rate, normalize, cu_seqlens, ("dout", dout, x.dtype))
+    state = (batch, width)
+    _held(x, ("state_in", state_in, state, torch.float32), ("d_state_out", d_state_out, state, torch.float32))
+    L = lib()
+    packed = int(cu_seqlens is not None)
+    if kept is not None:
+        _held(x, ("kept", kept, (L.retention_scan_kept_bytes(desc, packed, total) // 4,), torch.float32))
+    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    dx, ddecay, dgate, drate, dstate = new(x), new(decay), new(gate), new(rate), new(state_in)
+    need = L.retention_scan_bwd_workspace_bytes(desc, packed, total, int(kept is not None))
+    workspace, ws_bytes, _ = _workspace(workspace, need, x)
+    with _current(x):
+        _check(L.retention_scan_bwd(desc, _ptr(cu_seqlens), total, _ptr(x), _ptr(decay), _ptr(rate), _ptr(gate),
+                                    _ptr(dout), _ptr(state_in), _ptr(d_state_out), _ptr(kept), _ptr(dx),
+                                    _ptr(ddecay), _ptr(drate), _ptr(dgate), _ptr(dstate), _ptr(workspace), ws_bytes,
+                                    _stream(x)))
+    if check:
+        check_chunkwise(workspace)
+    grads = (dx, ddecay, dgate, drate)
+    return grads if state_in is None else grads + (dstate,)
+
+
+def gated_scan_step(x, decay, state, gate=None, *, rate=None, normalize=False, slots=None, out=None):
+    """One decode step of the gated linear recurrence (x: [batch, 1, width]);
+    updates `state` in place and returns the output. state: fp32 [batch,
+    width], or with `slots` (GPU int32 [batch]) a pool [num_slots, width], as in
+    delta_recurrent_step."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    desc, batch, _, width = _scan_call(x, decay, gate, rate, normalize, None, ("out", out, x.dtype))
+    if x.shape[1] != 1:
+        raise ValueError("gated_scan_step takes one token per sequence (seqlen 1)")
+    _held(x, ("state", state, (batch if slots is None else state.shape[0], width), torch.float32))
+    if slots is not None:
+        _slots("slots", slots, batch, x)
+    with _current(x):
+        _check(lib().retention_scan_step(desc, _ptr(x), _ptr(decay), _ptr(rate), _ptr(gate), _ptr(out), _ptr(state),
+                                         _ptr(slots), state.shape[0], _stream(x)))
+    return out
+
+
+def _conv_call(x, weight, bias, swish, cu_seqlens, *dense):
+    """Checks of a convolution call; returns (descriptor, batch, total_tokens, shape of a state)."""
+    code = _dtype_code(x)
+    batch, seqlen, total, width, strides = _token_rows((("x", x, x.dtype),), dense, cu_seqlens)
+    if weight.dim() != 2:
+        raise ValueError("weight must be [width, taps]")
+    taps = weight.shape[1]
+    _held(x, ("weight", weight, (width, taps), torch.float32), ("bias", bias, (width,), torch.float32))
+    desc = _conv_desc_of(batch, seqlen, width, taps, code, int(bool(swish)), *strides)[1]
+    return desc, batch, total, (taps - 1, width)
+
+
+def short_conv_fwd(x, weight, bias=None, *, swish=False, state_in=None, state_out=None, cu_seqlens=None, out=None,
+                   workspace=None, check=False):
+    """Short causal convolution of each channel along a sequence: x [batch,
+    seqlen, width], weight fp32 [width, taps] (2 to 4 taps, the last one at the
+    token itself), bias fp32 [width], then swish where asked. Returns the output;
+    state_in / state_out: the taps - 1 inputs before the first and up to the last
+    token, [batch, taps - 1, width] in x's dtype, oldest first (state_out may be
+    state_in itself). x may be columns of a wider projection. Packed sequences
+    and check as in gated_scan_fwd."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    desc, batch, total, held = _conv_call(x, weight, bias, swish, cu_seqlens, ("out", out, x.dtype))
+    state = (batch,) + held
+    _held(x, ("state_in", state_in, state, x.dtype), ("state_out", state_out, state, x.dtype))
+    L = lib()
+    ws_bytes = 0
+    if cu_seqlens is not None or workspace is not None:
+        need = L.retention_conv_workspace_bytes(desc, int(cu_seqlens is not None), total)
+        workspace, ws_bytes, _ = _workspace(workspace, need, x)
+    with _current(x):
+        _check(L.retention_conv_fwd(desc, _ptr(cu_seqlens), total, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
+                                    _ptr(state_in), _ptr(state_out), _ptr(workspace), ws_bytes, _stream(x)))
+    if check and cu_seqlens is not None:
+        check_chunkwise(workspace)
+    return out
+
+
+def short_conv_bwd(x, weight, dout, bias=None, *, swish=False, state_in=None, d_state_out=None, cu_seqlens=None,
+                   workspace=None, check=False):
+    """Gradients of sum(dout * out) (+ sum(d_state_out * state_out)) with out,
+    state_out = short_conv_fwd(x, weight, bias, ...): (dx, dweight, dbias), None
+    without a bias, and d_state_in after them when state_in is given. Packed
+    sequences, check and rows outside them as in gated_scan_bwd."""
+    desc, batch, total, held = _conv_call(x, weight, bias, swish, cu_seqlens, ("dout", dout, x.dtype))
+    state = (batch,) + held
+    _held(x, ("state_in", state_in, state, x.dtype), ("d_state_out", d_state_out, state, x.dtype))
+    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    dx, dweight, dbias, dstate = new(x), new(weight), new(bias), new(state_in)
+    L = lib()
+    need = L.retention_conv_bwd_workspace_bytes(desc, int(cu_seqlens is not None), total)
+    workspace, ws_bytes, _ = _workspace(workspace, need, x)
+    with _current(x):
+        _check(L.retention_conv_bwd(desc, _ptr(cu_seqlens), total, _ptr(x), _ptr(weight), _ptr(bias), _ptr(dout),
+                                    _ptr(state_in), _ptr(d_state_out), _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                    _ptr(dstate), _ptr(workspace), ws_bytes, _stream(x)))
+    if check and cu_seqlens is not None:
+        check_chunkwise(workspace)
+    return (dx, dweight, dbias) if state_in is None else (dx, dweight, dbias, dstate)
+
+
+def short_conv_step(x, weight, state, bias=None, *, swish=False, slots=None, out=None):
+    """One decode step of the short convolution (x: [batch, 1, width]); moves
+    the inputs in `state` on by one and returns the output. state: [batch,
+    taps - 1, width] in x's dtype, or with `slots` (GPU int32 [batch]) a pool of
+    such, as in delta_recurrent_step."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    desc, batch, _, held = _conv_call(x, weight, bias, swish, None, ("out", out, x.dtype))
+    if x.shape[1] != 1:
+        raise ValueError("short_conv_step takes one token per sequence (seqlen 1)")
+    _held(x, ("state", state, (batch if slots is None else state.shape[0],) + held, x.dtype))
+    if slots is not None:
+        _slots("slots", slots, batch, x)
+    with _current(x):
+        _check(lib().retention_conv_step(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(state), _ptr(slots),
+                                         state.shape[0], _stream(x)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Cache of parked states
+# ---------------------------------------------------------------------------
+CACHE_BLOCK = 64  # values of a cached state that share a scale
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_desc_of(*fields):
+    """(descriptor, reference to it): calls only read it."""
+    d = StateCacheDesc(*fields)
+    return d, ctypes.byref(d)
+
+
+def _cache_call(state, codes, scales, cache_slots, slots):
+    if state.get_device() < 0 or state.dtype != torch.float32 or not state.is_contiguous() or state.dim() < 2:
+        raise ValueError("state must be a contiguous fp32 GPU tensor [num_slots, ...]")
+    per = state.shape[1:]
+    values, n = per.numel(), codes.shape[0]
+    _held(state, ("codes", codes, (n,) + tuple(per), torch.int8),
+          ("scales", scales, (n, -(-values // CACHE_BLOCK)), torch.float32))
+    if cache_slots.dim() != 1:
+        raise ValueError("cache_slots must be a contiguous GPU int32 tensor [batch]")
+    batch = cache_slots.shape[0]
+    _slots("cache_slots", cache_slots, batch, state)
+    if slots is not None:
+        _slots("slots", slots, batch, state)
+    return _cache_desc_of(batch, 0, values, state.shape[0], n)[1]
+
+
+def state_cache_write(state, codes, scales, cache_slots, *, slots=None):
+    """Parks states in 8 bits: state [num_slots, ...] (fp32; the states of any
+    of the recurrent calls) goes to slots of a cache, codes int8 [cache_size,
+    ...] and scales fp32 [cache_size, ceil(values / 64)]: every 64 values share a
+    scale, a 127th of the largest magnitude. Sequence b (of cache_slots, GPU int32
+    [batch]) goes from state slots[b] (GPU int32 [batch]; None: b) to cache slot
+    cache_slots[b]; one with a slot outside either pool, or a cache slot that an
+    earlier one names, is left out. A block that holds NaN or infinity reads
+    back as NaN."""
+    desc = _cache_call(state, codes, scales, cache_slots, slots)
+    with _current(state):
+        _check(lib().retention_state_cache_write(desc, _ptr(state), _ptr(codes), _ptr(scales), _ptr(cache_slots),
+                                                 _ptr(slots), _stream(state)))
+
+
+def state_cache_read(codes, scales, state, cache_slots, *, slots=None):
+    """Resumes parked states: fills state slots[b] (None: b) from cache slot
+    cache_slots[b], for the tensors of state_cache_write. Several sequences may
+    read one cache slot; a cache slot outside the cache (-1) gives a state of
+    zeros. Returns state."""
+    desc = _cache_call(state, codes, scales, cache_slots, slots)
+    with _current(state):
+        _check(lib().retention_state_cache_read(desc, _ptr(codes), _ptr(scales), _ptr(state), _ptr(cache_slots),
+                                                _ptr(slots), _stream(state)))
+    return state

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libretention.so")
 
 SOURCES = ["api.hip", "rotary_table.hip", "recurrent_step.hip", "retention_fwd.hip", "backward.hip", "score_map.hip",
            "delta_api.hip", "delta_fwd.hip", "delta_bwd.hip", "delta_step.hip", "norm_api.hip",
-           "norm_fwd.hip", "norm_bwd.hip"]
+           "norm_fwd.hip", "norm_bwd.hip", "scan_api.hip", "scan_fwd.hip", "scan_bwd.hip", "scan_step.hip", "conv.hip",
+           "state_cache.hip"]
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}",

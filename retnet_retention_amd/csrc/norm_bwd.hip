@@ -186,6 +186,12 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* partial, 
   }
 }
 
+hipError_t launch_column_sum(const float* partial, int rows, int width, float* out, hipStream_t stream) {
+  hipLaunchKernelGGL(column_sum_kernel, dim3((width + 63) / 64), dim3(1024), 0, stream, partial, rows, width, out,
+                     static_cast<float*>(nullptr), static_cast<float*>(nullptr));
+  return hipGetLastError();
+}
+
 // Enough workgroups to fill the chip (2048 lanes a CU), and rows enough for
 // each that their sums' traffic stays small beside the rows'.
 int norm_bwd_blocks(int64_t rows, int width) {

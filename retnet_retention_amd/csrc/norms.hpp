@@ -30,4 +30,7 @@ hipError_t launch_head_norm_bwd(const NormParams& p, int dtype, hipStream_t stre
 hipError_t launch_residual_norm_fwd(const NormParams& p, int dtype, hipStream_t stream);
 hipError_t launch_residual_norm_bwd(const NormParams& p, int dtype, hipStream_t stream);
 
+// out[c] = sum over rows of partial[row][c], in a fixed order
+hipError_t launch_column_sum(const float* partial, int rows, int width, float* out, hipStream_t stream);
+
 }  // namespace ret

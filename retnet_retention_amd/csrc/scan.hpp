@@ -1,0 +1,94 @@
+// Internal interface between the C-ABI layers of the gated recurrence and the
+// short convolution and their kernels: parameters, workspaces, launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ret {
+
+// Tokens of a tile of the recurrence; the states that the forward keeps for the
+// backward stand before each tile. Tiles are numbered over the whole batch: tile i
+// of sequence b is b * tiles_max + i, for packed sequences (row cu[b]) / tile + b +
+// i, which no two sequences share.
+constexpr int kScanTile = 128;
+inline int64_t tile_count(int batch, int seqlen, bool packed, int64_t total, int tile) {
+  return packed ? total / tile + batch : (int64_t)batch * ((seqlen + (int64_t)tile - 1) / tile);
+}
+
+// Whether pairs of neighbouring elements of `size` bytes are aligned in every row.
+inline bool pairs_aligned(const void* p, int64_t stride, int size) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (2 * size) == 0 && stride % 2 == 0);
+}
+
+struct ScanParams {
+  const void *x, *decay, *gate;  // decay: log decays (fp32), or with `rate` what its sigmoid is taken of
+  const float* rate;             // [width] or null
+  const int* cu;                 // packed bounds or null
+  int batch, seqlen, width, total, normalize;
+  int64_t x_stride, decay_stride, gate_stride;  // elements from a token to the next
+  void* o;
+  const float* state_in;
+  float* state_out;
+  float* kept;  // [tiles][width], or null
+  int* ctrl;    // packed sequences: word 1 tells of bounds that had to be clamped
+  // backward
+  const void* dout;
+  const float* d_state_out;
+  float* d_state_in;
+  void *dx, *ddecay, *dgate;
+  float *drate, *partial;  // partial: [batch][width] sums of drate
+};
+hipError_t launch_scan_fwd(const ScanParams& p, int dtype, hipStream_t stream);
+hipError_t launch_scan_bwd(const ScanParams& p, int dtype, hipStream_t stream);
+
+struct ScanStepParams {
+  const void *x, *decay, *gate;
+  const float* rate;
+  void* o;
+  float* state;
+  const int* slots;  // state slot of each sequence, or null: its own index
+  int batch, width, num_slots, normalize;
+  int64_t x_stride, decay_stride, gate_stride;
+};
+hipError_t launch_scan_step(const ScanStepParams& p, int dtype, hipStream_t stream);
+
+constexpr int kMinTaps = 2, kMaxTaps = 4;
+struct ConvParams {
+  const void* x;
+  const float *weight, *bias;  // [width][taps], [width] or null
+  const int* cu;
+  int batch, seqlen, width, total, swish;
+  int64_t x_stride;
+  void* o;
+  const void* state_in;  // [batch][taps - 1][width], oldest first
+  void* state_out;
+  int* ctrl;
+  // backward
+  const void *dout, *d_state_out;
+  void *dx, *d_state_in;
+  float *dweight, *dbias;
+  float* partial;  // [blocks][taps + 1][width] sums of dweight and dbias
+};
+int64_t conv_bwd_blocks(int batch, int seqlen, bool packed, int64_t total);
+hipError_t launch_conv_fwd(const ConvParams& p, int taps, int dtype, hipStream_t stream);
+hipError_t launch_conv_bwd(const ConvParams& p, int taps, int dtype, hipStream_t stream);
+
+struct ConvStepParams {
+  const void* x;
+  const float *weight, *bias;
+  void *o, *state;
+  const int* slots;
+  int batch, width, num_slots, swish;
+  int64_t x_stride;
+};
+hipError_t launch_conv_step(const ConvStepParams& p, int taps, int dtype, hipStream_t stream);
+
+// ctrl[0] = 0, ctrl[1] = 2 if packed bounds leave the tensor or decrease, else 0
+hipError_t launch_check_bounds(const int* cu, int batch, int total, int* ctrl, hipStream_t stream);
+
+// Width limit of both: their launches count channels in groups of 64 or 128.
+constexpr int kMaxScanWidth = 65536;
+
+}  // namespace ret

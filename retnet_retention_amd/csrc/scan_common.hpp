@@ -1,0 +1,133 @@
+// What the kernels of the gated recurrence and the short convolution share: the
+// channels of a lane, packed sequences, and the recurrence's gates.
+#pragma once
+
+#include <type_traits>
+
+#include "common.hpp"
+#include "scan.hpp"
+
+namespace ret {
+
+// V neighbouring channels of a token, as they lie in memory and as floats.
+template <typename T, int V> struct Lane;
+template <> struct Lane<bf16, 1> {
+  using Raw = bf16;
+  __device__ static __forceinline__ void get(Raw r, float* x) { x[0] = (float)r; }
+  __device__ static __forceinline__ Raw put(const float* x) { return (bf16)x[0]; }
+};
+template <> struct Lane<bf16, 2> {
+  using Raw = uint32_t;
+  __device__ static __forceinline__ void get(Raw r, float* x) {
+    x[0] = __uint_as_float(r << 16);
+    x[1] = __uint_as_float(r & 0xffff0000u);
+  }
+  __device__ static __forceinline__ Raw put(const float* x) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, bf16x2{(bf16)x[0], (bf16)x[1]});
+  }
+};
+template <> struct Lane<float, 1> {
+  using Raw = float;
+  __device__ static __forceinline__ void get(Raw r, float* x) { x[0] = r; }
+  __device__ static __forceinline__ Raw put(const float* x) { return x[0]; }
+};
+template <> struct Lane<float, 2> {
+  typedef float Raw __attribute__((ext_vector_type(2)));
+  __device__ static __forceinline__ void get(Raw r, float* x) {
+    x[0] = r[0];
+    x[1] = r[1];
+  }
+  __device__ static __forceinline__ Raw put(const float* x) { return Raw{x[0], x[1]}; }
+};
+template <typename T, int V>
+using lane_raw = typename Lane<T, V>::Raw;
+
+// `row`: a wave-uniform pointer to a token's first channel
+template <typename T, int V>
+__device__ __forceinline__ lane_raw<T, V> lane_load(const T* row, int c) {
+  return *reinterpret_cast<const lane_raw<T, V>*>(row + c);
+}
+template <typename T, int V>
+__device__ __forceinline__ void lane_store(T* row, int c, const float* x) {
+  *reinterpret_cast<lane_raw<T, V>*>(row + c) = Lane<T, V>::put(x);
+}
+
+// Whether a lane may take two bf16 channels of every tensor at once.
+template <typename P>
+inline bool in_pairs(const P& p) {
+  return p.width % 2 == 0 && pairs_aligned(p.x, p.x_stride, 2) &&
+         pairs_aligned(p.decay, p.decay_stride, p.rate ? 2 : 4) && pairs_aligned(p.gate, p.gate_stride, 2);
+}
+
+// First row and length of sequence b, inside the tensor for any bounds.
+template <typename P>
+__device__ __forceinline__ void span_of(const P& p, int b, int& tok0, int& len) {
+  if (p.cu) {
+    packed_span(p.cu, b, p.total, p.total, tok0, len);
+  } else {
+    tok0 = b * p.seqlen;
+    len = p.seqlen;
+  }
+}
+
+// Tile `j` as sequence b and its tile i, for tiles numbered as scan.hpp tells.
+// Packed: b is the last sequence whose first tile is j or before it; every lane of
+// a wave looks at one sequence. A tile of no sequence gets an i behind every end.
+template <typename P>
+__device__ __forceinline__ void tile_of(const P& p, int64_t j, int tile, int& b, int& i) {
+  if (!p.cu) {
+    const int per = (p.seqlen + tile - 1) / tile;
+    b = (int)(j / per);
+    i = (int)(j - (int64_t)b * per);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 64) {
+    const int s = b0 + lane;
+    const bool hit = s < p.batch && min(max(p.cu[s], 0), p.total) / tile + (int64_t)s <= j;
+    before += __popcll(__ballot(hit));
+  }
+  b = max(before, 1) - 1;
+  i = (int)j - (min(max(uniform_i(p.cu[b]), 0), p.total) / tile + b);
+  if (i < 0 || i > p.total / tile) i = p.total / tile + 1;
+}
+
+__device__ __forceinline__ float sigmoid_of(float x, float) { return 1.f / (1.f + expf(-x)); }
+// bf16 tensors: the hardware's exp2 and reciprocal, about 1 ulp each
+__device__ __forceinline__ float sigmoid_of(float x, bf16) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+}
+
+// Factor a = exp(la) of a token and 1 - a^2. Near 1 the sum 1 + (a - 1) with a - 1
+// from its series: the factor is then off by half a step and not biased, so a
+// thousand tokens' product stays good, and 1 - a^2 = (1 - a)(1 + a) has no
+// cancellation. bf16 tensors take the series to |la| = 1/32, four terms (1e-8 of a
+// - 1), fp32 ones to 1/4, seven (2e-9); beyond it a - 1 is large enough for what a's
+// own rounding leaves of it.
+template <typename T>
+__device__ __forceinline__ void factor(float la, float& a, float& left) {
+  constexpr bool wide = sizeof(T) == 4;
+  float p;
+  if constexpr (wide) {
+    p = 1.f / 5040;
+    p = fmaf(p, la, 1.f / 720);
+    p = fmaf(p, la, 1.f / 120);
+    p = fmaf(p, la, 1.f / 24);
+  } else {
+    p = 1.f / 24;
+  }
+  p = fmaf(p, la, 1.f / 6);
+  p = fmaf(p, la, 0.5f);
+  p = fmaf(p, la, 1.f) * la;
+  const float e = wide ? expf(la) : __builtin_amdgcn_exp2f(1.4426950408889634f * la);
+  const bool near = fabsf(la) < (wide ? 0.25f : 0.03125f);
+  a = near ? 1.f + p : e;
+  left = near ? -p * (2.f + p) : fmaf(-e, e, 1.f);
+}
+
+// A factor of 0 forgets what was there, NaN and infinity too.
+__device__ __forceinline__ float step_or_forget(float a, float h, float u) { return a == 0.f ? u : fmaf(a, h, u); }
+
+}  // namespace ret

@@ -1,0 +1,127 @@
+// States of parked sessions in 8 bits. Blocks of 64 values of a state share a scale
+//     scale = max |x| (1 / 127),   code = x / scale rounded to the nearest, halves to even,
+// and are read back as code scale. Integers with a scale of their own every 64 values
+// keep a state to half a 127th of its block's largest value; e4m3 of the same size
+// keeps each value to a 16th of itself, five times worse over values of one
+// size. Bound by memory: 4 bytes a value on one side, 1.06 on the other.
+#include "common.hpp"
+#include "state_cache.hpp"
+
+namespace ret {
+
+// Slot `i` of a list, or -1 where it lies outside `n`.
+__device__ __forceinline__ int64_t listed(const int* list, int i, int64_t n) {
+  const int64_t s = list ? list[i] : i;
+  return s < 0 || s >= n ? -1 : s;
+}
+
+// Whether an earlier sequence of the batch names the same slot of `list`.
+__device__ __forceinline__ bool named_before(const int* list, int b) {
+  bool hit = false;
+  if (list)
+    for (int i = threadIdx.x; i < b; i += blockDim.x) hit |= list[i] == list[b];
+  return __syncthreads_or(hit);
+}
+
+// x / scale to the nearest integer, halves to even: the product with the reciprocal
+// can round to the wrong side of a half, which the remainder (exact) tells.
+__device__ __forceinline__ int code_of(float x, float scale, float inv) {
+  float q = rintf(x * inv);
+  const float r = fmaf(-q, scale, x), half = 0.5f * scale;
+  const bool odd = ((int)q & 1) != 0;
+  if (r > half || (r == half && odd)) q += 1.f;
+  if (r < -half || (r == -half && odd)) q -= 1.f;
+  return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// 16 lanes a block of 64 values, 4 values each
+__global__ __launch_bounds__(256) void state_cache_write_kernel(StateCacheParams p) {
+  const int b = blockIdx.y;
+  const int64_t to = listed(p.at, b, p.cache_slots), from = listed(p.slots, b, p.num_slots);
+  if (to < 0 || from < 0) return;
+  if (named_before(p.at, b)) return;
+  const int64_t block = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (block >= p.blocks) return;
+  const int64_t v = block * kCacheBlock + 4 * (threadIdx.x & 15);
+  const float* x = p.state + from * p.values;
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  const bool whole = v + 4 <= p.values && p.values % 4 == 0;
+  if (whole) {
+    y = *reinterpret_cast<const f32x4*>(x + v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v + e < p.values) y[e] = x[v + e];
+  }
+  // the largest magnitude by its bits: a NaN is above infinity
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, s, 64));
+  // NaN or infinity: the block reads back as NaN
+  const float scale = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) * (1.f / 127.f);
+  // a quotient's reciprocal stays finite if both sides of a tiny one are brought up (exact)
+  const float up = scale < 0x1p-64f ? 0x1p+64f : 1.f, s = scale * up, inv = 1.f / s;
+  uint32_t word = 0;
+  if (scale > 0.f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) word |= (uint32_t)(code_of(y[e] * up, s, inv) & 0xff) << (8 * e);
+  }
+  int8_t* codes = p.codes + to * p.values;
+  if (whole) {
+    *reinterpret_cast<uint32_t*>(codes + v) = word;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v + e < p.values) codes[v + e] = (int8_t)(word >> (8 * e));
+  }
+  if ((threadIdx.x & 15) == 0) p.scales[to * p.blocks + block] = scale;
+}
+
+__global__ __launch_bounds__(256) void state_cache_read_kernel(StateCacheParams p) {
+  const int b = blockIdx.y;
+  const int64_t from = listed(p.at, b, p.cache_slots), to = listed(p.slots, b, p.num_slots);
+  if (to < 0) return;
+  if (named_before(p.slots, b)) return;
+  const int64_t block = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (block >= p.blocks) return;
+  const int64_t v = block * kCacheBlock + 4 * (threadIdx.x & 15);
+  float* x = p.state + to * p.values;
+  const bool whole = v + 4 <= p.values && p.values % 4 == 0;
+  float scale = 0.f;
+  uint32_t word = 0;
+  if (from >= 0) {
+    scale = p.scales[from * p.blocks + block];
+    const int8_t* codes = p.codes + from * p.values;
+    if (whole) {
+      word = *reinterpret_cast<const uint32_t*>(codes + v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (v + e < p.values) word |= (uint32_t)(uint8_t)codes[v + e] << (8 * e);
+    }
+  }
+  f32x4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (float)(int8_t)(word >> (8 * e)) * scale;
+  if (whole) {
+    *reinterpret_cast<f32x4*>(x + v) = y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v + e < p.values) x[v + e] = y[e];
+  }
+}
+
+static dim3 grid_of(const StateCacheParams& p) { return dim3((unsigned)((p.blocks + 15) / 16), (unsigned)p.batch); }
+hipError_t launch_state_cache_write(const StateCacheParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL(state_cache_write_kernel, grid_of(p), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+hipError_t launch_state_cache_read(const StateCacheParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL(state_cache_read_kernel, grid_of(p), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace ret
