@@ -444,8 +444,9 @@ ret_status_t retention_residual_norm_bwd(const ret_norm_desc_t *desc, float skip
  * word 1 (retention_chunkwise_error reads it from these workspaces too); seqlen only
  * has to be >= 1. With cu_seqlens NULL total_tokens is ignored.
  *
- * Limits: width <= 65536, fewer than 2^31 - 2^16 tokens, and tokens * width small
- * enough for a launch (below 2^34).
+ * Limits: width <= 65536, at most 2^31 - 2^16 tokens, tokens * width small enough for
+ * a launch (2^34 always is); strides below 2^31, of packed sequences and of those of
+ * 128 tokens or more below 2^22.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t batch;        /* >= 1: sequences                                         */

@@ -8,14 +8,25 @@
 
 namespace ret {
 
-// Tokens of a tile of the recurrence; the states that the forward keeps for the
-// backward stand before each tile. Tiles are numbered over the whole batch: tile i
-// of sequence b is b * tiles_max + i, for packed sequences (row cu[b]) / tile + b +
-// i, which no two sequences share.
-constexpr int kScanTile = 128;
+// Tiles of a batch's tokens are numbered over all of it: tile i of sequence b is b *
+// (tiles of a sequence) + i, for packed sequences (row cu[b]) / tile + b + i, which no
+// two sequences share.
 inline int64_t tile_count(int batch, int seqlen, bool packed, int64_t total, int tile) {
   return packed ? total / tile + batch : (int64_t)batch * ((seqlen + (int64_t)tile - 1) / tile);
 }
+
+// The recurrence: tokens of a tile of the forward and of the backward. The states
+// that the forward keeps stand before each of the backward's tiles.
+constexpr int kScanTile = 256, kScanBwdTile = 128;
+// Channels of a workgroup.
+constexpr int kScanChannels = 64;
+
+// What the workgroups of a call hand each other: a control block (word 1: errors),
+// ticket counters 64 bytes apart, and a word for each tile and channel.
+constexpr int kScanQueues = 32;
+constexpr size_t kScanCtrlBytes = 64 * (1 + kScanQueues);
+// whether any sequence has more than one tile of `tile` tokens
+inline bool has_chain(int seqlen, bool packed, int64_t total, int tile) { return (packed ? total : seqlen) > tile; }
 
 // Whether pairs of neighbouring elements of `size` bytes are aligned in every row.
 inline bool pairs_aligned(const void* p, int64_t stride, int size) {
@@ -31,16 +42,20 @@ struct ScanParams {
   void* o;
   const float* state_in;
   float* state_out;
-  float* kept;  // [tiles][width], or null
-  int* ctrl;    // packed sequences: word 1 tells of bounds that had to be clamped
+  float* kept;     // [tiles of the backward][width], or null
+  int* ctrl;
+  uint64_t* hand;  // [tiles][width], or null: no sequence has two tiles
+  int tiles;
+  bool keep_error;  // the call's second launch: the control word stays
   // backward
   const void* dout;
   const float* d_state_out;
   float* d_state_in;
   void *dx, *ddecay, *dgate;
-  float *drate, *partial;  // partial: [batch][width] sums of drate
+  float *drate, *partial;  // partial: [tiles][width] sums of drate
 };
 hipError_t launch_scan_fwd(const ScanParams& p, int dtype, hipStream_t stream);
+hipError_t launch_scan_prep(const ScanParams& p, hipStream_t stream);  // the others' first step
 hipError_t launch_scan_bwd(const ScanParams& p, int dtype, hipStream_t stream);
 
 struct ScanStepParams {

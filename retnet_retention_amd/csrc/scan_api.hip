@@ -11,6 +11,8 @@ using namespace ret_host;
 using ret::tile_count;
 
 constexpr int64_t kMaxTokens = (int64_t)INT32_MAX - 65536;  // room for a tile behind the last token
+constexpr int kSmallestTile = 128;                            // tokens of a workgroup, at least
+constexpr int64_t kMaxTileStride = 1 << 22;
 constexpr int64_t kMaxThreads = (int64_t)1 << 32;           // of a launch
 
 // Bounds that the sequence calls share; threads: of a launch, for each token tile
@@ -20,7 +22,7 @@ ret_status_t check_shape(int32_t batch, int32_t seqlen, int32_t width, int32_t d
   if (batch < 1 || seqlen < 1 || width < 1 || width > ret::kMaxScanWidth) return RET_ERR_SHAPE;
   const int64_t tokens = packed ? total : (int64_t)batch * seqlen;
   if (tokens < 0 || tokens > kMaxTokens) return RET_ERR_SHAPE;
-  const int64_t tiles = tile_count(batch, seqlen, packed, total, ret::kScanTile);
+  const int64_t tiles = tile_count(batch, seqlen, packed, total, kSmallestTile);
   if (tiles > INT32_MAX || tiles * ((width + 63) / 64) >= kMaxThreads / threads_per_tile) return RET_ERR_SHAPE;
   if (dtype != RET_F32 && dtype != RET_BF16) return RET_ERR_UNSUPPORTED;
   return RET_OK;
@@ -48,14 +50,19 @@ ret_status_t check_scan(const ret_scan_desc_t* d, bool packed, int64_t total) {
   if (!d) return RET_ERR_NULL;
   const ret_status_t st = check_shape(d->batch, d->seqlen, d->width, d->dtype, packed, total, 1024);
   if (st != RET_OK) return st;
-  if (!stride_ok(d->x_stride, d->width) || !stride_ok(d->decay_stride, d->width) || !stride_ok(d->gate_stride, d->width))
-    return RET_ERR_SHAPE;
+  const int64_t strides[] = {d->x_stride, d->decay_stride, d->gate_stride};
+  for (const int64_t s : strides) {
+    if (!stride_ok(s, d->width)) return RET_ERR_SHAPE;
+    // whole tiles are addressed with 32 bits from their first row
+    if (s >= kMaxTileStride && (packed || d->seqlen >= kSmallestTile)) return RET_ERR_SHAPE;
+  }
   return RET_OK;
 }
 
 struct ScanSizes {
-  size_t tokens, row, x, decay, gate, o, ddecay, state, weight, kept;
-  int64_t tiles;
+  size_t tokens, x, decay, gate, o, ddecay, state, weight, kept;
+  int64_t tiles, bwd_tiles;
+  bool chain, bwd_chain;  // whether tiles hand anything on
 };
 ScanSizes sizes_of(const ret_scan_desc_t* d, bool packed, int64_t total, bool gates) {
   ScanSizes s;
@@ -69,13 +76,20 @@ ScanSizes sizes_of(const ret_scan_desc_t* d, bool packed, int64_t total, bool ga
   s.weight = (size_t)d->width * sizeof(float);
   s.state = d->batch * s.weight;
   s.tiles = tile_count(d->batch, d->seqlen, packed, total, ret::kScanTile);
-  s.kept = s.tiles * s.weight;
+  s.bwd_tiles = tile_count(d->batch, d->seqlen, packed, total, ret::kScanBwdTile);
+  s.chain = ret::has_chain(d->seqlen, packed, total, ret::kScanTile);
+  s.bwd_chain = ret::has_chain(d->seqlen, packed, total, ret::kScanBwdTile);
+  s.kept = s.bwd_tiles * s.weight;
   return s;
 }
 
+// control block with the tickets | words handed on | backward: sums of drate | states
+// of its own forward. The forward that a backward runs uses the first two before it.
 void carve_scan(Carve& c, ret::ScanParams& p, const ScanSizes& s, bool grad, bool own_kept) {
-  c.part(p.ctrl, 2 * sizeof(int32_t));
-  if (grad) c.part(p.partial, s.state);
+  const bool chain = grad ? s.bwd_chain || (own_kept && s.chain) : s.chain;
+  c.part(p.ctrl, ret::kScanCtrlBytes);
+  if (chain) c.part(p.hand, (grad ? s.bwd_tiles : s.tiles) * s.weight * 2);
+  if (grad) c.part(p.partial, s.kept);
   if (own_kept) c.part(p.kept, s.kept);
 }
 size_t scan_workspace(const ret_scan_desc_t* d, bool packed, int64_t total, bool grad, bool own_kept) {
@@ -239,9 +253,10 @@ ret_status_t retention_scan_fwd(const ret_scan_desc_t* desc, const int32_t* cu_s
   ret::ScanParams p = params_of(desc, cu_seqlens, s, x, decay, rate, gate, state_in);
   p.o = o;
   p.state_out = state_out;
-  p.kept = kept;
   Carve c{static_cast<char*>(workspace)};
   carve_scan(c, p, s, false, false);
+  p.kept = kept;
+  p.tiles = (int)s.tiles;
   return status_of(ret::launch_scan_fwd(p, desc->dtype, stream));
 }
 
@@ -292,12 +307,17 @@ ret_status_t retention_scan_bwd(const ret_scan_desc_t* desc, const int32_t* cu_s
   p.drate = drate;
   Carve c{static_cast<char*>(workspace)};
   carve_scan(c, p, s, true, kept == nullptr);
+  uint64_t* hand = p.hand;
   if (!kept) {  // the forward once more, for the states alone
-    const hipError_t e = ret::launch_scan_fwd(p, desc->dtype, stream);
-    if (e != hipSuccess) return RET_ERR_HIP;
+    p.tiles = (int)s.tiles;
+    p.hand = s.chain ? hand : nullptr;
+    if (ret::launch_scan_fwd(p, desc->dtype, stream) != hipSuccess) return RET_ERR_HIP;
+    p.keep_error = true;
   } else {
     p.kept = const_cast<float*>(kept);
   }
+  p.tiles = (int)s.bwd_tiles;
+  p.hand = s.bwd_chain ? hand : nullptr;
   return status_of(ret::launch_scan_bwd(p, desc->dtype, stream));
 }
 

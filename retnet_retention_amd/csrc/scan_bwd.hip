@@ -4,78 +4,98 @@
 //     dla = a g h_(t-1) - (a^2 / m) g s_i x   (the second term with normalize)
 //     ddecay = dla, or -rate s_d (1 - s_d) dla;   drate = -sum of s_d dla
 //     d state_in = a_0 g_0
-// A workgroup walks a sequence's tiles from the last to the first for the 64 V
-// channels of its lanes. A tile's states are formed again from the state kept before
-// it; each wave folds its tokens both ways, and what the waves hand each other goes
-// through LDS once a tile.
+// Laid out as the forward, over tiles of 128 tokens (a segment holds twice its values
+// a token): the tile's states are formed again from the one kept before it, and the
+// gradient of the state behind it comes from the tile after it, as a word in memory.
+// Tiles start from the last. A tile's share of drate goes to a row of sums that a
+// second launch adds up in a fixed order.
 #include "norms.hpp"
 #include "scan_common.hpp"
 
+// The variants of a kernel give the same bits: fused multiply-adds only where they are written.
+#pragma clang fp contract(off)
+
 namespace ret {
 
-template <typename T, bool GATES, bool IGATE, bool NORM, int V, int L, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void scan_bwd_kernel(ScanParams p) {
+constexpr int kSegment = 8;  // tokens; 16 segments a tile
+
+template <typename T, bool GATES, bool IGATE, bool NORM, int V>
+__global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p) {
   using D = std::conditional_t<GATES, T, float>;
-  static_assert(L * WAVES == kScanTile, "");
-  __shared__ float s_a[2][WAVES][64 * V], s_u[2][WAVES][64 * V], s_r[2][WAVES][64 * V];
-  const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
-  const int groups = (p.width + 64 * V - 1) / (64 * V);
-  const int b = blockIdx.x / groups, at = (blockIdx.x % groups * 64 + lane) * V;
-  const bool inside = at < p.width;
-  const int c = min(at, p.width - V);
+  constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = kScanBwdTile / kSegment;
+  __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_p[SEGS][kScanChannels],
+      s_r[SEGS][kScanChannels], s_back[kScanChannels];
+  clear_errors(p);
+  const Place at = place_of<true>(p, kScanBwdTile);
+  if (!at.any) return;
   int tok0, len;
-  span_of(p, b, tok0, len);
-  float rate[V], back[V], sum[V];
+  span_of(p, at.b, tok0, len);
+  const int from = at.i * kScanBwdTile;
+  const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
+  const int c0 = at.group * kScanChannels, ch = c0 + lane;
+  if (from >= len && !(at.i == 0 && len == 0)) {
+    if (GATES && wave == 0 && ch < p.width) p.partial[at.tile * p.width + ch] = 0.f;
+    return;
+  }
+  const int seg = wave * 2 + lane / LW, cl = lane % LW * V;  // the lane's first segment
+  const int c = min(c0 + cl, p.width - V);
+  const bool inside = c0 + cl < p.width;
+  T* dx = reinterpret_cast<T*>(p.dx);
+  D* ddecay = reinterpret_cast<D*>(p.ddecay);
+  T* dgate = reinterpret_cast<T*>(p.dgate);
+  if (p.cu && at.i == 0) {
+    // rows before the first sequence and behind the last have gradient 0
+    auto clear = [&](int t0, int t1) {
+      const float zero[V] = {};
+      for (int64_t t = t0 + seg; t < t1 && inside; t += SEGS) {
+        lane_store<T, V>(dx + t * p.width, c, zero);
+        lane_store<D, V>(ddecay + t * p.width, c, zero);
+        if constexpr (IGATE) lane_store<T, V>(dgate + t * p.width, c, zero);
+      }
+    };
+    if (at.b == 0) clear(0, tok0);
+    if (at.b == p.batch - 1) clear(tok0 + len, p.total);
+  }
+  const int left = len - from, n = left - seg * kSegment;  // tokens from the tile's, the lane's start on
+  const int64_t row = (int64_t)tok0 + from;
+  lane_raw<T, V> rx[L], ro[L];
+  // sd, si: the sigmoids; rest: 1 - a^2; hist: inputs, then the state before each token
+  float a[L][V], sd[GATES ? L : 1][V], si[IGATE ? L : 1][V], rest[NORM ? L : 1][V], hist[L][V];
+  float A[PARTS][V], U[PARTS][V], R[PARTS][V], rate[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     rate[e] = GATES ? p.rate[c + e] : 0.f;
-    back[e] = p.d_state_out ? p.d_state_out[(int64_t)b * p.width + c + e] : 0.f;
-    sum[e] = 0.f;
-  }
-  const int64_t first_tile = p.cu ? tok0 / kScanTile + b : (int64_t)b * ((p.seqlen + kScanTile - 1) / kScanTile);
-  const T* x = reinterpret_cast<const T*>(p.x) + tok0 * p.x_stride;
-  const D* decay = reinterpret_cast<const D*>(p.decay) + tok0 * p.decay_stride;
-  const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? tok0 * p.gate_stride : 0);
-  const int64_t row0 = (int64_t)tok0 * p.width;
-  const T* dout = reinterpret_cast<const T*>(p.dout) + row0;
-  T* dx = reinterpret_cast<T*>(p.dx) + row0;
-  D* ddecay = reinterpret_cast<D*>(p.ddecay) + row0;
-  T* dgate = reinterpret_cast<T*>(p.dgate) + (IGATE ? row0 : 0);
-  // rows before the first sequence and behind the last have gradient 0
-  auto clear = [&](int from, int to) {
-    const float zero[V] = {};
-    for (int t = from + wave; t < to && inside; t += WAVES) {
-      const int64_t r = ((int64_t)t - tok0) * p.width;
-      lane_store<T, V>(dx + r, c, zero);
-      lane_store<D, V>(ddecay + r, c, zero);
-      if constexpr (IGATE) lane_store<T, V>(dgate + r, c, zero);
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      A[k][e] = 1.f;
+      U[k][e] = R[k][e] = 0.f;
     }
-  };
-  if (p.cu && b == 0) clear(0, tok0);
-  if (p.cu && b == p.batch - 1) clear(tok0 + len, p.total);
-  int turn = 0;
-  for (int base = (len - 1) / kScanTile * kScanTile; len > 0 && base >= 0; base -= kScanTile, turn ^= 1) {
-    const int t0 = base + wave * L, n = min(max(len - t0, 0), L);
-    lane_raw<T, V> rx[L], rg[IGATE ? L : 1], ro[L];
+  }
+
+  auto fold = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.x_stride;
+    const D* decay = reinterpret_cast<const D*>(p.decay) + row * p.decay_stride;
+    const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? row * p.gate_stride : 0);
+    const T* dout = reinterpret_cast<const T*>(p.dout) + row * p.width;
+    lane_raw<T, V> rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-      const int t = min(t0 + j, len - 1);
-      rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
-      rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
-      if constexpr (IGATE) rg[j] = lane_load<T, V>(gate + t * p.gate_stride, c);
-      ro[j] = lane_load<T, V>(dout + (int64_t)t * p.width, c);
-    }
-    float h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = p.kept[(first_tile + base / kScanTile) * p.width + c + e];
-    // sd, si: the sigmoids; hist: u, then the state before the token
-    float a[L][V], sd[GATES ? L : 1][V], si[IGATE ? L : 1][V], left[NORM ? L : 1][V], hist[L][V];
-    float A[V], U[V], R[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      A[e] = 1.f;
-      U[e] = R[e] = 0.f;
+      if constexpr (FULL) {
+        // a scalar row and a lane's offset of 32 bits (strides below 2^22)
+        rx[j] = lane_load<T, V>(x + j * p.x_stride, (uint32_t)seg * kSegment * (uint32_t)p.x_stride + c);
+        rd[j] = lane_load<D, V>(decay + j * p.decay_stride, (uint32_t)seg * kSegment * (uint32_t)p.decay_stride + c);
+        if constexpr (IGATE)
+          rg[j] = lane_load<T, V>(gate + j * p.gate_stride, (uint32_t)seg * kSegment * (uint32_t)p.gate_stride + c);
+        ro[j] = lane_load<T, V>(dout + j * p.width, (uint32_t)seg * kSegment * p.width + c);
+      } else {
+        const int64_t t = min(seg * kSegment + j, left - 1);
+        rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
+        rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
+        if constexpr (IGATE) rg[j] = lane_load<T, V>(gate + t * p.gate_stride, c);
+        ro[j] = lane_load<T, V>(dout + t * p.width, c);
+      }
     }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
@@ -85,26 +105,27 @@ __global__ __launch_bounds__(WAVES * 64) void scan_bwd_kernel(ScanParams p) {
       if constexpr (IGATE) Lane<T, V>::get(rg[j], g);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        float la = d[e], lf;
+        float la = d[e], q;
         if constexpr (GATES) {
           sd[j][e] = sigmoid_of(d[e], T());
           la = -rate[e] * sd[j][e];
         }
-        factor<T>(la, a[j][e], lf);
+        factor<T>(la, a[j][e], q);
         if constexpr (IGATE) {
           si[j][e] = sigmoid_of(g[e], T());
           hist[j][e] *= si[j][e];
         }
         if constexpr (NORM) {
-          left[j][e] = lf;
-          hist[j][e] *= __builtin_amdgcn_sqrtf(lf);
+          rest[j][e] = q;
+          hist[j][e] *= __builtin_amdgcn_sqrtf(q);
         }
-        if (j >= n) {  // behind the end
+        if (!FULL && j >= n) {  // behind the end
           a[j][e] = 1.f;
           hist[j][e] = 0.f;
         }
-        U[e] = step_or_forget(a[j][e], U[e], hist[j][e]);
-        A[e] *= a[j][e];
+        float &A1 = A[j / kSegment][e], &U1 = U[j / kSegment][e];
+        U1 = fmaf(a[j][e], U1, hist[j][e]);
+        A1 *= a[j][e];
       }
     }
 #pragma unroll
@@ -113,106 +134,182 @@ __global__ __launch_bounds__(WAVES * 64) void scan_bwd_kernel(ScanParams p) {
       Lane<T, V>::get(ro[j], d);
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        if (j < n) R[e] = a[j][e] == 0.f ? 0.f : a[j][e] * (R[e] + d[e]);
+        if (FULL || j < n) R[j / kSegment][e] = a[j][e] * (R[j / kSegment][e] + d[e]);
     }
+  };
+  const bool full = left >= kScanBwdTile;
+  if (full)
+    fold(std::true_type());
+  else if (len > 0)
+    fold(std::false_type());
+  // a factor of 0 among the tokens (or a product that is): they may have to forget what is no number
+  bool forgets = false;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      s_a[turn][wave][lane * V + e] = A[e];
-      s_u[turn][wave][lane * V + e] = U[e];
-      s_r[turn][wave][lane * V + e] = R[e];
-    }
-    __syncthreads();
-    float g[V];
+  for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-      if (w < wave) {
+    for (int e = 0; e < V; ++e) forgets |= A[k][e] == 0.f;
+  forgets = __any(forgets);
+  if (forgets) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = step_or_forget(s_a[turn][w][lane * V + e], h[e], s_u[turn][w][lane * V + e]);
-      }
-#pragma unroll
-    for (int w = WAVES - 1; w >= 0; --w) {
+    for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if (w == wave) g[e] = back[e];
-        back[e] = step_or_forget(s_a[turn][w][lane * V + e], back[e], s_r[turn][w][lane * V + e]);
+        float& U1 = U[j / kSegment][e];
+        U1 = step_or_forget(a[j][e], j % kSegment ? U1 : 0.f, hist[j][e]);
+      }
+#pragma unroll
+    for (int j = L - 1; j >= 0; --j) {
+      float d[V];
+      Lane<T, V>::get(ro[j], d);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float& R1 = R[j / kSegment][e];
+        if ((j + 1) % kSegment == 0) R1 = 0.f;
+        if (j < n) R1 = a[j][e] == 0.f ? 0.f : a[j][e] * (R1 + d[e]);
       }
     }
+  }
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s_a[seg + k][cl + e] = A[k][e];
+      s_u[seg + k][cl + e] = U[k][e];
+      s_r[seg + k][cl + e] = R[k][e];
+    }
+  __syncthreads();
+  const bool mine = ch < p.width;
+  if (wave == 0) {
+    // gradients from behind
+    const bool last = left <= kScanBwdTile;
+    const int64_t held = (int64_t)at.b * p.width + ch;
+    float fa[SEGS], fr[SEGS], ta = 1.f, tr = 0.f;
+#pragma unroll
+    for (int s = SEGS - 1; s >= 0; --s) {
+      const float sa = s_a[s][lane], sr = s_r[s][lane];
+      fa[s] = ta;
+      fr[s] = tr;
+      tr = step_or_forget(sa, tr, sr);
+      ta *= sa;
+    }
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) {
+      s_p[s][lane] = fa[s];
+      s_r[s][lane] = fr[s];
+    }
+    float back = 0.f;
+    if (!last)
+      back = take_over(p.hand + (at.tile + 1) * p.width + ch, mine, p.ctrl);
+    else if (p.d_state_out && mine)
+      back = p.d_state_out[held];
+    s_back[lane] = back;
+    back = step_or_forget(ta, back, tr);
+    if (mine) {
+      if (at.i > 0)
+        hand_on(p.hand + at.tile * p.width + ch, back);
+      else if (p.d_state_in)
+        p.d_state_in[held] = back;
+    }
+  } else if (wave == 1) {
+    // states from before
+    float h = 0.f, before[SEGS];
+    if (mine && len > 0) h = p.kept[(kept_row(p, at.b, tok0) + at.i) * p.width + ch];
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) {
+      before[s] = h;
+      h = step_or_forget(s_a[s][lane], h, s_u[s][lane]);
+    }
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) s_u[s][lane] = before[s];
+  }
+  __syncthreads();
+  float sum[PARTS][V] = {};
+  auto run = [&](auto whole, auto forget) {
+    constexpr bool FULL = decltype(whole)::value, FORGET = decltype(forget)::value;
+    float h[V], g[V];  // g: what reaches the token's state from behind
 #pragma unroll
     for (int j = 0; j < L; ++j) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
+        if (j % kSegment == 0) h[e] = s_u[seg + j / kSegment][cl + e];
         const float u = hist[j][e];
         hist[j][e] = h[e];
-        h[e] = step_or_forget(a[j][e], h[e], u);
+        h[e] = FORGET ? step_or_forget(a[j][e], h[e], u) : fmaf(a[j][e], h[e], u);
       }
     }
-    // g: what reaches the token's state from behind
+    const uint32_t off = (uint32_t)seg * kSegment * p.width + c;
+    dx += row * p.width;
+    ddecay += row * p.width;
+    if (IGATE) dgate += row * p.width;
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
       float xs[V], d[V], o1[V], o2[V], o3[V];
+      if ((j + 1) % kSegment == 0) {
+        const int k = seg + j / kSegment;
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] = step_or_forget(s_p[k][cl + e], s_back[cl + e], s_r[k][cl + e]);
+      }
       Lane<T, V>::get(rx[j], xs);
       Lane<T, V>::get(ro[j], d);
-      if (j < n) {
+      if (FULL || j < n) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           g[e] += d[e];
           const float s = IGATE ? si[j][e] : 1.f, av = a[j][e];
           // a token that forgets lets no gradient through, whatever reaches it
-          const float ag = av == 0.f ? 0.f : av * g[e];
-          float dla = av == 0.f ? 0.f : ag * hist[j][e], m = 1.f;
+          const bool none = FORGET && av == 0.f;
+          const float ag = none ? 0.f : av * g[e];
+          float dla = none ? 0.f : ag * hist[j][e], m = 1.f;
           if constexpr (NORM) {
             // a^2 / m; 0 where the decay is 0, the limit towards which ddecay goes
-            const float inv = left[j][e] > 0.f ? __builtin_amdgcn_rsqf(left[j][e]) : 0.f;
-            m = left[j][e] * inv;
-            dla -= ag * av * inv * s * xs[e];
+            const float inv = rest[j][e] > 0.f ? __builtin_amdgcn_rsqf(rest[j][e]) : 0.f;
+            m = rest[j][e] * inv;
+            dla = fmaf(-ag * av * inv, s * xs[e], dla);
           }
-          const float gm = g[e] * m;
-          o1[e] = gm * s;
+          o1[e] = g[e] * m * s;
           if constexpr (IGATE) o3[e] = o1[e] * xs[e] * (1.f - s);
           if constexpr (GATES) {
-            const float t = sd[j][e] * dla;
-            sum[e] -= t;
-            o2[e] = -rate[e] * (1.f - sd[j][e]) * t;
+            sum[j / kSegment][e] = fmaf(-sd[j][e], dla, sum[j / kSegment][e]);
+            o2[e] = -rate[e] * (1.f - sd[j][e]) * (sd[j][e] * dla);
           } else {
             o2[e] = dla;
           }
           g[e] = ag;
         }
         if (inside) {
-          lane_store<T, V>(dx + (int64_t)(t0 + j) * p.width, c, o1);
-          lane_store<D, V>(ddecay + (int64_t)(t0 + j) * p.width, c, o2);
-          if constexpr (IGATE) lane_store<T, V>(dgate + (int64_t)(t0 + j) * p.width, c, o3);
+          lane_store<T, V>(dx + j * p.width, off, o1);
+          lane_store<D, V>(ddecay + j * p.width, off, o2);
+          if constexpr (IGATE) lane_store<T, V>(dgate + j * p.width, off, o3);
         }
       }
     }
-  }
-  if (p.d_state_in && wave == 0 && inside) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) p.d_state_in[(int64_t)b * p.width + c + e] = back[e];
+  };
+  if (len > 0) {
+    if (forgets)
+      run(std::false_type(), std::true_type());
+    else if (full)
+      run(std::true_type(), std::false_type());
+    else
+      run(std::false_type(), std::false_type());
   }
   if constexpr (GATES) {
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s_a[seg + k][cl + e] = sum[k][e];
     __syncthreads();
+    if (wave == 0 && mine) {
+      float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) s_a[0][wave][lane * V + e] = sum[e];
-    __syncthreads();
-    if (wave == 0 && inside) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) s += s_a[0][w][lane * V + e];
-        p.partial[(int64_t)b * p.width + c + e] = s;
-      }
+      for (int k = 0; k < SEGS; ++k) s += s_a[k][lane];
+      p.partial[at.tile * p.width + ch] = s;
     }
   }
 }
 
 template <typename T, bool GATES, bool IGATE, bool NORM, int V>
 static hipError_t launch_bwd(const ScanParams& p, hipStream_t stream) {
-  constexpr int L = 8, WAVES = kScanTile / L;
-  const int64_t groups = (p.width + 64 * V - 1) / (64 * V);
-  hipLaunchKernelGGL((scan_bwd_kernel<T, GATES, IGATE, NORM, V, L, WAVES>), dim3((unsigned)(groups * p.batch)),
-                     dim3(WAVES * 64), 0, stream, p);
+  hipLaunchKernelGGL((scan_bwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 template <typename T, int V>
@@ -230,15 +327,13 @@ static hipError_t launch_bwd_v(const ScanParams& p, hipStream_t s) {
   }
 }
 hipError_t launch_scan_bwd(const ScanParams& p, int dtype, hipStream_t stream) {
-  if (p.cu) {
-    const hipError_t e = launch_check_bounds(p.cu, p.batch, p.total, p.ctrl, stream);
-    if (e != hipSuccess) return e;
-  }
-  hipError_t e = dtype != 1 ? launch_bwd_v<float, 1>(p, stream)
-                 : in_pairs(p) ? launch_bwd_v<bf16, 2>(p, stream)
-                            : launch_bwd_v<bf16, 1>(p, stream);
+  hipError_t e = launch_scan_prep(p, stream);
+  if (e != hipSuccess) return e;
+  e = dtype != 1     ? launch_bwd_v<float, 1>(p, stream)
+      : in_pairs(p) ? launch_bwd_v<bf16, 2>(p, stream)
+                    : launch_bwd_v<bf16, 1>(p, stream);
   if (e != hipSuccess || !p.rate) return e;
-  return launch_column_sum(p.partial, p.batch, p.width, p.drate, stream);
+  return launch_column_sum(p.partial, p.tiles, p.width, p.drate, stream);
 }
 
 }  // namespace ret

@@ -7,6 +7,8 @@
 #include "common.hpp"
 #include "scan.hpp"
 
+#pragma clang fp contract(off)
+
 namespace ret {
 
 // V neighbouring channels of a token, as they lie in memory and as floats.
@@ -43,14 +45,14 @@ template <> struct Lane<float, 2> {
 template <typename T, int V>
 using lane_raw = typename Lane<T, V>::Raw;
 
-// `row`: a wave-uniform pointer to a token's first channel
+// `row`: a wave-uniform pointer; `at`: a lane's elements behind it, below 2^32 bytes
 template <typename T, int V>
-__device__ __forceinline__ lane_raw<T, V> lane_load(const T* row, int c) {
-  return *reinterpret_cast<const lane_raw<T, V>*>(row + c);
+__device__ __forceinline__ lane_raw<T, V> lane_load(const T* row, uint32_t at) {
+  return *reinterpret_cast<const lane_raw<T, V>*>(reinterpret_cast<const char*>(row) + at * (uint32_t)sizeof(T));
 }
 template <typename T, int V>
-__device__ __forceinline__ void lane_store(T* row, int c, const float* x) {
-  *reinterpret_cast<lane_raw<T, V>*>(row + c) = Lane<T, V>::put(x);
+__device__ __forceinline__ void lane_store(T* row, uint32_t at, const float* x) {
+  *reinterpret_cast<lane_raw<T, V>*>(reinterpret_cast<char*>(row) + at * (uint32_t)sizeof(T)) = Lane<T, V>::put(x);
 }
 
 // Whether a lane may take two bf16 channels of every tensor at once.
@@ -69,6 +71,12 @@ __device__ __forceinline__ void span_of(const P& p, int b, int& tok0, int& len) 
     tok0 = b * p.seqlen;
     len = p.seqlen;
   }
+}
+
+// Row of the kept states: before token 0 of sequence b.
+template <typename P>
+__device__ __forceinline__ int64_t kept_row(const P& p, int b, int tok0) {
+  return p.cu ? tok0 / kScanBwdTile + b : (int64_t)b * ((p.seqlen + kScanBwdTile - 1) / kScanBwdTile);
 }
 
 // Tile `j` as sequence b and its tile i, for tiles numbered as scan.hpp tells.
@@ -125,6 +133,83 @@ __device__ __forceinline__ void factor(float la, float& a, float& left) {
   const bool near = fabsf(la) < (wide ? 0.25f : 0.03125f);
   a = near ? 1.f + p : e;
   left = near ? -p * (2.f + p) : fmaf(-e, e, 1.f);
+}
+
+// A workgroup's tile and channels. Where tiles hand a state on, a workgroup takes
+// them by a ticket, so that whoever it waits for holds a lower one and runs already.
+// One counter for all of a launch would serialise its workgroups, so each has one of
+// up to 32 for its own part of the channels. Tiles of a queue run along time first,
+// the sequences of a batch side by side (reversed in the backward).
+struct ScanQueues {
+  int groups, each, queues;  // channel groups, those of a queue, queues
+};
+__host__ __device__ inline ScanQueues queues_of(int width) {
+  ScanQueues q;
+  q.groups = (width + kScanChannels - 1) / kScanChannels;
+  q.each = (q.groups + kScanQueues - 1) / kScanQueues;
+  q.queues = (q.groups + q.each - 1) / q.each;
+  return q;
+}
+// The control word of a call without a launch that clears it.
+template <typename P>
+__device__ __forceinline__ void clear_errors(const P& p) {
+  if (!p.hand && !p.cu && !p.keep_error && blockIdx.x == 0 && threadIdx.x < 2) p.ctrl[threadIdx.x] = 0;
+}
+struct Place {
+  int group, b, i;     // channel group, sequence, tile of it
+  int64_t tile;        // its number
+  bool any;
+};
+template <bool BACK, typename P>
+__device__ __forceinline__ Place place_of(const P& p, int tile) {
+  __shared__ int s_ticket;
+  const ScanQueues q = queues_of(p.width);
+  const int queue = blockIdx.x % q.queues;
+  int ticket = blockIdx.x / q.queues;
+  if (p.hand) {
+    if (threadIdx.x == 0) s_ticket = atomicAdd(p.ctrl + 16 * (1 + queue), 1);
+    __syncthreads();
+    ticket = uniform_i(s_ticket);
+  }
+  Place at;
+  at.group = queue + q.queues * (ticket % q.each);
+  int j = ticket / q.each;
+  if (BACK) j = p.tiles - 1 - j;
+  if (p.cu) {
+    tile_of(p, j, tile, at.b, at.i);
+    at.tile = j;
+  } else {
+    at.b = j % p.batch;
+    at.i = j / p.batch;
+    at.tile = (int64_t)at.b * (p.tiles / p.batch) + at.i;
+  }
+  at.any = at.group < q.groups;
+  return at;
+}
+inline unsigned scan_grid(const ScanParams& p) {
+  const ScanQueues q = queues_of(p.width);
+  return (unsigned)p.tiles * q.queues * q.each;
+}
+
+// A word that hands a value on: the value and a mark, in one store and one load, so
+// that nothing else has to be ordered around them. Agent scope: workgroups of other
+// XCDs, behind other L2s, see it.
+__device__ __forceinline__ void hand_on(uint64_t* word, float x) {
+  __hip_atomic_store(word, (uint64_t)__float_as_uint(x) | 1ull << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Waits until the word is there, in every lane of the wave that asks.
+__device__ __forceinline__ float take_over(const uint64_t* word, bool asks, int* ctrl) {
+  constexpr int kSpinLimit = 1 << 21;  // some seconds
+  uint64_t w = 0;
+  for (int spins = 0;; ++spins) {
+    if (asks) w = __hip_atomic_load(const_cast<uint64_t*>(word), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__all(!asks || (w >> 32))) break;
+    if (spins > kSpinLimit) {
+      atomicOr(ctrl + 1, 1);
+      break;
+    }
+  }
+  return __uint_as_float((uint32_t)w);
 }
 
 // A factor of 0 forgets what was there, NaN and infinity too.

@@ -1,58 +1,73 @@
 // Gated linear recurrence, forward: per channel
 //     h_t = a_t h_(t-1) + m_t sigmoid(gate_t) x_t,   a_t = exp(la_t),
 // la_t given, or -rate sigmoid(decay_t); m_t = sqrt(1 - a_t^2) or 1.
-// A workgroup walks a sequence in tiles of 128 tokens for the 64 V channels of its
-// lanes. Each wave holds 16 tokens of a tile in registers: it forms their factors
-// and inputs, folds them to one factor A and one input U, and the waves' pairs meet
-// in LDS; each then runs its tokens from the state that reaches it.
+// Bound by memory (8 bytes an element in bf16 with both gates) with the gates'
+// arithmetic close behind. Every element is read once: a workgroup holds 256 tokens
+// of 64 channels in registers, as factors a and inputs u, a wave two segments of 16
+// tokens: side by side in its half waves where lanes take pairs of bf16 channels, one
+// after the other with single channels (so that both give the same bits). Each
+// segment folds its tokens to one factor A and one input U, these meet in LDS, and
+// one wave, a lane a channel, runs them into states before each segment. The
+// state before the tile comes from the tile before it, as a word in memory that this
+// wave waits for; then every segment runs its tokens from its state and stores them.
+// Waiting one after the other takes 0.65 us a tile, less than the tiles of a
+// long sequence take at the memory's rate unless it is narrower than some 1000
+// channels; so tiles are long, 256 tokens.
 #include "scan_common.hpp"
+
+// The variants of a kernel give the same bits: fused multiply-adds only where they are written.
+#pragma clang fp contract(off)
 
 namespace ret {
 
-template <typename T, bool GATES, bool IGATE, bool NORM, int V, int L, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void scan_fwd_kernel(ScanParams p) {
+constexpr int kSegment = 16;  // tokens; 16 segments a tile
+
+template <typename T, bool GATES, bool IGATE, bool NORM, int V>
+__global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
   using D = std::conditional_t<GATES, T, float>;
-  static_assert(L * WAVES == kScanTile, "");
-  __shared__ float s_a[2][WAVES][64 * V], s_u[2][WAVES][64 * V];
-  const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
-  const int groups = (p.width + 64 * V - 1) / (64 * V);
-  const int b = blockIdx.x / groups, at = (blockIdx.x % groups * 64 + lane) * V;
-  const bool inside = at < p.width;
-  const int c = min(at, p.width - V);
+  constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = kScanTile / kSegment;
+  __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_h[kScanChannels];
+  clear_errors(p);
+  const Place at = place_of<false>(p, kScanTile);
+  if (!at.any) return;
   int tok0, len;
-  span_of(p, b, tok0, len);
-  float rate[V], carry[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    rate[e] = GATES ? p.rate[c + e] : 0.f;
-    carry[e] = p.state_in ? p.state_in[(int64_t)b * p.width + c + e] : 0.f;
-  }
-  const int64_t first_tile = p.cu ? tok0 / kScanTile + b : (int64_t)b * ((p.seqlen + kScanTile - 1) / kScanTile);
-  const T* x = reinterpret_cast<const T*>(p.x) + tok0 * p.x_stride;
-  const D* decay = reinterpret_cast<const D*>(p.decay) + tok0 * p.decay_stride;
-  const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? tok0 * p.gate_stride : 0);
-  T* o = reinterpret_cast<T*>(p.o) + (int64_t)tok0 * p.width;
-  int turn = 0;
-  for (int base = 0; base < len; base += kScanTile, turn ^= 1) {
-    if (p.kept && wave == 0 && inside) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) p.kept[(first_tile + base / kScanTile) * p.width + c + e] = carry[e];
-    }
-    const int t0 = base + wave * L, n = min(max(len - t0, 0), L);
+  span_of(p, at.b, tok0, len);
+  const int from = at.i * kScanTile;  // the tile's first token
+  if (from >= len && !(at.i == 0 && len == 0)) return;
+  const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
+  const int seg = wave * 2 + lane / LW, cl = lane % LW * V;  // the lane's first segment
+  const int c0 = at.group * kScanChannels, c = min(c0 + cl, p.width - V);
+  const bool inside = c0 + cl < p.width;
+  const int left = len - from, n = left - seg * kSegment;  // tokens from the tile's, the lane's start on
+  float a[L][V], u[L][V], A[PARTS][V], U[PARTS][V];
+
+  auto fold = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const int64_t row = (int64_t)tok0 + from;
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.x_stride;
+    const D* decay = reinterpret_cast<const D*>(p.decay) + row * p.decay_stride;
+    const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? row * p.gate_stride : 0);
     lane_raw<T, V> rx[L], rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-      const int t = min(t0 + j, len - 1);
-      rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
-      rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
-      if constexpr (IGATE) rg[j] = lane_load<T, V>(gate + t * p.gate_stride, c);
+      if constexpr (FULL) {
+        // a scalar row and a lane's offset of 32 bits (strides below 2^22)
+        rx[j] = lane_load<T, V>(x + j * p.x_stride, (uint32_t)seg * kSegment * (uint32_t)p.x_stride + c);
+        rd[j] = lane_load<D, V>(decay + j * p.decay_stride, (uint32_t)seg * kSegment * (uint32_t)p.decay_stride + c);
+        if constexpr (IGATE)
+          rg[j] = lane_load<T, V>(gate + j * p.gate_stride, (uint32_t)seg * kSegment * (uint32_t)p.gate_stride + c);
+      } else {
+        const int64_t t = min(seg * kSegment + j, left - 1);
+        rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
+        rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
+        if constexpr (IGATE) rg[j] = lane_load<T, V>(gate + t * p.gate_stride, c);
+      }
     }
-    float a[L][V], u[L][V], A[V], U[V];
+    float rate[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      A[e] = 1.f;
-      U[e] = 0.f;
+      rate[e] = GATES ? p.rate[c + e] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
@@ -63,46 +78,148 @@ __global__ __launch_bounds__(WAVES * 64) void scan_fwd_kernel(ScanParams p) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float la = GATES ? -rate[e] * sigmoid_of(a[j][e], T()) : a[j][e];
-        float left;
-        factor<T>(la, a[j][e], left);
+        float rest;
+        factor<T>(la, a[j][e], rest);
         if constexpr (IGATE) u[j][e] *= sigmoid_of(g[e], T());
-        if constexpr (NORM) u[j][e] *= __builtin_amdgcn_sqrtf(left);
-        if (j >= n) {  // behind the end
+        if constexpr (NORM) u[j][e] *= __builtin_amdgcn_sqrtf(rest);
+        if (!FULL && j >= n) {  // behind the end
           a[j][e] = 1.f;
           u[j][e] = 0.f;
         }
-        U[e] = step_or_forget(a[j][e], U[e], u[j][e]);
-        A[e] *= a[j][e];
+        float &A1 = A[j / kSegment][e], &U1 = U[j / kSegment][e];
+        U1 = fmaf(a[j][e], U1, u[j][e]);
+        A1 *= a[j][e];
       }
     }
+  };
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      s_a[turn][wave][lane * V + e] = A[e];
-      s_u[turn][wave][lane * V + e] = U[e];
+      A[k][e] = 1.f;
+      U[k][e] = 0.f;
     }
-    __syncthreads();
-    float h[V];
+  const bool full = left >= kScanTile;
+  if (full)
+    fold(std::true_type());
+  else if (len > 0)
+    fold(std::false_type());
+  // a factor of 0 among the tokens (or a product that is): they may have to forget what is no number
+  bool forgets = false;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
+  for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) forgets |= A[k][e] == 0.f;
+  forgets = __any(forgets);
+  if (forgets) {
+#pragma unroll
+    for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if (w == wave) h[e] = carry[e];
-        carry[e] = step_or_forget(s_a[turn][w][lane * V + e], carry[e], s_u[turn][w][lane * V + e]);
+        float& U1 = U[j / kSegment][e];
+        U1 = step_or_forget(a[j][e], j % kSegment ? U1 : 0.f, u[j][e]);
       }
+  }
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s_a[seg + k][cl + e] = A[k][e];
+      s_u[seg + k][cl + e] = U[k][e];
     }
-    if (p.o) {
+  __syncthreads();
+  if (wave == 0) {
+    const int ch = c0 + lane;
+    const bool mine = ch < p.width, last = left <= kScanTile;
+    const int64_t held = (int64_t)at.b * p.width + ch;
+    float fa[SEGS], fu[SEGS], ta = 1.f, tu = 0.f;
 #pragma unroll
-      for (int j = 0; j < L; ++j) {
+    for (int s = 0; s < SEGS; ++s) {
+      const float sa = s_a[s][lane], su = s_u[s][lane];
+      fa[s] = ta;
+      fu[s] = tu;
+      tu = step_or_forget(sa, tu, su);
+      ta *= sa;
+    }
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = step_or_forget(a[j][e], h[e], u[j][e]);
-        if (j < n && inside) lane_store<T, V>(o + (int64_t)(t0 + j) * p.width, c, h);
-      }
+    for (int s = 0; s < SEGS; ++s) {
+      s_a[s][lane] = fa[s];
+      s_u[s][lane] = fu[s];
+    }
+    float h = 0.f;
+    if (at.i > 0)
+      h = take_over(p.hand + (at.tile - 1) * p.width + ch, mine, p.ctrl);
+    else if (p.state_in && mine)
+      h = p.state_in[held];
+    s_h[lane] = h;
+    h = step_or_forget(ta, h, tu);
+    if (mine) {
+      if (!last)
+        hand_on(p.hand + at.tile * p.width + ch, h);
+      else if (p.state_out)
+        p.state_out[held] = h;
     }
   }
-  if (p.state_out && wave == 0 && inside) {
+  __syncthreads();
+  if (!inside || len == 0) return;
+  float h0[PARTS][V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) p.state_out[(int64_t)b * p.width + c + e] = carry[e];
+  for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      h0[k][e] = step_or_forget(s_a[seg + k][cl + e], s_h[cl + e], s_u[seg + k][cl + e]);
+  if (p.kept && seg * kSegment % kScanBwdTile == 0 && n > 0) {
+    float* kept = p.kept + (kept_row(p, at.b, tok0) + (from + seg * kSegment) / kScanBwdTile) * p.width + c;
+#pragma unroll
+    for (int e = 0; e < V; ++e) kept[e] = h0[0][e];
   }
+  if (!p.o) return;
+  T* o = reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width;
+  auto run = [&](auto full, auto forget) {
+    float h[V];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (j % kSegment == 0) h[e] = h0[j / kSegment][e];
+        h[e] = decltype(forget)::value ? step_or_forget(a[j][e], h[e], u[j][e]) : fmaf(a[j][e], h[e], u[j][e]);
+      }
+      if (decltype(full)::value || j < n) lane_store<T, V>(o + j * p.width, (uint32_t)seg * kSegment * p.width + c, h);
+    }
+  };
+  if (forgets)
+    run(std::false_type(), std::true_type());
+  else if (full)
+    run(std::true_type(), std::false_type());
+  else
+    run(std::false_type(), std::false_type());
+}
+
+// Clears what the workgroups hand each other and checks packed bounds.
+__global__ __launch_bounds__(256) void scan_prep_kernel(ScanParams p, int64_t words) {
+  if (blockIdx.x == 0) {
+    bool ok = true;
+    if (p.cu)
+      for (int i = threadIdx.x; i < p.batch; i += 256) {
+        int t0, n;
+        ok = clamp_span(p.cu[i], p.cu[i + 1], p.total, p.total, t0, n) && ok;
+      }
+    ok = __syncthreads_and(ok);
+    for (int i = threadIdx.x; i < (p.hand ? (int)kScanCtrlBytes / 4 : 2); i += 256)
+      if (i != 1) p.ctrl[i] = 0;
+    if (threadIdx.x == 0 && !p.keep_error) p.ctrl[1] = ok ? 0 : 2;
+  }
+  const u32x4 zero = {0, 0, 0, 0};
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words / 2; i += (int64_t)gridDim.x * 256)
+    reinterpret_cast<u32x4*>(p.hand)[i] = zero;
+  if (words % 2 && blockIdx.x == 0 && threadIdx.x == 0) p.hand[words - 1] = 0;
+}
+hipError_t launch_scan_prep(const ScanParams& p, hipStream_t stream) {
+  if (!p.hand && !p.cu) return hipSuccess;  // the kernels themselves clear the control word
+  const int64_t words = p.hand ? (int64_t)p.tiles * p.width : 0, blocks = (words + 2047) / 2048;
+  hipLaunchKernelGGL(scan_prep_kernel, dim3((unsigned)(blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks)), dim3(256), 0,
+                     stream, p, words);
+  return hipGetLastError();
 }
 
 __global__ __launch_bounds__(256) void check_bounds_kernel(const int* cu, int batch, int total, int* ctrl) {
@@ -124,10 +241,7 @@ hipError_t launch_check_bounds(const int* cu, int batch, int total, int* ctrl, h
 
 template <typename T, bool GATES, bool IGATE, bool NORM, int V>
 static hipError_t launch_fwd(const ScanParams& p, hipStream_t stream) {
-  constexpr int L = 16, WAVES = kScanTile / L;
-  const int64_t groups = (p.width + 64 * V - 1) / (64 * V);
-  hipLaunchKernelGGL((scan_fwd_kernel<T, GATES, IGATE, NORM, V, L, WAVES>), dim3((unsigned)(groups * p.batch)),
-                     dim3(WAVES * 64), 0, stream, p);
+  hipLaunchKernelGGL((scan_fwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 template <typename T, int V>
@@ -145,10 +259,8 @@ static hipError_t launch_fwd_v(const ScanParams& p, hipStream_t s) {
   }
 }
 hipError_t launch_scan_fwd(const ScanParams& p, int dtype, hipStream_t stream) {
-  if (p.cu) {
-    const hipError_t e = launch_check_bounds(p.cu, p.batch, p.total, p.ctrl, stream);
-    if (e != hipSuccess) return e;
-  }
+  const hipError_t e = launch_scan_prep(p, stream);
+  if (e != hipSuccess) return e;
   if (dtype != 1) return launch_fwd_v<float, 1>(p, stream);
   return in_pairs(p) ? launch_fwd_v<bf16, 2>(p, stream) : launch_fwd_v<bf16, 1>(p, stream);
 }
