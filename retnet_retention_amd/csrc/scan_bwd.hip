@@ -20,7 +20,7 @@ namespace ret {
 constexpr int kSegment = 8;  // tokens; 16 segments a tile
 
 template <typename T, bool GATES, bool IGATE, bool NORM, int V>
-__global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p) {
+__global__ __launch_bounds__(512, 4) void scan_bwd_kernel(ScanParams p) {
   using D = std::conditional_t<GATES, T, float>;
   constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = kScanBwdTile / kSegment;
   __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_p[SEGS][kScanChannels],
@@ -80,16 +80,20 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p) {
     const T* dout = reinterpret_cast<const T*>(p.dout) + row * p.width;
     lane_raw<T, V> rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
+    if constexpr (FULL) {
+      const Rows<T, V> xs(x, p.x_stride, seg * kSegment, c), gs(gate, p.gate_stride, seg * kSegment, c);
+      const Rows<T, V> os(dout, p.width, seg * kSegment, c);
+      const Rows<D, V> ds(decay, p.decay_stride, seg * kSegment, c);
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      if constexpr (FULL) {
-        // a scalar row and a lane's offset of 32 bits (strides below 2^22)
-        rx[j] = lane_load<T, V>(x + j * p.x_stride, (uint32_t)seg * kSegment * (uint32_t)p.x_stride + c);
-        rd[j] = lane_load<D, V>(decay + j * p.decay_stride, (uint32_t)seg * kSegment * (uint32_t)p.decay_stride + c);
-        if constexpr (IGATE)
-          rg[j] = lane_load<T, V>(gate + j * p.gate_stride, (uint32_t)seg * kSegment * (uint32_t)p.gate_stride + c);
-        ro[j] = lane_load<T, V>(dout + j * p.width, (uint32_t)seg * kSegment * p.width + c);
-      } else {
+      for (int j = 0; j < L; ++j) {
+        rx[j] = xs.load(j);
+        rd[j] = ds.load(j);
+        if constexpr (IGATE) rg[j] = gs.load(j);
+        ro[j] = os.load(j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
         const int64_t t = min(seg * kSegment + j, left - 1);
         rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
         rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
@@ -237,10 +241,9 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p) {
         h[e] = FORGET ? step_or_forget(a[j][e], h[e], u) : fmaf(a[j][e], h[e], u);
       }
     }
-    const uint32_t off = (uint32_t)seg * kSegment * p.width + c;
-    dx += row * p.width;
-    ddecay += row * p.width;
-    if (IGATE) dgate += row * p.width;
+    const Rows<T, V> to_x(dx + row * p.width, p.width, seg * kSegment, c);
+    const Rows<D, V> to_decay(ddecay + row * p.width, p.width, seg * kSegment, c);
+    const Rows<T, V> to_gate(dgate + (IGATE ? row * p.width : 0), p.width, seg * kSegment, c);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
       float xs[V], d[V], o1[V], o2[V], o3[V];
@@ -277,9 +280,9 @@ __global__ __launch_bounds__(512) void scan_bwd_kernel(ScanParams p) {
           g[e] = ag;
         }
         if (inside) {
-          lane_store<T, V>(dx + j * p.width, off, o1);
-          lane_store<D, V>(ddecay + j * p.width, off, o2);
-          if constexpr (IGATE) lane_store<T, V>(dgate + j * p.width, off, o3);
+          to_x.store(j, o1);
+          to_decay.store(j, o2);
+          if constexpr (IGATE) to_gate.store(j, o3);
         }
       }
     }

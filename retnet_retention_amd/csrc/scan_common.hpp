@@ -11,6 +11,8 @@
 
 namespace ret {
 
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
 // V neighbouring channels of a token, as they lie in memory and as floats.
 template <typename T, int V> struct Lane;
 template <> struct Lane<bf16, 1> {
@@ -54,6 +56,29 @@ template <typename T, int V>
 __device__ __forceinline__ void lane_store(T* row, uint32_t at, const float* x) {
   *reinterpret_cast<lane_raw<T, V>*>(reinterpret_cast<char*>(row) + at * (uint32_t)sizeof(T)) = Lane<T, V>::put(x);
 }
+
+// Rows of a tile behind a scalar descriptor: a lane's offset stays, the row is a scalar
+// offset, so that a load or store costs no address arithmetic. All below 2^32 bytes.
+template <typename T, int V>
+struct Rows {
+  using Raw = lane_raw<T, V>;
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t at, step;  // bytes: the lane's, from a row to the next
+  // `row`: the lane's first row behind `base`, `c` its channel
+  __device__ __forceinline__ Rows(const T* base, uint32_t stride, uint32_t row, uint32_t c)
+      : rs(scalar_rsrc(base)), at((row * stride + c) * (uint32_t)sizeof(T)), step(stride * (uint32_t)sizeof(T)) {}
+  __device__ __forceinline__ Raw load(int j) const {
+    if constexpr (sizeof(Raw) == 2) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b16(rs, at, j * step, 0));
+    else if constexpr (sizeof(Raw) == 4) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(rs, at, j * step, 0));
+    else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b64(rs, at, j * step, 0));
+  }
+  __device__ __forceinline__ void store(int j, const float* x) const {
+    const Raw r = Lane<T, V>::put(x);
+    if constexpr (sizeof(Raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, r), rs, at, j * step, 0);
+    else if constexpr (sizeof(Raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r), rs, at, j * step, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), rs, at, j * step, 0);
+  }
+};
 
 // Whether a lane may take two bf16 channels of every tensor at once.
 template <typename P>

@@ -49,15 +49,18 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
     const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? row * p.gate_stride : 0);
     lane_raw<T, V> rx[L], rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
+    if constexpr (FULL) {
+      const Rows<T, V> xs(x, p.x_stride, seg * kSegment, c), gs(gate, p.gate_stride, seg * kSegment, c);
+      const Rows<D, V> ds(decay, p.decay_stride, seg * kSegment, c);
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      if constexpr (FULL) {
-        // a scalar row and a lane's offset of 32 bits (strides below 2^22)
-        rx[j] = lane_load<T, V>(x + j * p.x_stride, (uint32_t)seg * kSegment * (uint32_t)p.x_stride + c);
-        rd[j] = lane_load<D, V>(decay + j * p.decay_stride, (uint32_t)seg * kSegment * (uint32_t)p.decay_stride + c);
-        if constexpr (IGATE)
-          rg[j] = lane_load<T, V>(gate + j * p.gate_stride, (uint32_t)seg * kSegment * (uint32_t)p.gate_stride + c);
-      } else {
+      for (int j = 0; j < L; ++j) {
+        rx[j] = xs.load(j);
+        rd[j] = ds.load(j);
+        if constexpr (IGATE) rg[j] = gs.load(j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
         const int64_t t = min(seg * kSegment + j, left - 1);
         rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
         rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
@@ -174,7 +177,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
     for (int e = 0; e < V; ++e) kept[e] = h0[0][e];
   }
   if (!p.o) return;
-  T* o = reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width;
+  const Rows<T, V> o(reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width, p.width, seg * kSegment, c);
   auto run = [&](auto full, auto forget) {
     float h[V];
 #pragma unroll
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
         if (j % kSegment == 0) h[e] = h0[j / kSegment][e];
         h[e] = decltype(forget)::value ? step_or_forget(a[j][e], h[e], u[j][e]) : fmaf(a[j][e], h[e], u[j][e]);
       }
-      if (decltype(full)::value || j < n) lane_store<T, V>(o + j * p.width, (uint32_t)seg * kSegment * p.width + c, h);
+      if (decltype(full)::value || j < n) o.store(j, h);
     }
   };
   if (forgets)
