@@ -20,7 +20,7 @@ namespace ret {
 constexpr int kSegment = 8;  // tokens; 16 segments a tile
 
 template <typename T, bool GATES, bool IGATE, bool NORM, int V>
-__global__ __launch_bounds__(512, 4) void scan_bwd_kernel(ScanParams p) {
+__global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParams p) {
   using D = std::conditional_t<GATES, T, float>;
   constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = kScanBwdTile / kSegment;
   __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_p[SEGS][kScanChannels],
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(512, 4) void scan_bwd_kernel(ScanParams p) {
 
 template <typename T, bool GATES, bool IGATE, bool NORM, int V>
 static hipError_t launch_bwd(const ScanParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((scan_bwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(512), 0, stream, p);
+  hipLaunchKernelGGL((scan_bwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(kScanBwdTile * 4), 0, stream, p);
   return hipGetLastError();
 }
 template <typename T, int V>
