@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
   const int64_t row = (int64_t)tok0 + from;
   lane_raw<T, V> rx[L], ro[L];
   // sd, si: the sigmoids; rest: 1 - a^2; hist: inputs, then the state before each token
-  float a[L][V], sd[GATES ? L : 1][V], si[IGATE ? L : 1][V], rest[NORM ? L : 1][V], hist[L][V];
+  float a[L][V], sd[GATES ? L : 1][V], si[IGATE ? L : 1][V], rest[NORM && !GATES ? L : 1][V], hist[L][V];
   float A[PARTS][V], U[PARTS][V], R[PARTS][V], rate[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
           hist[j][e] *= si[j][e];
         }
         if constexpr (NORM) {
-          rest[j][e] = q;
+          if constexpr (!GATES) rest[j][e] = q;  // (formed again from s_d: 16 registers less)
           hist[j][e] *= __builtin_amdgcn_sqrtf(q);
         }
         if (!FULL && j >= n) {  // behind the end
@@ -265,8 +265,13 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
           float dla = none ? 0.f : ag * hist[j][e], m = 1.f;
           if constexpr (NORM) {
             // a^2 / m; 0 where the decay is 0, the limit towards which ddecay goes
-            const float inv = rest[j][e] > 0.f ? __builtin_amdgcn_rsqf(rest[j][e]) : 0.f;
-            m = rest[j][e] * inv;
+            float q;
+            if constexpr (GATES)
+              q = left_of<T>(-rate[e] * sd[j][e], av);
+            else
+              q = rest[j][e];
+            const float inv = q > 0.f ? __builtin_amdgcn_rsqf(q) : 0.f;
+            m = q * inv;
             dla = fmaf(-ag * av * inv, s * xs[e], dla);
           }
           o1[e] = g[e] * m * s;

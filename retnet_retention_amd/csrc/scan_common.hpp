@@ -140,10 +140,11 @@ __device__ __forceinline__ float sigmoid_of(float x, bf16) {
 // - 1), fp32 ones to 1/4, seven (2e-9); beyond it a - 1 is large enough for what a's
 // own rounding leaves of it.
 template <typename T>
-__device__ __forceinline__ void factor(float la, float& a, float& left) {
-  constexpr bool wide = sizeof(T) == 4;
+constexpr float kNear = sizeof(T) == 4 ? 0.25f : 0.03125f;
+template <typename T>
+__device__ __forceinline__ float near_minus_1(float la) {  // exp(la) - 1
   float p;
-  if constexpr (wide) {
+  if constexpr (sizeof(T) == 4) {
     p = 1.f / 5040;
     p = fmaf(p, la, 1.f / 720);
     p = fmaf(p, la, 1.f / 120);
@@ -153,11 +154,21 @@ __device__ __forceinline__ void factor(float la, float& a, float& left) {
   }
   p = fmaf(p, la, 1.f / 6);
   p = fmaf(p, la, 0.5f);
-  p = fmaf(p, la, 1.f) * la;
-  const float e = wide ? expf(la) : __builtin_amdgcn_exp2f(1.4426950408889634f * la);
-  const bool near = fabsf(la) < (wide ? 0.25f : 0.03125f);
+  return fmaf(p, la, 1.f) * la;
+}
+template <typename T>
+__device__ __forceinline__ void factor(float la, float& a, float& left) {
+  const float p = near_minus_1<T>(la);
+  const float e = sizeof(T) == 4 ? expf(la) : __builtin_amdgcn_exp2f(1.4426950408889634f * la);
+  const bool near = fabsf(la) < kNear<T>;
   a = near ? 1.f + p : e;
   left = near ? -p * (2.f + p) : fmaf(-e, e, 1.f);
+}
+// 1 - a^2 once more, of a token whose factor is known
+template <typename T>
+__device__ __forceinline__ float left_of(float la, float a) {
+  const float p = near_minus_1<T>(la);
+  return fabsf(la) < kNear<T> ? -p * (2.f + p) : fmaf(-a, a, 1.f);
 }
 
 // A workgroup's tile and channels. Where tiles hand a state on, a workgroup takes
