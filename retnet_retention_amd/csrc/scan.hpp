@@ -17,7 +17,7 @@ inline int64_t tile_count(int batch, int seqlen, bool packed, int64_t total, int
 
 // The recurrence: tokens of a tile of the forward and of the backward. The states
 // that the forward keeps stand before each of the backward's tiles.
-constexpr int kScanTile = 256, kScanBwdTile = 64;
+constexpr int kScanTile = 256, kScanBwdTile = 128;
 // Channels of a workgroup.
 constexpr int kScanChannels = 64;
 

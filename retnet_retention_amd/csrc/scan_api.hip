@@ -53,8 +53,8 @@ ret_status_t check_scan(const ret_scan_desc_t* d, bool packed, int64_t total) {
   const int64_t strides[] = {d->x_stride, d->decay_stride, d->gate_stride};
   for (const int64_t s : strides) {
     if (!stride_ok(s, d->width)) return RET_ERR_SHAPE;
-    // whole tiles are addressed with 32 bits from their first row
-    if (s >= kMaxTileStride && (packed || d->seqlen >= kSmallestTile)) return RET_ERR_SHAPE;
+    // a tile is addressed with 32 bits from its first row
+    if (s >= kMaxTileStride && (packed || d->seqlen > 1)) return RET_ERR_SHAPE;
   }
   return RET_OK;
 }

@@ -57,6 +57,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
     if (at.b == p.batch - 1) clear(tok0 + len, p.total);
   }
   const int left = len - from, n = left - seg * kSegment;  // tokens from the tile's, the lane's start on
+  const int there = min(left, kScanBwdTile);
   const int64_t row = (int64_t)tok0 + from;
   lane_raw<T, V> rx[L], ro[L];
   // sd, si: the sigmoids; rest: 1 - a^2; hist: inputs, then the state before each token
@@ -80,26 +81,16 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
     const T* dout = reinterpret_cast<const T*>(p.dout) + row * p.width;
     lane_raw<T, V> rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
-    if constexpr (FULL) {
-      const Rows<T, V> xs(x, p.x_stride, seg * kSegment, c), gs(gate, p.gate_stride, seg * kSegment, c);
-      const Rows<T, V> os(dout, p.width, seg * kSegment, c);
-      const Rows<D, V> ds(decay, p.decay_stride, seg * kSegment, c);
+    const Rows<T, V> xs(x, p.x_stride, there, p.width, seg * kSegment, c);
+    const Rows<D, V> ds(decay, p.decay_stride, there, p.width, seg * kSegment, c);
+    const Rows<T, V> gs(gate, p.gate_stride, there, p.width, seg * kSegment, c);
+    const Rows<T, V> os(dout, p.width, there, p.width, seg * kSegment, c);
 #pragma unroll
-      for (int j = 0; j < L; ++j) {
-        rx[j] = xs.load(j);
-        rd[j] = ds.load(j);
-        if constexpr (IGATE) rg[j] = gs.load(j);
-        ro[j] = os.load(j);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const int64_t t = min(seg * kSegment + j, left - 1);
-        rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
-        rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
-        if constexpr (IGATE) rg[j] = lane_load<T, V>(gate + t * p.gate_stride, c);
-        ro[j] = lane_load<T, V>(dout + t * p.width, c);
-      }
+    for (int j = 0; j < L; ++j) {
+      rx[j] = FULL ? xs.load(j) : xs.load_if(j);
+      rd[j] = FULL ? ds.load(j) : ds.load_if(j);
+      if constexpr (IGATE) rg[j] = FULL ? gs.load(j) : gs.load_if(j);
+      ro[j] = FULL ? os.load(j) : os.load_if(j);
     }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
@@ -144,7 +135,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
   const bool full = left >= kScanBwdTile;
   if (full)
     fold(std::true_type());
-  else if (len > 0)
+  else if (wave * 2 * kSegment < left)
     fold(std::false_type());
   // a factor of 0 among the tokens (or a product that is): they may have to forget what is no number
   bool forgets = false;
@@ -241,9 +232,9 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
         h[e] = FORGET ? step_or_forget(a[j][e], h[e], u) : fmaf(a[j][e], h[e], u);
       }
     }
-    const Rows<T, V> to_x(dx + row * p.width, p.width, seg * kSegment, c);
-    const Rows<D, V> to_decay(ddecay + row * p.width, p.width, seg * kSegment, c);
-    const Rows<T, V> to_gate(dgate + (IGATE ? row * p.width : 0), p.width, seg * kSegment, c);
+    const Rows<T, V> to_x(dx + row * p.width, p.width, there, p.width, seg * kSegment, c);
+    const Rows<D, V> to_decay(ddecay + row * p.width, p.width, there, p.width, seg * kSegment, c);
+    const Rows<T, V> to_gate(dgate + (IGATE ? row * p.width : 0), p.width, there, p.width, seg * kSegment, c);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
       float xs[V], d[V], o1[V], o2[V], o3[V];
@@ -292,7 +283,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
       }
     }
   };
-  if (len > 0) {
+  if (wave * 2 * kSegment < left) {
     if (forgets)
       run(std::false_type(), std::true_type());
     else if (full)

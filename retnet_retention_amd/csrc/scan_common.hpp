@@ -57,26 +57,39 @@ __device__ __forceinline__ void lane_store(T* row, uint32_t at, const float* x) 
   *reinterpret_cast<lane_raw<T, V>*>(reinterpret_cast<char*>(row) + at * (uint32_t)sizeof(T)) = Lane<T, V>::put(x);
 }
 
-// Rows of a tile behind a scalar descriptor: a lane's offset stays, the row is a scalar
-// offset, so that a load or store costs no address arithmetic. All below 2^32 bytes.
+// Rows of a tile behind a scalar descriptor of `rows` rows: a lane's offset stays, the
+// row is a scalar offset, so that an access costs no address arithmetic. All below 2^32
+// bytes (strides below 2^22 where a sequence has more than one token).
 template <typename T, int V>
 struct Rows {
   using Raw = lane_raw<T, V>;
   __amdgpu_buffer_rsrc_t rs;
   uint32_t at, step;  // bytes: the lane's, from a row to the next
   // `row`: the lane's first row behind `base`, `c` its channel
-  __device__ __forceinline__ Rows(const T* base, uint32_t stride, uint32_t row, uint32_t c)
-      : rs(scalar_rsrc(base)), at((row * stride + c) * (uint32_t)sizeof(T)), step(stride * (uint32_t)sizeof(T)) {}
-  __device__ __forceinline__ Raw load(int j) const {
-    if constexpr (sizeof(Raw) == 2) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b16(rs, at, j * step, 0));
-    else if constexpr (sizeof(Raw) == 4) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(rs, at, j * step, 0));
-    else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b64(rs, at, j * step, 0));
-  }
+  __device__ __forceinline__ Rows(const T* base, int64_t stride, int rows, int width, int row, int c)
+      : rs(scalar_rsrc(base, (uint32_t)((rows - 1) * stride + width) * (uint32_t)sizeof(T))),
+        at((uint32_t)(row * (uint32_t)stride + c) * (uint32_t)sizeof(T)), step((uint32_t)stride * (uint32_t)sizeof(T)) {}
+  // a row that is there; one that may be behind the end (then zeros)
+  __device__ __forceinline__ Raw load(int j) const { return get(at, j * step); }
+  __device__ __forceinline__ Raw load_if(int j) const { return get(at + j * step, 0); }
   __device__ __forceinline__ void store(int j, const float* x) const {
     const Raw r = Lane<T, V>::put(x);
-    if constexpr (sizeof(Raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, r), rs, at, j * step, 0);
-    else if constexpr (sizeof(Raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r), rs, at, j * step, 0);
-    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), rs, at, j * step, 0);
+    if constexpr (sizeof(Raw) == 2)
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, r), rs, at, j * step, 0);
+    else if constexpr (sizeof(Raw) == 4)
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r), rs, at, j * step, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), rs, at, j * step, 0);
+  }
+
+ private:
+  __device__ __forceinline__ Raw get(uint32_t lane, uint32_t scalar) const {
+    if constexpr (sizeof(Raw) == 2)
+      return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b16(rs, lane, scalar, 0));
+    else if constexpr (sizeof(Raw) == 4)
+      return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b32(rs, lane, scalar, 0));
+    else
+      return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b64(rs, lane, scalar, 0));
   }
 };
 

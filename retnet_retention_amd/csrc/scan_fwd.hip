@@ -49,23 +49,15 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
     const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? row * p.gate_stride : 0);
     lane_raw<T, V> rx[L], rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
-    if constexpr (FULL) {
-      const Rows<T, V> xs(x, p.x_stride, seg * kSegment, c), gs(gate, p.gate_stride, seg * kSegment, c);
-      const Rows<D, V> ds(decay, p.decay_stride, seg * kSegment, c);
+    const int there = min(left, kScanTile);
+    const Rows<T, V> xs(x, p.x_stride, there, p.width, seg * kSegment, c);
+    const Rows<D, V> ds(decay, p.decay_stride, there, p.width, seg * kSegment, c);
+    const Rows<T, V> gs(gate, p.gate_stride, there, p.width, seg * kSegment, c);
 #pragma unroll
-      for (int j = 0; j < L; ++j) {
-        rx[j] = xs.load(j);
-        rd[j] = ds.load(j);
-        if constexpr (IGATE) rg[j] = gs.load(j);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const int64_t t = min(seg * kSegment + j, left - 1);
-        rx[j] = lane_load<T, V>(x + t * p.x_stride, c);
-        rd[j] = lane_load<D, V>(decay + t * p.decay_stride, c);
-        if constexpr (IGATE) rg[j] = lane_load<T, V>(gate + t * p.gate_stride, c);
-      }
+    for (int j = 0; j < L; ++j) {
+      rx[j] = FULL ? xs.load(j) : xs.load_if(j);
+      rd[j] = FULL ? ds.load(j) : ds.load_if(j);
+      if constexpr (IGATE) rg[j] = FULL ? gs.load(j) : gs.load_if(j);
     }
     float rate[V];
 #pragma unroll
@@ -105,7 +97,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
   const bool full = left >= kScanTile;
   if (full)
     fold(std::true_type());
-  else if (len > 0)
+  else if (wave * 2 * kSegment < left)
     fold(std::false_type());
   // a factor of 0 among the tokens (or a product that is): they may have to forget what is no number
   bool forgets = false;
@@ -164,20 +156,21 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
     }
   }
   __syncthreads();
-  if (!inside || len == 0) return;
+  if (!inside || n <= 0) return;
   float h0[PARTS][V];
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
     for (int e = 0; e < V; ++e)
       h0[k][e] = step_or_forget(s_a[seg + k][cl + e], s_h[cl + e], s_u[seg + k][cl + e]);
-  if (p.kept && seg * kSegment % kScanBwdTile == 0 && n > 0) {
+  if (p.kept && seg * kSegment % kScanBwdTile == 0) {
     float* kept = p.kept + (kept_row(p, at.b, tok0) + (from + seg * kSegment) / kScanBwdTile) * p.width + c;
 #pragma unroll
     for (int e = 0; e < V; ++e) kept[e] = h0[0][e];
   }
   if (!p.o) return;
-  const Rows<T, V> o(reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width, p.width, seg * kSegment, c);
+  const Rows<T, V> o(reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width, p.width, min(left, kScanTile),
+                     p.width, seg * kSegment, c);
   auto run = [&](auto full, auto forget) {
     float h[V];
 #pragma unroll
