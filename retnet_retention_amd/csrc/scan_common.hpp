@@ -60,6 +60,7 @@ __device__ __forceinline__ void lane_store(T* row, uint32_t at, const float* x) 
 // Rows of a tile behind a scalar descriptor of `rows` rows: a lane's offset stays, the
 // row is a scalar offset, so that an access costs no address arithmetic. All below 2^32
 // bytes (strides below 2^22 where a sequence has more than one token).
+constexpr int kStreamed = 2;  // store policy: not kept in the caches
 template <typename T, int V>
 struct Rows {
   using Raw = lane_raw<T, V>;
@@ -72,14 +73,15 @@ struct Rows {
   // a row that is there; one that may be behind the end (then zeros)
   __device__ __forceinline__ Raw load(int j) const { return get(at, j * step); }
   __device__ __forceinline__ Raw load_if(int j) const { return get(at + j * step, 0); }
+  template <int POLICY = 0>
   __device__ __forceinline__ void store(int j, const float* x) const {
     const Raw r = Lane<T, V>::put(x);
     if constexpr (sizeof(Raw) == 2)
-      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, r), rs, at, j * step, 0);
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, r), rs, at, j * step, POLICY);
     else if constexpr (sizeof(Raw) == 4)
-      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r), rs, at, j * step, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r), rs, at, j * step, POLICY);
     else
-      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), rs, at, j * step, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), rs, at, j * step, POLICY);
   }
 
  private:
