@@ -936,33 +936,44 @@ def _token_rows(rows, dense, cu_seqlens):
     """Checks of tensors [batch, seqlen, width], or packed [total_tokens,
     width]: `rows` may have a token stride, `dense` may not. Returns (batch,
     seqlen, total_tokens, width, strides of `rows` (0 for None))."""
-    name, x = rows[0][:2]
+    name, x, _ = rows[0]
     dev, shape = x.get_device(), x.shape
     if dev < 0:
         raise ValueError(f"{name} must be a GPU tensor")
     packed = cu_seqlens is not None
     if len(shape) != (2 if packed else 3):
         raise ValueError(f"{name} must be " + ("[total_tokens, width]" if packed else "[batch, seqlen, width]"))
-    for n, t, dtype in rows + dense:
-        if t is not None and (t.get_device() != dev or t.dtype != dtype or t.shape != shape):
+    width, strides = shape[-1], []
+    for n, t, dtype in rows:
+        if t is None:
+            strides.append(0)
+            continue
+        if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{n} must be a {dtype} tensor {list(shape)} on {x.device}")
-    for n, t, _ in dense:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    strides = [0 if t is None else _token_stride(n, t) for n, t, _ in rows]
+        strides.append(width if t.is_contiguous() else _token_stride(n, t))
+    for n, t, dtype in dense:
+        if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous {dtype} tensor {list(shape)} on {x.device}")
     if not packed:
-        return shape[0], shape[1], 0, shape[2], strides
+        return shape[0], shape[1], 0, width, strides
     if (cu_seqlens.get_device() != dev or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1
             or not cu_seqlens.is_contiguous()):
         raise ValueError("cu_seqlens must be a contiguous GPU int32 tensor [batch + 1]")
-    return cu_seqlens.numel() - 1, 1, shape[0], shape[1], strides
+    return cu_seqlens.numel() - 1, 1, shape[0], width, strides
+
+
+def _dense_like(t):
+    """A new dense tensor of t's shape and type (t may be columns of a wider one)."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _held(like, *tensors):
     """Checks of (name, tensor or None, shape, dtype), contiguous on `like`'s device."""
+    dev = like.get_device()
     for name, t, shape, dtype in tensors:
-        if t is not None and (t.get_device() != like.get_device() or t.dtype != dtype or not t.is_contiguous()
-                              or t.shape != shape):
+        if t is not None and (t.get_device() != dev or t.dtype != dtype or not t.is_contiguous() or t.shape != shape):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {like.device}")
 
 
@@ -1011,7 +1022,7 @@ def gated_scan_fwd(x, decay, gate=None, *, rate=None, normalize=False, state_in=
     (GPU int32 [batch + 1]); rows outside every sequence are left as they were.
     A factor of 0 (log decay -infinity) forgets whatever the state holds. check:
     as delta_chunkwise_fwd."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    out = _dense_like(x) if out is None else out
     desc, batch, total, width = _scan_call(x, decay, gate, rate, normalize, cu_seqlens, ("out", out, x.dtype))
     state = (batch, width)
     _held(x, ("state_in", state_in, state, torch.float32), ("state_out", state_out, state, torch.float32))
@@ -1046,7 +1057,7 @@ def gated_scan_bwd(x, decay, dout, gate=None, *, rate=None, normalize=False, sta
     packed = int(cu_seqlens is not None)
     if kept is not None:
         _held(x, ("kept", kept, (L.retention_scan_kept_bytes(desc, packed, total) // 4,), torch.float32))
-    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    new = lambda t: None if t is None else _dense_like(t)  # noqa: E731
     dx, ddecay, dgate, drate, dstate = new(x), new(decay), new(gate), new(rate), new(state_in)
     need = L.retention_scan_bwd_workspace_bytes(desc, packed, total, int(kept is not None))
     workspace, ws_bytes, _ = _workspace(workspace, need, x)
@@ -1066,7 +1077,7 @@ def gated_scan_step(x, decay, state, gate=None, *, rate=None, normalize=False, s
     updates `state` in place and returns the output. state: fp32 [batch,
     width], or with `slots` (GPU int32 [batch]) a pool [num_slots, width], as in
     delta_recurrent_step."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    out = _dense_like(x) if out is None else out
     desc, batch, _, width = _scan_call(x, decay, gate, rate, normalize, None, ("out", out, x.dtype))
     if x.shape[1] != 1:
         raise ValueError("gated_scan_step takes one token per sequence (seqlen 1)")
@@ -1100,7 +1111,7 @@ def short_conv_fwd(x, weight, bias=None, *, swish=False, state_in=None, state_ou
     token, [batch, taps - 1, width] in x's dtype, oldest first (state_out may be
     state_in itself). x may be columns of a wider projection. Packed sequences
     and check as in gated_scan_fwd."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    out = _dense_like(x) if out is None else out
     desc, batch, total, held = _conv_call(x, weight, bias, swish, cu_seqlens, ("out", out, x.dtype))
     state = (batch,) + held
     _held(x, ("state_in", state_in, state, x.dtype), ("state_out", state_out, state, x.dtype))
@@ -1126,7 +1137,7 @@ def short_conv_bwd(x, weight, dout, bias=None, *, swish=False, state_in=None, d_
     desc, batch, total, held = _conv_call(x, weight, bias, swish, cu_seqlens, ("dout", dout, x.dtype))
     state = (batch,) + held
     _held(x, ("state_in", state_in, state, x.dtype), ("d_state_out", d_state_out, state, x.dtype))
-    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    new = lambda t: None if t is None else _dense_like(t)  # noqa: E731
     dx, dweight, dbias, dstate = new(x), new(weight), new(bias), new(state_in)
     L = lib()
     need = L.retention_conv_bwd_workspace_bytes(desc, int(cu_seqlens is not None), total)
@@ -1145,7 +1156,7 @@ def short_conv_step(x, weight, state, bias=None, *, swish=False, slots=None, out
     the inputs in `state` on by one and returns the output. state: [batch,
     taps - 1, width] in x's dtype, or with `slots` (GPU int32 [batch]) a pool of
     such, as in delta_recurrent_step."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    out = _dense_like(x) if out is None else out
     desc, batch, _, held = _conv_call(x, weight, bias, swish, None, ("out", out, x.dtype))
     if x.shape[1] != 1:
         raise ValueError("short_conv_step takes one token per sequence (seqlen 1)")
