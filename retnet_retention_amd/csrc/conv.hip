@@ -88,19 +88,24 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p) {
   }
 }
 
+// A wave walks `p.rows` tokens, kConvStep at a time, the next ones on their way from
+// memory; what it carries are the last K - 1 inputs and dz. It looks K - 1 tokens past
+// its own for the dx of its last ones.
+constexpr int kConvStep = 8;
+
 template <typename T, int K, int V>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
-  constexpr int L = kConvRows;
+__global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
+  constexpr int S = kConvStep, H = K - 1;
   __shared__ float s_sum[4][K + 1][64 * V];
   const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
   const int groups = (p.width + 64 * V - 1) / (64 * V);
   const int64_t block = blockIdx.x / groups;
   int b, i, tok0, len;
-  tile_of(p, block, kConvTile, b, i);
+  tile_of(p, block, 4 * p.rows, b, i);
   span_of(p, b, tok0, len);
   const int at = (blockIdx.x % groups * 64 + lane) * V, c = min(at, p.width - V);
   const bool inside = at < p.width;
-  const int t0 = i * kConvTile + wave * L;
+  const int t0 = (4 * i + wave) * p.rows;
   const bool begins = i == 0 && wave == 0;
   T* dx = reinterpret_cast<T*>(p.dx);
   // rows before the first sequence and behind the last have gradient 0
@@ -111,11 +116,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
   if (p.cu && i == 0 && b == 0) clear(0, tok0);
   if (p.cu && i == 0 && b == p.batch - 1) clear(tok0 + len, p.total);
   dx += (int64_t)tok0 * p.width;
-  const int64_t held = (int64_t)b * (K - 1) * p.width;
+  const int64_t held = (int64_t)b * H * p.width;
   const T* after = p.d_state_out ? reinterpret_cast<const T*>(p.d_state_out) + held : nullptr;
   // what the state behind the last token adds to index s
   auto add_after = [&](int s, float* d) {
-    const int j = s + K - 1 - len;
+    const int j = s + H - len;
     if (after && j >= 0) {
       float y[V];
       Lane<T, V>::get(lane_load<T, V>(after + (int64_t)j * p.width, c), y);
@@ -125,7 +130,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
   };
   auto put_state = [&](int s, float* d) {
     add_after(s, d);
-    if (inside) lane_store<T, V>(reinterpret_cast<T*>(p.d_state_in) + held + (int64_t)(K - 1 + s) * p.width, c, d);
+    if (inside) lane_store<T, V>(reinterpret_cast<T*>(p.d_state_in) + held + (int64_t)(H + s) * p.width, c, d);
   };
   float w[V][K], bias[V], sum[K + 1][V];
 #pragma unroll
@@ -139,58 +144,86 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
   if (t0 < len) {
     const ConvLine<T, K, V> line(p, b, tok0, len, c);
     const T* dout = reinterpret_cast<const T*>(p.dout) + (int64_t)tok0 * p.width;
-    lane_raw<T, V> rx[L + 2 * (K - 1)], rd[L + K - 1];
+    const int end = min(t0 + p.rows + H, len);  // tokens that are looked at
+    lane_raw<T, V> nx[S], nd[S];
+    auto ask = [&](int t) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) rx[j] = line.at(t0 - (K - 1) + j);
+      for (int j = 0; j < S; ++j) {
+        const int64_t u = min(t + j, len - 1);
+        nx[j] = lane_load<T, V>(line.x + u * p.x_stride, c);
+        nd[j] = lane_load<T, V>(dout + u * p.width, c);
+      }
+    };
+    ask(t0);
+    float x[S + H][V], dz[S + H][V];  // the first H: of the tokens before
 #pragma unroll
-    for (int j = 0; j < L + K - 1; ++j) {
-      rx[j + K - 1] = line.token(t0 + j);
-      rd[j] = lane_load<T, V>(dout + (int64_t)min(t0 + j, len - 1) * p.width, c);
+    for (int j = 0; j < H; ++j) {
+      Lane<T, V>::get(line.at(t0 - H + j), x[j]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) dz[j][e] = 0.f;
     }
-    float x[K][V], dz[K][V] = {};
+    for (int t = t0; t < t0 + p.rows + H && t - H < len; t += S) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) Lane<T, V>::get(rx[j], x[j]);
-#pragma unroll
-    for (int j = 0; j < L + K - 1; ++j) {  // token t0 + j
-      Lane<T, V>::get(rx[j + K - 1], x[(j + K - 1) % K]);
-      float d[V], out[V];
-      Lane<T, V>::get(rd[j], d);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (p.swish) {
-          float z = bias[e];
-#pragma unroll
-          for (int k = 0; k < K; ++k) z = fmaf(w[e][k], x[(j + k) % K][e], z);
-          const float s = sigmoid_of(z, T());
-          d[e] *= s * fmaf(z, 1.f - s, 1.f);
-        }
-        if (t0 + j >= len) d[e] = 0.f;
-        dz[j % K][e] = d[e];
-        if (j < L) {
-#pragma unroll
-          for (int k = 0; k < K; ++k) sum[k][e] = fmaf(d[e], t0 + j < len ? x[(j + k) % K][e] : 0.f, sum[k][e]);
-          sum[K][e] += d[e];
-        }
-        out[e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (j - k >= 0) out[e] = fmaf(w[e][k], dz[(j - k + K) % K][e], out[e]);
+      for (int j = 0; j < S; ++j) {
+        Lane<T, V>::get(nx[j], x[H + j]);
+        Lane<T, V>::get(nd[j], dz[H + j]);
       }
-      const int s = t0 + j - (K - 1);
-      if (j >= K - 1) {
-        if (s < len) {
-          add_after(s, out);
-          if (inside) lane_store<T, V>(dx + (int64_t)s * p.width, c, out);
+      if (t + S < end) ask(t + S);
+      auto step = [&](auto whole) {
+        // whole: every token is one of the wave's own, and none of the last H of the sequence
+        constexpr bool FULL = decltype(whole)::value;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          const bool there = FULL || t + j < end, own = FULL || (there && t + j < t0 + p.rows);
+          float out[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            float& d = dz[H + j][e];
+            if (p.swish) {
+              float z = bias[e];
+#pragma unroll
+              for (int k = 0; k < K; ++k) z = fmaf(w[e][k], x[j + k][e], z);
+              const float s = sigmoid_of(z, T());
+              d *= s * fmaf(z, 1.f - s, 1.f);
+            }
+            if (!there) d = 0.f;
+            if (own) {
+#pragma unroll
+              for (int k = 0; k < K; ++k) sum[k][e] = fmaf(d, x[j + k][e], sum[k][e]);
+              sum[K][e] += d;
+            }
+            out[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) out[e] = fmaf(w[e][k], dz[H + j - k][e], out[e]);
+          }
+          const int s = t + j - H;
+          if (FULL || s >= t0) {
+            if (FULL || (s < len && s < t0 + p.rows)) {
+              if (!FULL) add_after(s, out);
+              if (inside) lane_store<T, V>(dx + (int64_t)s * p.width, c, out);
+            }
+          } else if (begins && p.d_state_in) {
+            put_state(s, out);
+          }
         }
-      } else if (begins && p.d_state_in) {
-        put_state(s, out);
-      }
+      };
+      if (t > t0 && t + S <= min(t0 + p.rows, len))
+        step(std::true_type());
+      else
+        step(std::false_type());
+#pragma unroll
+      for (int j = 0; j < H; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          x[j][e] = x[S + j][e];
+          dz[j][e] = dz[S + j][e];
+        }
     }
   } else if (begins && len == 0 && p.d_state_in) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
+    for (int j = 0; j < H; ++j) {
       float d[V] = {};
-      put_state(j - (K - 1), d);
+      put_state(j - H, d);
     }
   }
 #pragma unroll
@@ -231,8 +264,17 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* partial, in
   }
 }
 
-int64_t conv_bwd_blocks(int batch, int seqlen, bool packed, int64_t total) {
-  return tile_count(batch, seqlen, packed, total, kConvTile);
+// Tokens of a wave in the backward: many, as each looks K - 1 past its own on both
+// sides and leaves a row of sums, but at least 4096 waves of 128 channels.
+int conv_bwd_rows(int64_t tokens, int width) {
+  const int64_t groups = (width + 127) / 128;
+  int rows = 128;
+  while (rows > 16 && tokens / rows * groups < 4096) rows /= 2;
+  return rows;
+}
+int64_t conv_bwd_blocks(int batch, int seqlen, int width, bool packed, int64_t total) {
+  const int64_t tokens = packed ? total : (int64_t)batch * seqlen;
+  return tile_count(batch, seqlen, packed, total, 4 * conv_bwd_rows(tokens, width));
 }
 
 // Pairs of bf16 channels where they are aligned in every row.
@@ -252,8 +294,9 @@ static hipError_t launch_conv_fwd_k(const ConvParams& p, hipStream_t stream) {
   });
 }
 template <typename T, int K>
-static hipError_t launch_conv_bwd_k(const ConvParams& p, hipStream_t stream) {
-  const int64_t tiles = conv_bwd_blocks(p.batch, p.seqlen, p.cu, p.total);
+static hipError_t launch_conv_bwd_k(ConvParams p, hipStream_t stream) {
+  const int64_t tiles = conv_bwd_blocks(p.batch, p.seqlen, p.width, p.cu, p.total);
+  p.rows = conv_bwd_rows(p.total, p.width);
   const hipError_t e = with_lanes<T, K>(p, [&](auto v) {
     constexpr int V = decltype(v)::value;
     const int64_t n = tiles * ((p.width + 64 * V - 1) / (64 * V));

@@ -75,6 +75,7 @@ struct ConvParams {
   const float *weight, *bias;  // [width][taps], [width] or null
   const int* cu;
   int batch, seqlen, width, total, swish;
+  int rows;  // backward: tokens of a wave
   int64_t x_stride;
   void* o;
   const void* state_in;  // [batch][taps - 1][width], oldest first
@@ -86,7 +87,7 @@ struct ConvParams {
   float *dweight, *dbias;
   float* partial;  // [blocks][taps + 1][width] sums of dweight and dbias
 };
-int64_t conv_bwd_blocks(int batch, int seqlen, bool packed, int64_t total);
+int64_t conv_bwd_blocks(int batch, int seqlen, int width, bool packed, int64_t total);
 hipError_t launch_conv_fwd(const ConvParams& p, int taps, int dtype, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvParams& p, int taps, int dtype, hipStream_t stream);
 

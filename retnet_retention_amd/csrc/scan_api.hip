@@ -144,7 +144,7 @@ ConvSizes sizes_of(const ret_conv_desc_t* d, bool packed, int64_t total) {
   s.state = (size_t)d->batch * (d->taps - 1) * d->width * e;
   s.bias = (size_t)d->width * sizeof(float);
   s.weight = s.bias * d->taps;
-  s.partial = (size_t)ret::conv_bwd_blocks(d->batch, d->seqlen, packed, total) * (s.weight + s.bias);
+  s.partial = (size_t)ret::conv_bwd_blocks(d->batch, d->seqlen, d->width, packed, total) * (s.weight + s.bias);
   return s;
 }
 void carve_conv(Carve& c, ret::ConvParams& p, const ConvSizes& s, bool grad) {
