@@ -445,8 +445,7 @@ ret_status_t retention_residual_norm_bwd(const ret_norm_desc_t *desc, float skip
  * has to be >= 1. With cu_seqlens NULL total_tokens is ignored.
  *
  * Limits: width <= 65536, at most 2^31 - 2^16 tokens, tokens * width small enough for
- * a launch (2^34 always is); strides of the recurrence below 2^22, of single tokens
- * and of the convolution below 2^31.
+ * a launch (2^34 always is); strides below 2^22, of single tokens below 2^31.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t batch;        /* >= 1: sequences                                         */

@@ -146,12 +146,24 @@ __global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
     const T* dout = reinterpret_cast<const T*>(p.dout) + (int64_t)tok0 * p.width;
     const int end = min(t0 + p.rows + H, len);  // tokens that are looked at
     lane_raw<T, V> nx[S], nd[S];
+    const int rows = min(p.rows + H, len - t0);
+    const Rows<T, V> xs(line.x + t0 * p.x_stride, p.x_stride, rows, p.width, 0, c);
+    const Rows<T, V> ds(dout + (int64_t)t0 * p.width, p.width, rows, p.width, 0, c);
+    const Rows<T, V> to(dx + (int64_t)t0 * p.width, p.width, rows, p.width, 0, c);
     auto ask = [&](int t) {
+      const int from = t - t0;
+      if (from + S <= rows) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        const int64_t u = min(t + j, len - 1);
-        nx[j] = lane_load<T, V>(line.x + u * p.x_stride, c);
-        nd[j] = lane_load<T, V>(dout + u * p.width, c);
+        for (int j = 0; j < S; ++j) {
+          nx[j] = xs.load(from + j);
+          nd[j] = ds.load(from + j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          nx[j] = xs.load_if(from + j);
+          nd[j] = ds.load_if(from + j);
+        }
       }
     };
     ask(t0);
@@ -192,15 +204,15 @@ __global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
               for (int k = 0; k < K; ++k) sum[k][e] = fmaf(d, x[j + k][e], sum[k][e]);
               sum[K][e] += d;
             }
-            out[e] = 0.f;
+            out[e] = w[e][0] * d;
 #pragma unroll
-            for (int k = 0; k < K; ++k) out[e] = fmaf(w[e][k], dz[H + j - k][e], out[e]);
+            for (int k = 1; k < K; ++k) out[e] = fmaf(w[e][k], dz[H + j - k][e], out[e]);
           }
           const int s = t + j - H;
           if (FULL || s >= t0) {
             if (FULL || (s < len && s < t0 + p.rows)) {
               if (!FULL) add_after(s, out);
-              if (inside) lane_store<T, V>(dx + (int64_t)s * p.width, c, out);
+              if (inside) to.template store<kStreamed>(s - t0, out);
             }
           } else if (begins && p.d_state_in) {
             put_state(s, out);

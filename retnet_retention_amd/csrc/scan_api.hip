@@ -128,6 +128,7 @@ ret_status_t check_conv(const ret_conv_desc_t* d, bool packed, int64_t total) {
   const ret_status_t st = check_shape(d->batch, d->seqlen, d->width, d->dtype, packed, total, 1024);
   if (st != RET_OK) return st;
   if (!stride_ok(d->x_stride, d->width)) return RET_ERR_SHAPE;
+  if (d->x_stride >= kMaxTileStride && (packed || d->seqlen > 1)) return RET_ERR_SHAPE;  // as check_scan
   if (d->taps < ret::kMinTaps || d->taps > ret::kMaxTaps) return RET_ERR_UNSUPPORTED;
   return RET_OK;
 }
