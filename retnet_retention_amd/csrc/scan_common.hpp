@@ -142,7 +142,21 @@ __device__ __forceinline__ void tile_of(const P& p, int64_t j, int tile, int& b,
   if (i < 0 || i > p.total / tile) i = p.total / tile + 1;
 }
 
-__device__ __forceinline__ float sigmoid_of(float x, float) { return 1.f / (1.f + expf(-x)); }
+// exp(x) from the hardware's exp2 (about 1 ulp) with what the product x log2 e loses of
+// the exponent put back: 2^t (1 + r ln 2), t + r = x log2 e. Below -120 it is 0, above
+// 88.72 infinity; NaN stays.
+__device__ __forceinline__ float exp_f32(float x) {
+  constexpr float hi = 1.442695041f, lo = 1.925963e-8f;  // log2 e in two parts
+  const float y = x < -120.f ? -120.f : x;
+  const float t = y * hi, r = fmaf(y, lo, fmaf(y, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return x > 88.72f ? __builtin_inff() : fmaf(e * 0.6931471806f, r, e);
+}
+// 1 / (1 + exp(-x)): the hardware's reciprocal with one step of Newton's
+__device__ __forceinline__ float sigmoid_of(float x, float) {
+  const float d = 1.f + exp_f32(-x), y = __builtin_amdgcn_rcpf(d);
+  return x < -88.f ? 0.f : fmaf(fmaf(-d, y, 1.f), y, y);
+}
 // bf16 tensors: the hardware's exp2 and reciprocal, about 1 ulp each
 __device__ __forceinline__ float sigmoid_of(float x, bf16) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
@@ -174,7 +188,7 @@ __device__ __forceinline__ float near_minus_1(float la) {  // exp(la) - 1
 template <typename T>
 __device__ __forceinline__ void factor(float la, float& a, float& left) {
   const float p = near_minus_1<T>(la);
-  const float e = sizeof(T) == 4 ? expf(la) : __builtin_amdgcn_exp2f(1.4426950408889634f * la);
+  const float e = sizeof(T) == 4 ? exp_f32(la) : __builtin_amdgcn_exp2f(1.4426950408889634f * la);
   const bool near = fabsf(la) < kNear<T>;
   a = near ? 1.f + p : e;
   left = near ? -p * (2.f + p) : fmaf(-e, e, 1.f);
