@@ -444,8 +444,9 @@ ret_status_t retention_residual_norm_bwd(const ret_norm_desc_t *desc, float skip
  * word 1 (retention_chunkwise_error reads it from these workspaces too); seqlen only
  * has to be >= 1. With cu_seqlens NULL total_tokens is ignored.
  *
- * Limits: width <= 65536, at most 2^31 - 2^16 tokens, tokens * width small enough for
- * a launch (2^34 always is); strides below 2^22, of single tokens below 2^31.
+ * Limits: width <= 65536; at most 2^31 - 2^16 tokens; ceil(width / 64) times
+ * the 128-token tiles of all sequences (at least one each; packed: total_tokens / 128
+ * + batch) below 2^22; strides below 2^22, of single tokens below 2^31.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t batch;        /* >= 1: sequences                                         */

@@ -11,7 +11,7 @@ using namespace ret_host;
 using ret::tile_count;
 
 constexpr int64_t kMaxTokens = (int64_t)INT32_MAX - 65536;  // room for a tile behind the last token
-constexpr int kSmallestTile = 64;                             // tokens of a workgroup, at least
+constexpr int kSmallestTile = 128;                            // tokens of a workgroup where there are many
 constexpr int64_t kMaxTileStride = 1 << 22;
 constexpr int64_t kMaxThreads = (int64_t)1 << 32;           // of a launch
 

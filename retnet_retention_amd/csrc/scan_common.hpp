@@ -121,7 +121,7 @@ __device__ __forceinline__ int64_t kept_row(const P& p, int b, int tok0) {
 
 // Tile `j` as sequence b and its tile i, for tiles numbered as scan.hpp tells.
 // Packed: b is the last sequence whose first tile is j or before it; every lane of
-// a wave looks at one sequence. A tile of no sequence gets an i behind every end.
+// a wave looks at one of 64. A tile of no sequence gets an i behind every end.
 template <typename P>
 __device__ __forceinline__ void tile_of(const P& p, int64_t j, int tile, int& b, int& i) {
   if (!p.cu) {
@@ -131,13 +131,16 @@ __device__ __forceinline__ void tile_of(const P& p, int64_t j, int tile, int& b,
     return;
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += 64) {
-    const int s = b0 + lane;
-    const bool hit = s < p.batch && min(max(p.cu[s], 0), p.total) / tile + (int64_t)s <= j;
-    before += __popcll(__ballot(hit));
+  int from = 0, n = p.batch;  // the sequences among which it is
+  auto begun = [&](int s) { return min(max(p.cu[s], 0), p.total) / tile + (int64_t)s <= j; };
+  while (n > 64) {
+    const int step = (n + 63) / 64, end = from + n;
+    const int hits = __popcll(__ballot(lane * step < n && begun(from + lane * step)));
+    from += max(hits - 1, 0) * step;
+    n = min(step, end - from);
   }
-  b = max(before, 1) - 1;
+  const int hits = __popcll(__ballot(lane < n && begun(from + lane)));
+  b = from + max(hits, 1) - 1;
   i = (int)j - (min(max(uniform_i(p.cu[b]), 0), p.total) / tile + b);
   if (i < 0 || i > p.total / tile) i = p.total / tile + 1;
 }
@@ -264,11 +267,13 @@ __device__ __forceinline__ void hand_on(uint64_t* word, float x) {
 }
 // Waits until the word is there, in every lane of the wave that asks.
 __device__ __forceinline__ float take_over(const uint64_t* word, bool asks, int* ctrl) {
-  constexpr int kSpinLimit = 1 << 21;  // some seconds
+  constexpr int kSpinLimit = 1 << 21;  // more than a second
   uint64_t w = 0;
   for (int spins = 0;; ++spins) {
     if (asks) w = __hip_atomic_load(const_cast<uint64_t*>(word), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (__all(!asks || (w >> 32))) break;
+    // after an error (bounds that do not follow each other among them) nobody may come
+    if (spins % 256 == 255 && __hip_atomic_load(ctrl + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0) break;
     if (spins > kSpinLimit) {
       atomicOr(ctrl + 1, 1);
       break;
