@@ -475,8 +475,9 @@ ret_status_t retention_scan_fwd(const ret_scan_desc_t *desc, const int32_t *cu_s
  * state_in; drate, dgate, d_state_in are non-NULL exactly when rate, gate, state_in
  * are. kept: what a forward of the same inputs wrote there, or NULL. Rows before
  * the first packed sequence and behind the last get gradient 0. Where a log decay is
- * 0, normalize gives it the gradient of the recurrence alone (sqrt(1 - a^2) has
- * none there; decay's gradient goes to this as its sigmoid goes to 0). A factor of 0
+ * 0 (or 1 - a^2 below the smallest normal number), normalize gives it the gradient
+ * of the recurrence alone: sqrt(1 - a^2) has none there, and decay's gradient goes to
+ * this as its sigmoid goes to 0. A factor of 0
  * in 32 bits has gradient 0. */
 size_t retention_scan_bwd_workspace_bytes(const ret_scan_desc_t *desc, int32_t packed, int64_t total_tokens,
                                           int32_t has_kept);

@@ -262,7 +262,8 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
               q = left_of<T>(-rate[e] * sd[j][e], av);
             else
               q = rest[j][e];
-            const float inv = q > 0.f ? __builtin_amdgcn_rsqf(q) : 0.f;
+            // (below the normal numbers too: the hardware's root takes those for 0)
+            const float inv = q >= 0x1p-126f ? __builtin_amdgcn_rsqf(q) : 0.f;
             m = q * inv;
             dla = fmaf(-ag * av * inv, s * xs[e], dla);
           }

@@ -299,3 +299,22 @@ def test_convolution_of_one_tensor_with_itself_in_pieces_of_any_size():
             outs.append(rr.short_conv_fwd(x["x"][:, a:b], x["weight"], x["bias"], swish=True, state_in=s, state_out=s))
         near(torch.cat(outs, 1), f64(whole["o"]), CONV, "o")
         assert torch.equal(s, whole["state"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decays_next_to_nothing(dtype):
+    """Gates so far shut, or rates so small, that 1 - a^2 has no normal number: finite gradients, and the formula's where
+    they count. A decay that small moves nothing: 2^-63 is the root of the smallest normal number."""
+    x = scan_inputs(64, (2, 140), 66, dtype, "gates", state=2)
+    x["decay"][:, ::3] = -87.0
+    x["decay"][:, 1::3] = -100.0
+    x["rate"][:20], x["rate"][20:30], x["rate"][30:35] = 0.01, 0.0, 1e-38
+    got, a = run_scan(dev(x), True), {k: f64(t) for k, t in x.items()}
+    want = dict(zip(("o", "state"), oracle.scan(a["x"], a["decay"], a["gate"], a["rate"], True, a["s0"])))
+    g = oracle.scan_grad(a["x"], a["decay"], a["dout"], a["gate"], a["rate"], True, a["s0"], a["ds"])
+    want.update(dict(zip(("dx", "ddecay", "dgate", "drate", "dstate"), g)))
+    for k in got:
+        assert torch.isfinite(got[k].float()).all(), k
+        if k == "drate":  # the root's own share, s_d / m times a gradient, is below 2^-40 of the rest where 1 - a^2 is lost
+            continue
+        near(got[k], want[k], 4 * fwd_bar(140), k)
