@@ -9,7 +9,12 @@
 // gradient of the state behind it comes from the tile after it, as a word in memory.
 // Tiles start from the last. A tile's share of drate goes to a row of sums that a
 // second launch adds up in a fixed order. The gradients' stores bypass the caches, which
-// leaves the inputs there: 4 x 2048 x 2560 right after its forward 80 -> 64 us.
+// leaves the inputs there for whatever reads them next to the call.
+// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 70 us (4.2 TB/s), the
+// stores through the caches 80; 1 x 32768 x 1024 170 us (the chain of 256 tiles), 1 x
+// 131072 x 2560 1185 us (4.0 TB/s). Bound by the two together: the SIMDs compute in 60 % of
+// their cycles (74 vector instructions for 64 elements), waves wait in 35 % of theirs for
+// memory. 128 registers a lane, two workgroups a CU: one of each fetches while the other computes.
 #include "norms.hpp"
 #include "scan_common.hpp"
 
@@ -233,9 +238,10 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
         h[e] = FORGET ? step_or_forget(a[j][e], h[e], u) : fmaf(a[j][e], h[e], u);
       }
     }
-    const Rows<T, V> to_x(dx + row * p.width, p.width, there, p.width, seg * kSegment, c);
-    const Rows<D, V> to_decay(ddecay + row * p.width, p.width, there, p.width, seg * kSegment, c);
-    const Rows<T, V> to_gate(dgate + (IGATE ? row * p.width : 0), p.width, there, p.width, seg * kSegment, c);
+    const Rows<T, V> to_x(dx + row * p.width, p.width, there, p.width, seg * kSegment, c, inside);
+    const Rows<D, V> to_decay(ddecay + row * p.width, p.width, there, p.width, seg * kSegment, c, inside);
+    const Rows<T, V> to_gate(dgate + (IGATE ? row * p.width : 0), p.width, there, p.width, seg * kSegment, c,
+                             inside);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
       float xs[V], d[V], o1[V], o2[V], o3[V];
@@ -254,9 +260,9 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
           // a token that forgets lets no gradient through, whatever reaches it
           const bool none = FORGET && av == 0.f;
           const float ag = none ? 0.f : av * g[e];
-          float dla = none ? 0.f : ag * hist[j][e], m = 1.f;
+          float dla = none ? 0.f : ag * hist[j][e], m = 1.f, r = 0.f;
           if constexpr (NORM) {
-            // a^2 / m; 0 where the decay is 0, the limit towards which ddecay goes
+            // a / m; 0 where the decay is 0, the limit towards which ddecay goes
             float q;
             if constexpr (GATES)
               q = left_of<T>(-rate[e] * sd[j][e], av);
@@ -265,23 +271,24 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
             // (below the normal numbers too: the hardware's root takes those for 0)
             const float inv = q >= 0x1p-126f ? __builtin_amdgcn_rsqf(q) : 0.f;
             m = q * inv;
-            dla = fmaf(-ag * av * inv, s * xs[e], dla);
+            r = av * inv;
           }
           o1[e] = g[e] * m * s;
-          if constexpr (IGATE) o3[e] = o1[e] * xs[e] * (1.f - s);
+          const float to_gated = o1[e] * xs[e];  // g m s_i x
+          if constexpr (NORM) dla = none ? 0.f : fmaf(-r * r, to_gated, dla);
+          if constexpr (IGATE) o3[e] = fmaf(-s, to_gated, to_gated);
           if constexpr (GATES) {
-            sum[j / kSegment][e] = fmaf(-sd[j][e], dla, sum[j / kSegment][e]);
-            o2[e] = -rate[e] * (1.f - sd[j][e]) * (sd[j][e] * dla);
+            const float t = sd[j][e] * dla;
+            sum[j / kSegment][e] -= t;
+            o2[e] = fmaf(rate[e], sd[j][e], -rate[e]) * t;
           } else {
             o2[e] = dla;
           }
           g[e] = ag;
         }
-        if (inside) {
-          to_x.template store<kStreamed>(j, o1);
-          to_decay.template store<kStreamed>(j, o2);
-          if constexpr (IGATE) to_gate.template store<kStreamed>(j, o3);
-        }
+        to_x.template store<kStreamed>(j, o1);
+        to_decay.template store<kStreamed>(j, o2);
+        if constexpr (IGATE) to_gate.template store<kStreamed>(j, o3);
       }
     }
   };
@@ -310,7 +317,8 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
 
 template <typename T, bool GATES, bool IGATE, bool NORM, int V>
 static hipError_t launch_bwd(const ScanParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((scan_bwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(kScanBwdTile * 4), 0, stream, p);
+  hipLaunchKernelGGL((scan_bwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(kScanBwdTile * 4), 0,
+                     stream, p);
   return hipGetLastError();
 }
 template <typename T, int V>

@@ -66,10 +66,13 @@ struct Rows {
   using Raw = lane_raw<T, V>;
   __amdgpu_buffer_rsrc_t rs;
   uint32_t at, step;  // bytes: the lane's, from a row to the next
-  // `row`: the lane's first row behind `base`, `c` its channel
-  __device__ __forceinline__ Rows(const T* base, int64_t stride, int rows, int width, int row, int c)
+  // `row`: the lane's first row behind `base`, `c` its channel; a lane that is not inside
+  // is sent behind the end of dense rows (below 2^31 bytes), where a store is dropped
+  __device__ __forceinline__ Rows(const T* base, int64_t stride, int rows, int width, int row, int c,
+                                  bool inside = true)
       : rs(scalar_rsrc(base, (uint32_t)((rows - 1) * stride + width) * (uint32_t)sizeof(T))),
-        at((uint32_t)(row * (uint32_t)stride + c) * (uint32_t)sizeof(T)), step((uint32_t)stride * (uint32_t)sizeof(T)) {}
+        at(inside ? (uint32_t)(row * (uint32_t)stride + c) * (uint32_t)sizeof(T) : 0x80000000u),
+        step((uint32_t)stride * (uint32_t)sizeof(T)) {}
   // a row that is there; one that may be behind the end (then zeros)
   __device__ __forceinline__ Raw load(int j) const { return get(at, j * step); }
   __device__ __forceinline__ Raw load_if(int j) const { return get(at + j * step, 0); }
