@@ -5,6 +5,10 @@
 //     dx_t = sum_j w_j dz_(t+K-1-j),   dw_j = sum_t dz_t x_(t-K+1+j),   dbias = sum dz.
 // Bound by memory: a wave holds 64 V channels of a tile's tokens and the K - 1 rows
 // beside it, so each row is read once but for those.
+// Measured in bf16, 4 taps with bias and swish, kernel alone: forward 2 x 8192 x 12288 165 us
+// (4.9 TB/s; a copy reaches 5.07), its stores past the caches 160, but then whoever reads
+// the result next takes 13 us longer; backward 4 x 2048 x 7680 82 us (4.6 TB/s) and
+// 4.8 for the sums, with the SIMDs computing in 66 % of their cycles.
 #include "norms.hpp"
 #include "scan_common.hpp"
 
@@ -277,7 +281,9 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* partial, in
 }
 
 // Tokens of a wave in the backward: many, as each looks K - 1 past its own on both
-// sides and leaves a row of sums, but at least 4096 waves of 128 channels.
+// sides and leaves a row of sums, but at least 4096 waves of 128 channels, 16 a CU.
+// With 16 / 32 / 64 / 128: 4 x 2048 x 7680 109 / 86 / 75 / 72 us, 8 x 2048 x 2048 54 / 50 /
+// 45 / 45, 1 x 8192 x 1024 19 / 19 / 22 / 30.
 int conv_bwd_rows(int64_t tokens, int width) {
   const int64_t groups = (width + 127) / 128;
   int rows = 128;

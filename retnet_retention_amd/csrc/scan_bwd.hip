@@ -9,10 +9,11 @@
 // gradient of the state behind it comes from the tile after it, as a word in memory.
 // Tiles start from the last. A tile's share of drate goes to a row of sums that a
 // second launch adds up in a fixed order. The gradients' stores bypass the caches, which
-// leaves the inputs there for whatever reads them next to the call.
-// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 70 us (4.2 TB/s), the
-// stores through the caches 80; 1 x 32768 x 1024 170 us (the chain of 256 tiles), 1 x
-// 131072 x 2560 1185 us (4.0 TB/s). Bound by the two together: the SIMDs compute in 60 % of
+// leaves the inputs there: 4 x 2048 x 2560 again and again 63 us a call, not 80, right
+// after its forward 70 and 71.
+// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 70 us (4.2 TB/s); 1 x
+// 32768 x 1024 170 us (the chain of 256 tiles); 1 x 131072 x 2560 1185 us (4.0 TB/s).
+// Bound by memory and arithmetic together: the SIMDs compute in 60 % of
 // their cycles (74 vector instructions for 64 elements), waves wait in 35 % of theirs for
 // memory. 128 registers a lane, two workgroups a CU: one of each fetches while the other computes.
 #include "norms.hpp"

