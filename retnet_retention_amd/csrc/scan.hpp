@@ -22,6 +22,9 @@ inline int64_t tile_count(int batch, int seqlen, bool packed, int64_t total, int
 //     2 x 8192 x 4096 123 and 122, 4 x 2048 x 2560 with its inputs in the caches 40 and 36;
 //   backward, 128 and 64: 1 x 32768 x 1024 188 and 327 us, 4 x 2048 x 2560 72 and 70.
 constexpr int kScanTile = 256, kScanBwdTile = 128;
+// Sequences of up to this many tokens may be one tile of the forward, of 1024 threads: then
+// there is nothing to hand on, and nothing to clear before (scan_fwd.hip tells when).
+constexpr int kScanOnly = 512;
 // Channels of a workgroup: rows of 128 bytes in bf16, and a wave's lanes in the chain.
 constexpr int kScanChannels = 64;
 

@@ -17,6 +17,8 @@
 // reaches 5.07), 1 x 32768 x 1024 86 us (the chain of 128 tiles), 1 x 131072 x 2560 577 us
 // (4.65 TB/s); 4 x 2048 x 2560 with the states kept 43 us. The SIMDs compute in 56 % of
 // their cycles (34 vector instructions for 64 elements), waves wait in 43 % of theirs.
+#include <algorithm>
+
 #include "scan_common.hpp"
 
 // The variants of a kernel give the same bits: fused multiply-adds only where they are written.
@@ -24,19 +26,20 @@
 
 namespace ret {
 
-constexpr int kSegment = 16;  // tokens; 16 segments a tile
+constexpr int kSegment = 16;  // tokens
 
-template <typename T, bool GATES, bool IGATE, bool NORM, int V>
-__global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
+// TILE: kScanTile, or kScanOnly where no sequence has more than that
+template <typename T, bool GATES, bool IGATE, bool NORM, int V, int TILE>
+__global__ __launch_bounds__(TILE * 2) void scan_fwd_kernel(ScanParams p) {
   using D = std::conditional_t<GATES, T, float>;
-  constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = kScanTile / kSegment;
+  constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = TILE / kSegment;
   __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_h[kScanChannels];
   clear_errors(p);
-  const Place at = place_of<false>(p, kScanTile);
+  const Place at = place_of<false>(p, TILE);
   if (!at.any) return;
   int tok0, len;
   span_of(p, at.b, tok0, len);
-  const int from = at.i * kScanTile;  // the tile's first token
+  const int from = at.i * TILE;  // the tile's first token
   if (from >= len && !(at.i == 0 && len == 0)) return;
   const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
   const int seg = wave * 2 + lane / LW, cl = lane % LW * V;  // the lane's first segment
@@ -53,7 +56,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
     const T* gate = reinterpret_cast<const T*>(p.gate) + (IGATE ? row * p.gate_stride : 0);
     lane_raw<T, V> rx[L], rg[IGATE ? L : 1];
     lane_raw<D, V> rd[L];
-    const int there = min(left, kScanTile);
+    const int there = min(left, TILE);
     const Rows<T, V> xs(x, p.x_stride, there, p.width, seg * kSegment, c);
     const Rows<D, V> ds(decay, p.decay_stride, there, p.width, seg * kSegment, c);
     const Rows<T, V> gs(gate, p.gate_stride, there, p.width, seg * kSegment, c);
@@ -98,7 +101,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
       A[k][e] = 1.f;
       U[k][e] = 0.f;
     }
-  const bool full = left >= kScanTile;
+  const bool full = left >= TILE;
   if (full)
     fold(std::true_type());
   else if (wave * 2 * kSegment < left)
@@ -129,34 +132,46 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
   __syncthreads();
   if (wave == 0) {
     const int ch = c0 + lane;
-    const bool mine = ch < p.width, last = left <= kScanTile;
+    const bool mine = ch < p.width, last = left <= TILE;
     const int64_t held = (int64_t)at.b * p.width + ch;
-    float fa[SEGS], fu[SEGS], ta = 1.f, tu = 0.f;
-#pragma unroll
-    for (int s = 0; s < SEGS; ++s) {
-      const float sa = s_a[s][lane], su = s_u[s][lane];
-      fa[s] = ta;
-      fu[s] = tu;
-      tu = step_or_forget(sa, tu, su);
-      ta *= sa;
-    }
-#pragma unroll
-    for (int s = 0; s < SEGS; ++s) {
-      s_a[s][lane] = fa[s];
-      s_u[s][lane] = fu[s];
-    }
     float h = 0.f;
-    if (at.i > 0)
-      h = take_over(p.hand + (at.tile - 1) * p.width + ch, mine, p.ctrl);
-    else if (p.state_in && mine)
-      h = p.state_in[held];
-    s_h[lane] = h;
-    h = step_or_forget(ta, h, tu);
-    if (mine) {
-      if (!last)
-        hand_on(p.hand + at.tile * p.width + ch, h);
-      else if (p.state_out)
-        p.state_out[held] = h;
+    if (TILE == kScanOnly) {
+      // no state to wait for: the segments one after the other
+      if (p.state_in && mine) h = p.state_in[held];
+#pragma unroll 8
+      for (int s = 0; s < SEGS; ++s) {
+        const float sa = s_a[s][lane], su = s_u[s][lane];
+        s_u[s][lane] = h;
+        h = step_or_forget(sa, h, su);
+      }
+      if (mine && p.state_out) p.state_out[held] = h;
+    } else {
+      float fa[SEGS], fu[SEGS], ta = 1.f, tu = 0.f;
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s) {
+        const float sa = s_a[s][lane], su = s_u[s][lane];
+        fa[s] = ta;
+        fu[s] = tu;
+        tu = step_or_forget(sa, tu, su);
+        ta *= sa;
+      }
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s) {
+        s_a[s][lane] = fa[s];
+        s_u[s][lane] = fu[s];
+      }
+      if (at.i > 0)
+        h = take_over(p.hand + (at.tile - 1) * p.width + ch, mine, p.ctrl);
+      else if (p.state_in && mine)
+        h = p.state_in[held];
+      s_h[lane] = h;
+      h = step_or_forget(ta, h, tu);
+      if (mine) {
+        if (!last)
+          hand_on(p.hand + at.tile * p.width + ch, h);
+        else if (p.state_out)
+          p.state_out[held] = h;
+      }
     }
   }
   __syncthreads();
@@ -166,14 +181,15 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanParams p) {
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      h0[k][e] = step_or_forget(s_a[seg + k][cl + e], s_h[cl + e], s_u[seg + k][cl + e]);
+      h0[k][e] = TILE == kScanOnly ? s_u[seg + k][cl + e]
+                                   : step_or_forget(s_a[seg + k][cl + e], s_h[cl + e], s_u[seg + k][cl + e]);
   if (p.kept && seg * kSegment % kScanBwdTile == 0) {
     float* kept = p.kept + (kept_row(p, at.b, tok0) + (from + seg * kSegment) / kScanBwdTile) * p.width + c;
 #pragma unroll
     for (int e = 0; e < V; ++e) kept[e] = h0[0][e];
   }
   if (!p.o) return;
-  const Rows<T, V> o(reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width, p.width, min(left, kScanTile),
+  const Rows<T, V> o(reinterpret_cast<T*>(p.o) + ((int64_t)tok0 + from) * p.width, p.width, min(left, TILE),
                      p.width, seg * kSegment, c);
   auto run = [&](auto full, auto forget) {
     float h[V];
@@ -239,30 +255,50 @@ hipError_t launch_check_bounds(const int* cu, int batch, int total, int* ctrl, h
   return hipGetLastError();
 }
 
-template <typename T, bool GATES, bool IGATE, bool NORM, int V>
+template <typename T, bool GATES, bool IGATE, bool NORM, int V, int TILE>
 static hipError_t launch_fwd(const ScanParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((scan_fwd_kernel<T, GATES, IGATE, NORM, V>), dim3(scan_grid(p)), dim3(512), 0, stream, p);
+  hipLaunchKernelGGL((scan_fwd_kernel<T, GATES, IGATE, NORM, V, TILE>), dim3(scan_grid(p)), dim3(TILE * 2), 0, stream,
+                     p);
   return hipGetLastError();
 }
-template <typename T, int V>
+template <typename T, int V, int TILE>
 static hipError_t launch_fwd_v(const ScanParams& p, hipStream_t s) {
   const int which = (p.rate ? 4 : 0) + (p.gate ? 2 : 0) + (p.normalize ? 1 : 0);
   switch (which) {
-    case 0: return launch_fwd<T, false, false, false, V>(p, s);
-    case 1: return launch_fwd<T, false, false, true, V>(p, s);
-    case 2: return launch_fwd<T, false, true, false, V>(p, s);
-    case 3: return launch_fwd<T, false, true, true, V>(p, s);
-    case 4: return launch_fwd<T, true, false, false, V>(p, s);
-    case 5: return launch_fwd<T, true, false, true, V>(p, s);
-    case 6: return launch_fwd<T, true, true, false, V>(p, s);
-    default: return launch_fwd<T, true, true, true, V>(p, s);
+    case 0: return launch_fwd<T, false, false, false, V, TILE>(p, s);
+    case 1: return launch_fwd<T, false, false, true, V, TILE>(p, s);
+    case 2: return launch_fwd<T, false, true, false, V, TILE>(p, s);
+    case 3: return launch_fwd<T, false, true, true, V, TILE>(p, s);
+    case 4: return launch_fwd<T, true, false, false, V, TILE>(p, s);
+    case 5: return launch_fwd<T, true, false, true, V, TILE>(p, s);
+    case 6: return launch_fwd<T, true, true, false, V, TILE>(p, s);
+    default: return launch_fwd<T, true, true, true, V, TILE>(p, s);
   }
 }
-hipError_t launch_scan_fwd(const ScanParams& p, int dtype, hipStream_t stream) {
+template <int TILE>
+static hipError_t launch_fwd_t(const ScanParams& p, int dtype, hipStream_t stream) {
   const hipError_t e = launch_scan_prep(p, stream);
   if (e != hipSuccess) return e;
-  if (dtype != 1) return launch_fwd_v<float, 1>(p, stream);
-  return in_pairs(p) ? launch_fwd_v<bf16, 2>(p, stream) : launch_fwd_v<bf16, 1>(p, stream);
+  if (dtype != 1) return launch_fwd_v<float, 1, TILE>(p, stream);
+  return in_pairs(p) ? launch_fwd_v<bf16, 2, TILE>(p, stream) : launch_fwd_v<bf16, 1, TILE>(p, stream);
+}
+// A sequence of up to kScanOnly tokens as one tile spares the launch that clears the
+// words, and a hop, but its workgroups fill a CU alone; taken where there is one for each
+// CU at most. bf16, a whole call from a graph, as one and as two tiles: 1 x 257 x 1024 10.2
+// and 10.8 us (from the host 13.3 and 16.4), 16 x 300 x 1024 12.4 and 15.0, 32 x 300 x
+// 1024 24.9 and 23.2, 64 x 300 x 1024 44 and 41.
+static bool in_one(const ScanParams& p) {
+  const int groups = (p.width + kScanChannels - 1) / kScanChannels;
+  // (its rows are addressed with 32 bits from its first one)
+  const bool far = std::max({p.x_stride, p.decay_stride, p.gate_stride}) >= (int64_t)1 << 21;
+  return p.hand && !far && !has_chain(p.seqlen, p.cu, p.total, kScanOnly) && (int64_t)p.batch * groups <= 256;
+}
+hipError_t launch_scan_fwd(const ScanParams& p, int dtype, hipStream_t stream) {
+  if (!in_one(p)) return launch_fwd_t<kScanTile>(p, dtype, stream);
+  ScanParams only = p;
+  only.hand = nullptr;
+  only.tiles = (int)tile_count(p.batch, p.seqlen, p.cu, p.total, kScanOnly);
+  return launch_fwd_t<kScanOnly>(only, dtype, stream);
 }
 
 }  // namespace ret

@@ -8,7 +8,8 @@ import torch
 
 import retnet_retention_amd as rr
 from oracle import scan_oracle as oracle
-from test_gpu_scan import CONV, DEV, conv_inputs, dev, f64, fwd_bar, near, run_conv, run_scan, scan_inputs
+from test_gpu_scan import (CONV, DEV, FORMS, check_scan, conv_inputs, dev, f64, fwd_bar, near, run_conv, run_scan,
+                           scan_inputs, scan_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -318,3 +319,57 @@ def test_decays_next_to_nothing(dtype):
         if k == "drate":  # the root's own share, s_d / m times a gradient, is below 2^-40 of the rest where 1 - a^2 is lost
             continue
         near(got[k], want[k], 4 * fwd_bar(140), k)
+
+
+@pytest.mark.parametrize("form,gate,normalize", FORMS)
+@pytest.mark.parametrize("dtype,w", [("bf16", 130), ("bf16", 67), ("f32", 65)])
+def test_forms_of_more_than_one_tile(form, gate, normalize, dtype, w):
+    x = scan_inputs(60, (2, 700), w, dtype, form, gate, state=2)
+    check_scan(run_scan(dev(x), normalize), scan_reference(x, normalize), 700, 1400)
+
+
+@pytest.mark.parametrize("b,n,lens", [(1, 512, None), (1, 257, None), (5, 400, None), (260, 260, None),
+                                      (3, None, [257, 0, 200]), (4, None, [1, 510, 0, 1]), (2, None, [0, 300]),
+                                      (600, None, [1, 0] * 250 + [2] * 100)])
+def test_sequences_of_one_workgroup(b, n, lens):
+    """Up to 512 tokens: sequences that are one tile where there are few of them, and two where there are many."""
+    rows = (sum(lens),) if lens else (b, n)
+    x = scan_inputs(61, rows, 66, "bf16", "gates", state=b)
+    more = dict(cu_seqlens=i32([0] + list(np.cumsum(lens))), check=True) if lens else {}
+    got = run_scan(dev(x), True, **more)
+    check_scan(got, scan_reference(x, True, lens), max(lens) if lens else n, int(np.prod(rows)))
+    # a state of NaN behind a factor of 0 is forgotten there too
+    y = dev(x)
+    if lens:
+        y["decay"][torch.tensor([t for t, k in zip(np.cumsum([0] + lens[:-1]), lens) if k], device=DEV)] = 88.
+    else:
+        y["decay"][:, 0] = 88.
+    y["rate"] = torch.full_like(y["rate"], 200.)
+    y["s0"] = torch.full_like(y["s0"], float("nan"))
+    s = y["s0"].clone()
+    o = rr.gated_scan_fwd(y["x"], y["decay"], y["gate"], rate=y["rate"], state_in=y["s0"], state_out=s, **more)
+    assert torch.isfinite(o.float()).all()
+    held = torch.tensor([k > 0 for k in lens], device=DEV) if lens else torch.ones(b, dtype=torch.bool, device=DEV)
+    assert torch.isfinite(s[held]).all() and torch.isnan(s[~held]).all()
+
+
+@pytest.mark.parametrize("stride", [2 ** 20, 2 ** 21, 2 ** 22 - 8])
+def test_rows_that_lie_far_apart(stride):
+    """300 tokens up to 8 MiB from one another."""
+    free_memory(300 * stride * 2 + (2 << 30))
+    x = scan_inputs(62, (1, 300), 66, "bf16", "gates", state=1)
+    y = dev(x)
+    big = torch.empty(300 * stride, dtype=torch.bfloat16, device=DEV)
+    y["x"] = big.view(1, 300, stride)[:, :, 7 * 64:7 * 64 + 66].copy_(y["x"])
+    assert y["x"].stride(1) == stride
+    check_scan(run_scan(y, True), scan_reference(x, True), 300, 300)
+
+
+def test_rows_of_fp32_that_lie_far_apart():
+    """300 tokens 8 MiB apart in fp32."""
+    stride = 2 ** 21
+    free_memory(300 * stride * 4 + (2 << 30))
+    x = scan_inputs(63, (1, 300), 65, "f32", "log", state=1)
+    y = dev(x)
+    y["decay"] = torch.empty(300 * stride, device=DEV).view(1, 300, stride)[:, :, :65].copy_(y["decay"])
+    check_scan(run_scan(y, True), scan_reference(x, True), 300, 300)
