@@ -4,8 +4,8 @@
 // keep a state to half a 127th of its block's largest value; e4m3 of the same size
 // keeps each value to a 16th of itself, five times worse over values of one
 // size. Bound by memory: 4 bytes a value on one side, 1.06 on the other. Measured, 64
-// states of 4 MiB, kernels alone: written in 78 us (4.4 TB/s), read back into a pool of fp32 in 49
-// (6.9 TB/s by the bytes; the codes just written come from the caches).
+// states of 4 MiB, kernels alone: written in 78 us (4.4 TB/s), read back in 49
+// (6.9 TB/s by the bytes: the codes just written come from the caches), read from 24 others' in 45.
 #include "common.hpp"
 #include "state_cache.hpp"
 
@@ -36,9 +36,11 @@ __device__ __forceinline__ int code_of(float x, float scale, float inv) {
   return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// 16 lanes take a block of 64 values, 4 values each; a workgroup 16 blocks at a time,
-// kAtOnce times, all of them on their way from memory together.
-constexpr int kAtOnce = 4;
+// 16 lanes take a block of 64 values, 4 values each; a workgroup 16 blocks at a time, 4
+// times where it writes the cache, twice where it reads it, all of them on their way from
+// memory together. 64 states of 4 MiB written with 2 / 4 / 8: 81 / 78 / 80 us; read
+// with 1 / 2 / 4 / 8: 59 / 45 / 48 / 52 us.
+constexpr int kWriteAtOnce = 4, kReadAtOnce = 2;
 // `whole`: the states' rows are aligned to 4 values, so 4 are there or none
 // STREAM: states past the caches
 template <bool STREAM>
@@ -61,16 +63,16 @@ __global__ __launch_bounds__(256) void state_cache_write_kernel(StateCacheParams
   const int64_t to = listed(p.at, b, p.cache_slots), from = listed(p.slots, b, p.num_slots);
   if (to < 0 || from < 0) return;
   if (named_before(p.at, b)) return;
-  const int64_t first = (int64_t)blockIdx.x * 16 * kAtOnce + (threadIdx.x >> 4);
+  const int64_t first = (int64_t)blockIdx.x * 16 * kWriteAtOnce + (threadIdx.x >> 4);
   const int64_t v0 = first * kCacheBlock + 4 * (threadIdx.x & 15);
   const float* x = p.state + from * p.values;
   int8_t* codes = p.codes + to * p.values;
   const bool whole = p.values % 4 == 0;
-  f32x4 y[kAtOnce];
+  f32x4 y[kWriteAtOnce];
 #pragma unroll
-  for (int k = 0; k < kAtOnce; ++k) y[k] = four_of<STREAM>(x, v0 + k * 16 * kCacheBlock, p.values, whole);
+  for (int k = 0; k < kWriteAtOnce; ++k) y[k] = four_of<STREAM>(x, v0 + k * 16 * kCacheBlock, p.values, whole);
 #pragma unroll
-  for (int k = 0; k < kAtOnce; ++k) {
+  for (int k = 0; k < kWriteAtOnce; ++k) {
     const int64_t v = v0 + k * 16 * kCacheBlock, block = first + k * 16;
     // the largest magnitude by its bits: a NaN is above infinity
     uint32_t top = 0;
@@ -105,16 +107,16 @@ __global__ __launch_bounds__(256) void state_cache_read_kernel(StateCacheParams 
   const int64_t from = listed(p.at, b, p.cache_slots), to = listed(p.slots, b, p.num_slots);
   if (to < 0) return;
   if (named_before(p.slots, b)) return;
-  const int64_t first = (int64_t)blockIdx.x * 16 * kAtOnce + (threadIdx.x >> 4);
+  const int64_t first = (int64_t)blockIdx.x * 16 * kReadAtOnce + (threadIdx.x >> 4);
   const int64_t v0 = first * kCacheBlock + 4 * (threadIdx.x & 15);
   float* x = p.state + to * p.values;
   const bool whole = p.values % 4 == 0;
-  float scale[kAtOnce] = {};
-  uint32_t word[kAtOnce] = {};
+  float scale[kReadAtOnce] = {};
+  uint32_t word[kReadAtOnce] = {};
   if (from >= 0) {
     const int8_t* codes = p.codes + from * p.values;
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
+    for (int k = 0; k < kReadAtOnce; ++k) {
       const int64_t v = v0 + k * 16 * kCacheBlock, block = first + k * 16;
       if (block < p.blocks) scale[k] = p.scales[from * p.blocks + block];
       if (whole) {
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(256) void state_cache_read_kernel(StateCacheParams 
     }
   }
 #pragma unroll
-  for (int k = 0; k < kAtOnce; ++k) {
+  for (int k = 0; k < kReadAtOnce; ++k) {
     const int64_t v = v0 + k * 16 * kCacheBlock;
     f32x4 y;
 #pragma unroll
@@ -148,8 +150,8 @@ __global__ __launch_bounds__(256) void state_cache_read_kernel(StateCacheParams 
   }
 }
 
-static dim3 grid_of(const StateCacheParams& p) {
-  return dim3((unsigned)((p.blocks + 16 * kAtOnce - 1) / (16 * kAtOnce)), (unsigned)p.batch);
+static dim3 grid_of(const StateCacheParams& p, int at_once) {
+  return dim3((unsigned)((p.blocks + 16 * at_once - 1) / (16 * at_once)), (unsigned)p.batch);
 }
 // States that do not fit the cache behind the L2s (256 MB) cannot be found there
 // by whoever reads them next, so they bypass it: 64 states of 4 MiB are written in 76
@@ -160,16 +162,16 @@ static bool streams(const StateCacheParams& p) { return (size_t)p.batch * p.valu
 
 hipError_t launch_state_cache_write(const StateCacheParams& p, hipStream_t stream) {
   if (streams(p))
-    hipLaunchKernelGGL((state_cache_write_kernel<true>), grid_of(p), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((state_cache_write_kernel<true>), grid_of(p, kWriteAtOnce), dim3(256), 0, stream, p);
   else
-    hipLaunchKernelGGL((state_cache_write_kernel<false>), grid_of(p), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((state_cache_write_kernel<false>), grid_of(p, kWriteAtOnce), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 hipError_t launch_state_cache_read(const StateCacheParams& p, hipStream_t stream) {
   if (streams(p))
-    hipLaunchKernelGGL((state_cache_read_kernel<true>), grid_of(p), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((state_cache_read_kernel<true>), grid_of(p, kReadAtOnce), dim3(256), 0, stream, p);
   else
-    hipLaunchKernelGGL((state_cache_read_kernel<false>), grid_of(p), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((state_cache_read_kernel<false>), grid_of(p, kReadAtOnce), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
