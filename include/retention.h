@@ -542,7 +542,7 @@ ret_status_t retention_conv_step(const ret_conv_desc_t *desc, const void *x, con
  * Sequence b of `batch` moves between slot slots[b] of state (slots NULL: b itself,
  * then num_slots must equal batch) and slot cache_slots_of[b] of the cache (both
  * DEVICE int32 [batch], 4-byte aligned). Write: a sequence with a slot outside
- * either pool, or with a cache slot that an earlier one names, writes nothing.
+ * either pool, or with a cache slot that an earlier one writes, writes nothing.
  * Read: several sequences may read one cache slot (a shared prefix); a cache slot
  * outside the cache (-1) gives a state of zeros; a slot outside state, or named by an
  * earlier sequence, is not written.

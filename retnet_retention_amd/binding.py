@@ -1205,7 +1205,7 @@ def state_cache_write(state, codes, scales, cache_slots, *, slots=None):
     scale, a 127th of the largest magnitude. Sequence b (of cache_slots, GPU int32
     [batch]) goes from state slots[b] (GPU int32 [batch]; None: b) to cache slot
     cache_slots[b]; one with a slot outside either pool, or a cache slot that an
-    earlier one names, is left out. A block that holds NaN or infinity reads
+    earlier one writes, is left out. A block that holds NaN or infinity reads
     back as NaN."""
     desc = _cache_call(state, codes, scales, cache_slots, slots)
     with _current(state):

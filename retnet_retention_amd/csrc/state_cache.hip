@@ -17,11 +17,13 @@ __device__ __forceinline__ int64_t listed(const int* list, int i, int64_t n) {
   return s < 0 || s >= n ? -1 : s;
 }
 
-// Whether an earlier sequence of the batch names the same slot of `list`.
-__device__ __forceinline__ bool named_before(const int* list, int b) {
+// Whether an earlier sequence of the batch names the same slot of `list` and, with
+// `source`, one of its `n` slots there.
+__device__ __forceinline__ bool named_before(const int* list, int b, const int* source, int64_t n) {
   bool hit = false;
   if (list)
-    for (int i = threadIdx.x; i < b; i += blockDim.x) hit |= list[i] == list[b];
+    for (int i = threadIdx.x; i < b; i += blockDim.x)
+      hit |= list[i] == list[b] && (!source || (source[i] >= 0 && source[i] < n));
   return __syncthreads_or(hit);
 }
 
@@ -62,7 +64,7 @@ __global__ __launch_bounds__(256) void state_cache_write_kernel(StateCacheParams
   const int b = blockIdx.y;
   const int64_t to = listed(p.at, b, p.cache_slots), from = listed(p.slots, b, p.num_slots);
   if (to < 0 || from < 0) return;
-  if (named_before(p.at, b)) return;
+  if (named_before(p.at, b, p.slots, p.num_slots)) return;
   const int64_t first = (int64_t)blockIdx.x * 16 * kWriteAtOnce + (threadIdx.x >> 4);
   const int64_t v0 = first * kCacheBlock + 4 * (threadIdx.x & 15);
   const float* x = p.state + from * p.values;
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(256) void state_cache_read_kernel(StateCacheParams 
   const int b = blockIdx.y;
   const int64_t from = listed(p.at, b, p.cache_slots), to = listed(p.slots, b, p.num_slots);
   if (to < 0) return;
-  if (named_before(p.slots, b)) return;
+  if (named_before(p.slots, b, nullptr, 0)) return;
   const int64_t first = (int64_t)blockIdx.x * 16 * kReadAtOnce + (threadIdx.x >> 4);
   const int64_t v0 = first * kCacheBlock + 4 * (threadIdx.x & 15);
   float* x = p.state + to * p.values;

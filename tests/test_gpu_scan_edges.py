@@ -373,3 +373,14 @@ def test_rows_of_fp32_that_lie_far_apart():
     y = dev(x)
     y["decay"] = torch.empty(300 * stride, device=DEV).view(1, 300, stride)[:, :, :65].copy_(y["decay"])
     check_scan(run_scan(y, True), scan_reference(x, True), 300, 300)
+
+
+def test_a_sequence_that_parks_nothing_takes_no_slot():
+    """Idle sequences may name any cache slot: the next one that names it and has a state is parked there."""
+    live = torch.randn(3, 130, device=DEV)
+    codes, scales = torch.full((2, 130), 55, dtype=torch.int8, device=DEV), torch.full((2, 3), -1.0, device=DEV)
+    rr.state_cache_write(live, codes, scales, i32([1, 1, 1, 1, 0]), slots=i32([-1, 3, 2, 0, -5]))
+    want = oracle.park(f64(live[2:]))
+    np.testing.assert_array_equal(codes[1].cpu().numpy(), want[0][0])
+    np.testing.assert_array_equal(scales[1].cpu().numpy(), want[1][0])
+    assert (codes[0] == 55).all() and (scales[0] == -1).all()
