@@ -30,7 +30,7 @@ constexpr int kScanChannels = 64;
 
 // What the workgroups of a call hand each other: a control block (word 1: errors),
 // ticket counters 64 bytes apart, and a word for each tile and channel.
-constexpr int kScanQueues = 32;
+constexpr int kScanQueues = 16;
 constexpr size_t kScanCtrlBytes = 64 * (1 + kScanQueues);
 // whether any sequence has more than one tile of `tile` tokens
 inline bool has_chain(int seqlen, bool packed, int64_t total, int tile) { return (packed ? total : seqlen) > tile; }

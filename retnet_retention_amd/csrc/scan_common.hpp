@@ -209,8 +209,13 @@ __device__ __forceinline__ float left_of(float la, float a) {
 // A workgroup's tile and channels. Where tiles hand a state on, a workgroup takes
 // them by a ticket, so that whoever it waits for holds a lower one and runs already.
 // One counter for all of a launch would serialise its workgroups, so each has one of
-// up to 32 for its own part of the channels. Tiles of a queue run along time first,
-// the sequences of a batch side by side (reversed in the backward).
+// up to 16 for its own run of neighbouring channel groups. Workgroups go round the 8 XCDs,
+// so the queues of an XCD get neighbouring runs too: what its workgroups ask for at one
+// time are long pieces of a row. Tiles of a queue run along time first, the sequences of a
+// batch side by side (reversed in the backward).
+// Measured, forward in us, with 32 queues of groups 32 apart, then runs on 64 / 32 / 16 /
+// 8 queues: 2 x 8192 x 4096 128, 124 / 119 / 115 / 117; 1 x 16384 x 8192 238, 209 / 202 /
+// 202 / 197; 2 x 8192 x 5120 133, 139 / 133 / 137 / 139; 2 x 4096 x 6000 105, 103 / 95 / 95 / 96.
 struct ScanQueues {
   int groups, each, queues;  // channel groups, those of a queue, queues
 };
@@ -243,7 +248,8 @@ __device__ __forceinline__ Place place_of(const P& p, int tile) {
     ticket = uniform_i(s_ticket);
   }
   Place at;
-  at.group = queue + q.queues * (ticket % q.each);
+  const int run = q.queues % 8 ? queue : queue % 8 * (q.queues / 8) + queue / 8;
+  at.group = run * q.each + ticket % q.each;
   int j = ticket / q.each;
   if (BACK) j = p.tiles - 1 - j;
   if (p.cu) {

@@ -73,7 +73,7 @@ def test_any_bounds_stay_inside(batch):
 
 def queues_of(width):
     groups = -(-width // 64)
-    each = -(-groups // 32)
+    each = -(-groups // 16)
     return groups, each, -(-groups // each)
 
 
@@ -81,7 +81,7 @@ def queues_of(width):
 @pytest.mark.parametrize("batch,per", [(1, 1), (1, 5), (3, 4)])
 @pytest.mark.parametrize("back", [False, True])
 def test_whoever_is_waited_for_holds_a_lower_ticket(width, batch, per, back):
-    """Tickets of a queue cover every tile of its channel groups once, a tile's predecessor
+    """Tickets of a queue cover every tile of its run of channel groups once, a tile's predecessor
     (its successor in the backward) before the tile; the queues cover all groups."""
     groups, each, queues = queues_of(width)
     tiles = batch * per
@@ -92,7 +92,8 @@ def test_whoever_is_waited_for_holds_a_lower_ticket(width, batch, per, back):
         assert issued == tiles * each
         done = set()
         for ticket in range(issued):
-            group, j = queue + queues * (ticket % each), ticket // each
+            run = queue if queues % 8 else queue % 8 * (queues // 8) + queue // 8  # neighbouring ones on an XCD
+            group, j = run * each + ticket % each, ticket // each
             j = tiles - 1 - j if back else j
             b, i = j % batch, j // batch
             if group >= groups:
