@@ -5,9 +5,9 @@
 //     dx_t = sum_j w_j dz_(t+K-1-j),   dw_j = sum_t dz_t x_(t-K+1+j),   dbias = sum dz.
 // Bound by memory: a wave holds 64 V channels of a tile's tokens and the K - 1 rows
 // beside it, so each row is read once but for those.
-// Measured in bf16, 4 taps with bias and swish, kernel alone: forward 2 x 8192 x 12288 165 us
-// (4.9 TB/s; a copy reaches 5.07), its stores past the caches 160, but then whoever reads
-// the result next takes 13 us longer; backward 4 x 2048 x 7680 82 us (4.6 TB/s) and
+// Measured in bf16, 4 taps with bias and swish, kernel alone: forward 2 x 8192 x 12288 151 us
+// (5.3 TB/s; a copy reaches 5.07; its stores past the caches were 6 us faster, but then whoever
+// reads the result next takes 13 us longer); backward 4 x 2048 x 7680 82 us (4.6 TB/s) and
 // 4.8 for the sums, with the SIMDs computing in 66 % of their cycles.
 #include "norms.hpp"
 #include "scan_common.hpp"
@@ -37,15 +37,26 @@ struct ConvLine {
   }
 };
 
+// The piece of work, a tile's `groups` channel groups one after the other, of this
+// workgroup. Workgroups go round the 8 XCDs; of each 8 s of them an XCD's s, some eighth of
+// a tile's row, take neighbouring pieces. Forward and backward in us, taken as they come and
+// so: 2 x 8192 x 12288 168 / 279 and 153 / 278, 2 x 8192 x 6000 94 / 157 and 83 / 146, 2 x 8192
+// x 5120 72 / 115 and 65 / 112, 2 x 8192 x 4096 44 / 76 and 44 / 78.
+__device__ __forceinline__ unsigned piece_of(int groups) {
+  const unsigned s = (groups + 7) / 8, at = blockIdx.x % (8 * s), first = blockIdx.x - at;
+  return first + 8 * s <= gridDim.x ? first + at % 8 * s + at / 8 : blockIdx.x;
+}
+
 template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p) {
   constexpr int L = kConvRows;
   const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
   const int groups = (p.width + 64 * V - 1) / (64 * V);
   int b, i, tok0, len;
-  tile_of(p, blockIdx.x / groups, kConvTile, b, i);
+  const unsigned piece = piece_of(groups);
+  tile_of(p, piece / groups, kConvTile, b, i);
   span_of(p, b, tok0, len);
-  const int c = (blockIdx.x % groups * 64 + lane) * V;
+  const int c = (piece % groups * 64 + lane) * V;
   const int t0 = i * kConvTile + wave * L;
   const bool ends = p.state_out && i == 0 && wave == 0;  // reads the old state, and so writes the new one
   if (c >= p.width || (t0 >= len && !ends)) return;
@@ -103,11 +114,12 @@ __global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
   __shared__ float s_sum[4][K + 1][64 * V];
   const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6);
   const int groups = (p.width + 64 * V - 1) / (64 * V);
-  const int64_t block = blockIdx.x / groups;
+  const unsigned piece = piece_of(groups);
+  const int64_t block = piece / groups;
   int b, i, tok0, len;
   tile_of(p, block, 4 * p.rows, b, i);
   span_of(p, b, tok0, len);
-  const int at = (blockIdx.x % groups * 64 + lane) * V, c = min(at, p.width - V);
+  const int at = (piece % groups * 64 + lane) * V, c = min(at, p.width - V);
   const bool inside = at < p.width;
   const int t0 = (4 * i + wave) * p.rows;
   const bool begins = i == 0 && wave == 0;
