@@ -10,9 +10,12 @@
 // Tiles start from the last. A tile's share of drate goes to a row of sums that a
 // second launch adds up in a fixed order. The gradients' stores bypass the caches, which
 // leaves the inputs there: 4 x 2048 x 2560 again and again 63 us a call, not 80, right
-// after its forward 70 and 71.
-// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 70 us (4.2 TB/s); 1 x
-// 32768 x 1024 170 us (the chain of 256 tiles); 1 x 131072 x 2560 1185 us (4.0 TB/s).
+// after its forward 70 and 71. Not where rows end inside a line of 128 bytes, whose parts
+// two workgroups write: 4 x 8192 x 4100 609 us through the caches and 784 past them, 2 x
+// 8192 x 4095 284 and 346, 2 x 4096 x 6000 189 and 207.
+// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 69 us (4.3 TB/s); calls of
+// 2 x 8192 x 4096 195 to 220 us, 1 x 16384 x 8192 375 us (5.0 TB/s), 1 x 32768 x 1024 171 us
+// (the chain of 256 tiles), 1 x 131072 x 2560 1146 us (4.1 TB/s).
 // Bound by memory and arithmetic together: the SIMDs compute in 60 % of
 // their cycles (74 vector instructions for 64 elements), waves wait in 35 % of theirs for
 // memory. 128 registers a lane, two workgroups a CU: one of each fetches while the other computes.
@@ -226,8 +229,9 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
   }
   __syncthreads();
   float sum[PARTS][V] = {};
-  auto run = [&](auto whole, auto forget) {
+  auto run = [&](auto whole, auto forget, auto stream) {
     constexpr bool FULL = decltype(whole)::value, FORGET = decltype(forget)::value;
+    constexpr int POLICY = decltype(stream)::value ? kStreamed : 0;
     float h[V], g[V];  // g: what reaches the token's state from behind
 #pragma unroll
     for (int j = 0; j < L; ++j) {
@@ -287,19 +291,23 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
           }
           g[e] = ag;
         }
-        to_x.template store<kStreamed>(j, o1);
-        to_decay.template store<kStreamed>(j, o2);
-        if constexpr (IGATE) to_gate.template store<kStreamed>(j, o3);
+        to_x.template store<POLICY>(j, o1);
+        to_decay.template store<POLICY>(j, o2);
+        if constexpr (IGATE) to_gate.template store<POLICY>(j, o3);
       }
     }
   };
   if (wave * 2 * kSegment < left) {
+    // rows of whole lines, or parts of a line have to meet in the L2
+    const bool lines = (uint32_t)p.width * (uint32_t)sizeof(T) % 128 == 0;
     if (forgets)
-      run(std::false_type(), std::true_type());
+      run(std::false_type(), std::true_type(), std::false_type());
+    else if (full && lines)
+      run(std::true_type(), std::false_type(), std::true_type());
     else if (full)
-      run(std::true_type(), std::false_type());
+      run(std::true_type(), std::false_type(), std::false_type());
     else
-      run(std::false_type(), std::false_type());
+      run(std::false_type(), std::false_type(), std::false_type());
   }
   if constexpr (GATES) {
 #pragma unroll
