@@ -16,8 +16,8 @@
 // Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 69 us (4.3 TB/s); calls of
 // 2 x 8192 x 4096 195 to 220 us, 1 x 16384 x 8192 375 us (5.0 TB/s), 1 x 32768 x 1024 171 us
 // (the chain of 256 tiles), 1 x 131072 x 2560 1146 us (4.1 TB/s).
-// Bound by memory and arithmetic together: the SIMDs compute in 60 % of
-// their cycles (74 vector instructions for 64 elements), waves wait in 35 % of theirs for
+// Bound by memory and arithmetic together: the SIMDs compute in 59 % of
+// their cycles (71 vector instructions for 64 elements), waves wait in 38 % of theirs for
 // memory. 128 registers a lane, two workgroups a CU: one of each fetches while the other computes.
 #include "norms.hpp"
 #include "scan_common.hpp"

@@ -13,8 +13,8 @@
 // Waiting one after the other takes 0.65 us a tile, less than the tiles of a
 // long sequence take at the memory's rate unless it is narrower than some 1000
 // channels; so tiles are long, 256 tokens.
-// Measured in bf16 with both gates, kernel alone: 2 x 8192 x 4096 109 us (4.9 TB/s; a copy
-// reaches 5.07), 4 x 2048 x 2560 with the states kept 43 us; calls of 1 x 16384 x 8192 200
+// Measured in bf16 with both gates, kernel alone: 2 x 8192 x 4096 109 to 115 us (4.7 to 4.9 TB/s; a
+// copy reaches 5.07), 4 x 2048 x 2560 with the states kept 43 us; calls of 1 x 16384 x 8192 200
 // us (5.4 TB/s), 1 x 32768 x 1024 86 us (the chain of 128 tiles), 1 x 131072 x 2560 562 us
 // (4.8 TB/s). Bound by memory: without any arithmetic or wait it took as long. 34 vector
 // instructions for 64 elements, more than half of the SIMDs' cycles. Segments of 8 tokens
