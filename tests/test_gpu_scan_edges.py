@@ -8,8 +8,8 @@ import torch
 
 import retnet_retention_amd as rr
 from oracle import scan_oracle as oracle
-from test_gpu_scan import (CONV, DEV, FORMS, check_scan, conv_inputs, dev, f64, fwd_bar, near, run_conv, run_scan,
-                           scan_inputs, scan_reference)
+from test_gpu_scan import (CONV, DEV, FORMS, check_conv, check_scan, conv_inputs, dev, f64, fwd_bar, near, run_conv,
+                           run_scan, scan_inputs, scan_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -384,3 +384,20 @@ def test_a_sequence_that_parks_nothing_takes_no_slot():
     np.testing.assert_array_equal(codes[1].cpu().numpy(), want[0][0])
     np.testing.assert_array_equal(scales[1].cpu().numpy(), want[1][0])
     assert (codes[0] == 55).all() and (scales[0] == -1).all()
+
+
+@pytest.mark.parametrize("dtype,w", [("bf16", 1024), ("bf16", 1155), ("bf16", 1282), ("bf16", 7000), ("f32", 2049)])
+@pytest.mark.parametrize("lens", [None, [130, 0, 700, 1]])
+def test_widths_of_the_convolution(dtype, w, lens):
+    """Each channel by itself, also where a row is more than eight workgroups wide: the formula's values on the first
+    channels, the last ones and some between."""
+    rows, b = ((sum(lens),), len(lens)) if lens else ((3, 300), 3)
+    x = conv_inputs(64, rows, w, 4, dtype, state=b)
+    more = dict(cu_seqlens=i32([0] + list(np.cumsum(lens))), check=True) if lens else {}
+    got = run_conv(dev(x), True, **more)
+    for at in (0, 512, w - 70):
+        part = {k: None if t is None else t[at:at + 70] if k in ("weight", "bias") else
+                t[..., at:at + 70] for k, t in x.items()}
+        cut = {k: None if t is None else t[at:at + 70] if k in ("dweight", "dbias") else
+               t[..., at:at + 70] for k, t in got.items()}
+        check_conv(cut, part, True, lens)
