@@ -1030,7 +1030,7 @@ def gated_scan_fwd(x, decay, gate=None, *, rate=None, normalize=False, state_in=
     packed = int(cu_seqlens is not None)
     kept = None
     if keep:
-        kept = torch.empty(L.retention_scan_kept_bytes(desc, packed, total) // 4, device=x.device)
+        kept = torch.empty(L.retention_scan_kept_bytes(desc, packed, total) // 4, dtype=torch.float32, device=x.device)
     workspace, ws_bytes, _ = _workspace(workspace, L.retention_scan_workspace_bytes(desc, packed, total), x)
     with _current(x):
         _check(L.retention_scan_fwd(desc, _ptr(cu_seqlens), total, _ptr(x), _ptr(decay), _ptr(rate), _ptr(gate),

@@ -2,6 +2,7 @@
 the host: the fp64 oracle against differences and other forms of itself, the C
 ABI's refusals and sizes, the binding's checks (no kernel is launched)."""
 
+import contextlib
 import ctypes
 import os
 
@@ -283,3 +284,33 @@ def test_tensors_on_the_host_are_refused():
     with pytest.raises(ValueError):
         binding.state_cache_write(torch.zeros(2, 64), torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2, 1),
                                   torch.zeros(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("default", [torch.bfloat16, torch.float16, torch.float64, torch.float32])
+def test_kept_states_are_fp32_whatever_the_default_type(monkeypatch, default):
+    """The library takes no size for them: the buffer has the bytes that it asked for."""
+    need, seen = 4 * 640, {}
+
+    class Library:
+        def retention_scan_kept_bytes(self, *_):
+            return need
+
+        def retention_scan_workspace_bytes(self, *_):
+            return 256
+
+        def retention_scan_fwd(self, *args):
+            seen["kept"] = args[10]
+            return 0
+
+    monkeypatch.setattr(binding, "lib", Library)
+    monkeypatch.setattr(binding, "_scan_call", lambda x, *_: (None, x.shape[0], 0, x.shape[2]))
+    monkeypatch.setattr(binding, "_current", lambda t: contextlib.nullcontext())
+    monkeypatch.setattr(binding, "_stream", lambda t: None)
+    x = torch.zeros(2, 300, 64, dtype=torch.float32)
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        _, kept = binding.gated_scan_fwd(x, x, keep=True)
+    finally:
+        torch.set_default_dtype(before)
+    assert kept.data_ptr() == seen["kept"] and kept.dtype == torch.float32 and kept.numel() * kept.element_size() == need
