@@ -57,7 +57,8 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
     // rows before the first sequence and behind the last have gradient 0
     auto clear = [&](int t0, int t1) {
       const float zero[V] = {};
-      for (int64_t t = t0 + seg; t < t1 && inside; t += SEGS) {
+      // a row for each wave, with pairs of channels for each half of one
+      for (int64_t t = t0 + (V == 1 ? wave : seg); t < t1 && inside; t += V == 1 ? SEGS / 2 : SEGS) {
         lane_store<T, V>(dx + t * p.width, c, zero);
         lane_store<D, V>(ddecay + t * p.width, c, zero);
         if constexpr (IGATE) lane_store<T, V>(dgate + t * p.width, c, zero);

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import retnet_retention_amd as rr
+from retnet_retention_amd import binding
 from oracle import scan_oracle as oracle
 from test_gpu_scan import (CONV, DEV, FORMS, check_conv, check_scan, conv_inputs, dev, f64, fwd_bar, near, run_conv,
                            run_scan, scan_inputs, scan_reference)
@@ -401,3 +402,20 @@ def test_widths_of_the_convolution(dtype, w, lens):
         cut = {k: None if t is None else t[at:at + 70] if k in ("dweight", "dbias") else
                t[..., at:at + 70] for k, t in got.items()}
         check_conv(cut, part, True, lens)
+
+
+@pytest.mark.parametrize("dtype,w,columns", [("bf16", 66, False), ("bf16", 67, False), ("bf16", 66, True), ("f32", 65, False)])
+@pytest.mark.parametrize("form,gate", [("gates", True), ("log", False)])
+@pytest.mark.parametrize("cu", [[300, 310, 390], [1, 1, 1], [0, 699, 699], [700, 700, 700], [17, 40, 683]])
+def test_every_row_outside_the_sequences_has_a_gradient_of_zero(monkeypatch, dtype, w, columns, form, gate, cu):
+    """Whether lanes take one channel or two, in gradients that held NaN before the call."""
+    x = dev(scan_inputs(65, (700,), w, dtype, form, gate, state=2))
+    if columns:  # at an odd offset: lanes cannot take pairs
+        x["x"] = torch.cat([x["x"][:, :1], x["x"]], 1)[:, 1:]
+        assert x["x"].data_ptr() % 4 == 2
+    monkeypatch.setattr(binding, "_dense_like", lambda t: torch.full(t.shape, float("nan"), dtype=t.dtype, device=t.device))
+    g = rr.gated_scan_bwd(x["x"], x["decay"], x["dout"], x["gate"], rate=x["rate"], state_in=x["s0"], d_state_out=x["ds"],
+                          cu_seqlens=i32(cu), check=True)
+    assert len(g) == 5 and all(t is None or torch.isfinite(t.float()).all() for t in g)
+    for t in g[:3]:
+        assert t is None or ((t[:cu[0]] == 0).all() and (t[cu[2]:] == 0).all())
