@@ -433,9 +433,13 @@ ret_status_t retention_residual_norm_bwd(const ret_norm_desc_t *desc, float skip
  * apart than `width` (columns of a wider projection): their strides count elements
  * from a token to the next, over the whole batch, and they need no more than their
  * element's alignment; o and all gradients are dense.
- * Log decays are meant to be <= 0. At -infinity, as for every factor that is 0 in
- * 32 bits, a token forgets whatever the state holds, NaN and infinity too. Other
- * values are computed as they stand (normalize gives NaN for those above 0).
+ * Log decays are meant to be <= 0. At -infinity, as for every factor that is 0 (below
+ * -87.3, where 32 bits have no normal numbers), a token forgets whatever the state
+ * holds, NaN and infinity too, and whatever the factors before it were. No product of
+ * other factors does: a state that is NaN or infinite stays so until such a token.
+ * Other values are computed as they stand (normalize gives NaN for those above 0); with
+ * factors above 1 a sequence is joined from parts of 8 to 16 tokens that may overflow by
+ * themselves, and what is then infinite token by token may be NaN.
  *
  * Packed sequences: with cu_seqlens (DEVICE int32 [batch + 1]) the tensors are
  * [total_tokens, width], sequence b holds rows cu_seqlens[b] .. cu_seqlens[b+1]-1,
@@ -478,7 +482,7 @@ ret_status_t retention_scan_fwd(const ret_scan_desc_t *desc, const int32_t *cu_s
  * 0 (or 1 - a^2 below the smallest normal number), normalize gives it the gradient
  * of the recurrence alone: sqrt(1 - a^2) has none there, and decay's gradient goes to
  * this as its sigmoid goes to 0. A factor of 0
- * in 32 bits has gradient 0. */
+ * has gradient 0 and lets none through to the tokens before it. */
 size_t retention_scan_bwd_workspace_bytes(const ret_scan_desc_t *desc, int32_t packed, int64_t total_tokens,
                                           int32_t has_kept);
 ret_status_t retention_scan_bwd(const ret_scan_desc_t *desc, const int32_t *cu_seqlens, int64_t total_tokens,

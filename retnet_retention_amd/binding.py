@@ -1020,8 +1020,9 @@ def gated_scan_fwd(x, decay, gate=None, *, rate=None, normalize=False, state_in=
     way for gated_scan_bwd. x, decay and gate may be columns of a wider
     projection. Packed sequences: [total_tokens, width] tensors with cu_seqlens
     (GPU int32 [batch + 1]); rows outside every sequence are left as they were.
-    A factor of 0 (log decay -infinity) forgets whatever the state holds. check:
-    as delta_chunkwise_fwd."""
+    A factor of 0 (log decay below -87.3) forgets whatever the state holds, NaN and
+    infinity too; no product of other factors does. check: as
+    delta_chunkwise_fwd."""
     out = _dense_like(x) if out is None else out
     desc, batch, total, width = _scan_call(x, decay, gate, rate, normalize, cu_seqlens, ("out", out, x.dtype))
     state = (batch, width)

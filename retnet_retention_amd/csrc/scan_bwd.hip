@@ -34,7 +34,9 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
   using D = std::conditional_t<GATES, T, float>;
   constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = kScanBwdTile / kSegment;
   __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_p[SEGS][kScanChannels],
-      s_r[SEGS][kScanChannels], s_back[kScanChannels];
+      s_r[SEGS][kScanChannels], s_pr[SEGS][kScanChannels], s_back[kScanChannels];
+  // exponents of products (s_a, s_p) that are no normal number; s_odd: whether a wave has some
+  __shared__ int s_e[SEGS][kScanChannels], s_pe[SEGS][kScanChannels], s_odd[SEGS / 2];
   clear_errors(p);
   const Place at = place_of<true>(p, kScanBwdTile);
   if (!at.any) return;
@@ -148,20 +150,20 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
     fold(std::true_type());
   else if (wave * 2 * kSegment < left)
     fold(std::false_type());
-  // a factor of 0 among the tokens (or a product that is): they may have to forget what is no number
-  bool forgets = false;
+  // a product that is no normal number: exact, and sums that forget what stood before them
+  bool odd = false;
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e) forgets |= A[k][e] == 0.f;
-  forgets = __any(forgets);
-  if (forgets) {
+    for (int e = 0; e < V; ++e) odd |= !is_normal(A[k][e]);
+  odd = __any(odd);
+  if (odd) {
 #pragma unroll
     for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float& U1 = U[j / kSegment][e];
-        U1 = step_or_forget(a[j][e], j % kSegment ? U1 : 0.f, hist[j][e]);
+        U1 = j % kSegment ? step_or_forget(a[j][e], U1, hist[j][e]) : hist[j][e];
       }
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
@@ -174,6 +176,21 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
         if (j < n) R1 = a[j][e] == 0.f ? 0.f : a[j][e] * (R1 + d[e]);
       }
     }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (!is_normal(A[k][e])) {
+          Growing t;
+          bool none = false;
+#pragma unroll
+          for (int j = 0; j < kSegment; ++j) {
+            none |= a[k * kSegment + j][e] == 0.f;
+            t.by(a[k * kSegment + j][e]);
+          }
+          A[k][e] = none ? 0.f : -t.m;
+          s_e[seg + k][cl + e] = t.e;
+        }
   }
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
@@ -183,25 +200,50 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
       s_u[seg + k][cl + e] = U[k][e];
       s_r[seg + k][cl + e] = R[k][e];
     }
+  if (lane == 0) s_odd[wave] = odd;
   __syncthreads();
-  const bool mine = ch < p.width;
+  const bool mine = ch < p.width, any_odd = __any(s_odd[lane % (SEGS / 2)]);
   if (wave == 0) {
     // gradients from behind
     const bool last = left <= kScanBwdTile;
     const int64_t held = (int64_t)at.b * p.width + ch;
-    float fa[SEGS], fr[SEGS], ta = 1.f, tr = 0.f;
+    float ta = 1.f, tr = 0.f, low = 1.f;
 #pragma unroll
     for (int s = SEGS - 1; s >= 0; --s) {
       const float sa = s_a[s][lane], sr = s_r[s][lane];
-      fa[s] = ta;
-      fr[s] = tr;
-      tr = step_or_forget(sa, tr, sr);
+      s_p[s][lane] = ta;
+      s_pr[s][lane] = tr;
+      tr = fmaf(sa, tr, sr);
       ta *= sa;
+      low = fminf(low, ta);
     }
+    bool far = !is_normal(ta) || !is_normal(low);
+    if (any_odd)
+      for (int s = 0; s < SEGS; ++s) far |= !is_normal(s_a[s][lane]);
+    const bool any_far = __any(far);
+    Product total = {ta, 0};
+    if (far) {
+      Growing t;
+      if (any_odd) {
+        tr = 0.f;
+#pragma unroll 4
+        for (int s = SEGS - 1; s >= 0; --s) {
+          const Product one = {s_a[s][lane], s_e[s][lane]};
+          s_p[s][lane] = -t.m;
+          s_pe[s][lane] = t.e;
+          s_pr[s][lane] = tr;
+          tr = step_over(one, tr, s_r[s][lane]);
+          t.by(one);
+        }
+      } else {  // (the sums as they are: every segment's factor is a normal number)
 #pragma unroll
-    for (int s = 0; s < SEGS; ++s) {
-      s_p[s][lane] = fa[s];
-      s_r[s][lane] = fr[s];
+        for (int s = SEGS - 1; s >= 0; --s) {
+          s_p[s][lane] = -t.m;
+          s_pe[s][lane] = t.e;
+          t.by(s_a[s][lane]);
+        }
+      }
+      total = t.product();
     }
     float back = 0.f;
     if (!last)
@@ -209,7 +251,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
     else if (p.d_state_out && mine)
       back = p.d_state_out[held];
     s_back[lane] = back;
-    back = step_or_forget(ta, back, tr);
+    back = any_far ? step_over(total, back, tr) : fmaf(ta, back, tr);
     if (mine) {
       if (at.i > 0)
         hand_on(p.hand + at.tile * p.width + ch, back);
@@ -218,15 +260,25 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
     }
   } else if (wave == 1) {
     // states from before
-    float h = 0.f, before[SEGS];
+    float h = 0.f;
     if (mine && len > 0) h = p.kept[(kept_row(p, at.b, tok0) + at.i) * p.width + ch];
+    if (any_odd) {
+#pragma unroll 1
+      for (int s = 0; s < SEGS; ++s) {
+        const float su = s_u[s][lane];
+        s_u[s][lane] = h;
+        h = step_over({s_a[s][lane], s_e[s][lane]}, h, su);
+      }
+    } else {
+      float before[SEGS];
 #pragma unroll
-    for (int s = 0; s < SEGS; ++s) {
-      before[s] = h;
-      h = step_or_forget(s_a[s][lane], h, s_u[s][lane]);
+      for (int s = 0; s < SEGS; ++s) {
+        before[s] = h;
+        h = fmaf(s_a[s][lane], h, s_u[s][lane]);
+      }
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s) s_u[s][lane] = before[s];
     }
-#pragma unroll
-    for (int s = 0; s < SEGS; ++s) s_u[s][lane] = before[s];
   }
   __syncthreads();
   float sum[PARTS][V] = {};
@@ -254,7 +306,9 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
       if ((j + 1) % kSegment == 0) {
         const int k = seg + j / kSegment;
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[e] = step_or_forget(s_p[k][cl + e], s_back[cl + e], s_r[k][cl + e]);
+        for (int e = 0; e < V; ++e) {
+          g[e] = step_over(s_p[k][cl + e], &s_pe[k][cl + e], s_back[cl + e], s_pr[k][cl + e]);
+        }
       }
       Lane<T, V>::get(rx[j], xs);
       Lane<T, V>::get(ro[j], d);
@@ -301,7 +355,7 @@ __global__ __launch_bounds__(kScanBwdTile * 4, 4) void scan_bwd_kernel(ScanParam
   if (wave * 2 * kSegment < left) {
     // rows of whole lines, or parts of a line have to meet in the L2
     const bool lines = (uint32_t)p.width * (uint32_t)sizeof(T) % 128 == 0;
-    if (forgets)
+    if (odd)
       run(std::false_type(), std::true_type(), std::false_type());
     else if (full && lines)
       run(std::true_type(), std::false_type(), std::true_type());

@@ -294,4 +294,43 @@ __device__ __forceinline__ float take_over(const uint64_t* word, bool asks, int*
 // A factor of 0 forgets what was there, NaN and infinity too.
 __device__ __forceinline__ float step_or_forget(float a, float h, float u) { return a == 0.f ? u : fmaf(a, h, u); }
 
+// Products of factors. Only a token's own factor of 0 forgets: a product of others that is
+// no normal number in 32 bits has to keep a state that is NaN or infinite, and one that is
+// 0 or far from 1, whatever stood beside it. So a product is one float where that is a
+// normal number, 0 where a token among its own forgot (whatever the other factors were),
+// and else -m with an exponent e beside it: m 2^e, m in [1/2, 1), infinity or NaN.
+struct Product {
+  float m;
+  int e;  // meant where m < 0
+};
+__device__ __forceinline__ bool is_normal(float a) { return a >= 0x1p-126f && a < __builtin_inff(); }
+__device__ __forceinline__ float step_over(Product a, float h, float u) {
+  const float far = __builtin_ldexpf(-a.m * h, a.e) + u;
+  return a.m < 0.f ? far : step_or_forget(a.m, h, u);
+}
+// The same with the exponent in memory, where it is read only if it is meant.
+__device__ __forceinline__ float step_over(float m, const int* e, float h, float u) {
+  float y = fmaf(m, h, u);
+  if (m <= 0.f) y = m == 0.f ? u : __builtin_ldexpf(-m * h, *e) + u;
+  return y;
+}
+// How such a product grows: m 2^e with m >= 0, from 1. By a factor that is not 0, and by
+// the product of some.
+struct Growing {
+  float m = 1.f;
+  int e = 0;
+  __device__ __forceinline__ void by(float a) {
+    const float q = m * a;
+    m = __builtin_amdgcn_frexp_mantf(q);
+    e += __builtin_amdgcn_frexp_expf(q);
+  }
+  __device__ __forceinline__ void by(Product a) {
+    const bool none = m == 0.f || a.m == 0.f;
+    by(fabsf(a.m));
+    e += a.m < 0.f ? a.e : 0;
+    if (none) *this = {0.f, 0};
+  }
+  __device__ __forceinline__ Product product() const { return {-m, e}; }
+};
+
 }  // namespace ret

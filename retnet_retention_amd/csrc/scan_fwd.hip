@@ -12,7 +12,10 @@
 // wave waits for; then every segment runs its tokens from its state and stores them.
 // Waiting one after the other takes 0.65 us a tile, less than the tiles of a
 // long sequence take at the memory's rate unless it is narrower than some 1000
-// channels; so tiles are long, 256 tokens.
+// channels; so tiles are long, 256 tokens. Where factors' products are no normal numbers
+// (256 tokens that forget a third of the state each) the wave that joins forms them again with
+// exponents, beside the others' inputs: with rates up to 10 2 x 8192 x 4096 takes 120 us, not
+// 115, 4 x 2048 x 2560 41, not 38.5; with rates up to 0.5 nothing.
 // Measured in bf16 with both gates, kernel alone: 2 x 8192 x 4096 109 to 115 us (4.7 to 4.9 TB/s; a
 // copy reaches 5.07), 4 x 2048 x 2560 with the states kept 43 us; calls of 1 x 16384 x 8192 200
 // us (5.4 TB/s), 1 x 32768 x 1024 86 us (the chain of 128 tiles), 1 x 131072 x 2560 562 us
@@ -30,12 +33,18 @@ namespace ret {
 
 constexpr int kSegment = 16;  // tokens
 
-// TILE: kScanTile, or kScanOnly where no sequence has more than that
+// TILE: kScanTile, or kScanOnly where no sequence has more than that. Without the bound of
+// 128 registers fp32 inputs with a gate and log decays take 144, and a CU one workgroup.
 template <typename T, bool GATES, bool IGATE, bool NORM, int V, int TILE>
-__global__ __launch_bounds__(TILE * 2) void scan_fwd_kernel(ScanParams p) {
+__global__ __launch_bounds__(TILE * 2, sizeof(T) == 4 && !GATES ? 4 : 2) void scan_fwd_kernel(ScanParams p) {
   using D = std::conditional_t<GATES, T, float>;
   constexpr int LW = kScanChannels / V, PARTS = 2 / V, L = kSegment * PARTS, SEGS = TILE / kSegment;
+  // factors and inputs of the segments, and of what stands before each; exponents of products
+  // that are no normal number; whether a wave has some
+  constexpr int BEFORE = TILE == kScanOnly ? 1 : SEGS;
   __shared__ float s_a[SEGS][kScanChannels], s_u[SEGS][kScanChannels], s_h[kScanChannels];
+  __shared__ float s_p[BEFORE][kScanChannels], s_pu[BEFORE][kScanChannels];
+  __shared__ int s_e[SEGS][kScanChannels], s_pe[BEFORE][kScanChannels], s_odd[SEGS / 2];
   clear_errors(p);
   const Place at = place_of<false>(p, TILE);
   if (!at.any) return;
@@ -108,21 +117,36 @@ __global__ __launch_bounds__(TILE * 2) void scan_fwd_kernel(ScanParams p) {
     fold(std::true_type());
   else if (wave * 2 * kSegment < left)
     fold(std::false_type());
-  // a factor of 0 among the tokens (or a product that is): they may have to forget what is no number
-  bool forgets = false;
+  // a product that is no normal number: exact, and inputs that forget what stood before them
+  bool odd = false;
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e) forgets |= A[k][e] == 0.f;
-  forgets = __any(forgets);
-  if (forgets) {
+    for (int e = 0; e < V; ++e) odd |= !is_normal(A[k][e]);
+  odd = __any(odd);
+  if (odd) {
 #pragma unroll
     for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         float& U1 = U[j / kSegment][e];
-        U1 = step_or_forget(a[j][e], j % kSegment ? U1 : 0.f, u[j][e]);
+        U1 = j % kSegment ? step_or_forget(a[j][e], U1, u[j][e]) : u[j][e];
       }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (!is_normal(A[k][e])) {
+          Growing t;
+          bool none = false;
+#pragma unroll
+          for (int j = 0; j < kSegment; ++j) {
+            none |= a[k * kSegment + j][e] == 0.f;
+            t.by(a[k * kSegment + j][e]);
+          }
+          A[k][e] = none ? 0.f : -t.m;
+          s_e[seg + k][cl + e] = t.e;
+        }
   }
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
@@ -131,43 +155,75 @@ __global__ __launch_bounds__(TILE * 2) void scan_fwd_kernel(ScanParams p) {
       s_a[seg + k][cl + e] = A[k][e];
       s_u[seg + k][cl + e] = U[k][e];
     }
+  if (lane == 0) s_odd[wave] = odd;
   __syncthreads();
   if (wave == 0) {
     const int ch = c0 + lane;
     const bool mine = ch < p.width, last = left <= TILE;
     const int64_t held = (int64_t)at.b * p.width + ch;
+    const bool any_odd = __any(s_odd[lane % (SEGS / 2)]);
     float h = 0.f;
-    if (TILE == kScanOnly) {
+    if constexpr (TILE == kScanOnly) {
       // no state to wait for: the segments one after the other
       if (p.state_in && mine) h = p.state_in[held];
+      auto walk = [&](auto some) {
 #pragma unroll 8
-      for (int s = 0; s < SEGS; ++s) {
-        const float sa = s_a[s][lane], su = s_u[s][lane];
-        s_u[s][lane] = h;
-        h = step_or_forget(sa, h, su);
-      }
+        for (int s = 0; s < SEGS; ++s) {
+          const float sa = s_a[s][lane], su = s_u[s][lane];
+          s_u[s][lane] = h;
+          h = decltype(some)::value ? step_over({sa, s_e[s][lane]}, h, su) : fmaf(sa, h, su);
+        }
+      };
+      if (any_odd)
+        walk(std::true_type());
+      else
+        walk(std::false_type());
       if (mine && p.state_out) p.state_out[held] = h;
     } else {
-      float fa[SEGS], fu[SEGS], ta = 1.f, tu = 0.f;
+      float ta = 1.f, tu = 0.f, low = 1.f;
 #pragma unroll
       for (int s = 0; s < SEGS; ++s) {
         const float sa = s_a[s][lane], su = s_u[s][lane];
-        fa[s] = ta;
-        fu[s] = tu;
-        tu = step_or_forget(sa, tu, su);
+        s_p[s][lane] = ta;
+        s_pu[s][lane] = tu;
+        tu = fmaf(sa, tu, su);
         ta *= sa;
+        low = fminf(low, ta);
       }
+      bool far = !is_normal(ta) || !is_normal(low);
+      if (any_odd)
+        for (int s = 0; s < SEGS; ++s) far |= !is_normal(s_a[s][lane]);
+      const bool any_far = __any(far);
+      Product total = {ta, 0};
+      if (far) {
+        Growing t;
+        if (any_odd) {
+          tu = 0.f;
+#pragma unroll 4
+          for (int s = 0; s < SEGS; ++s) {
+            const Product one = {s_a[s][lane], s_e[s][lane]};
+            s_p[s][lane] = -t.m;
+            s_pe[s][lane] = t.e;
+            s_pu[s][lane] = tu;
+            tu = step_over(one, tu, s_u[s][lane]);
+            t.by(one);
+          }
+        } else {  // (the inputs as they are: every segment's factor is a normal number)
 #pragma unroll
-      for (int s = 0; s < SEGS; ++s) {
-        s_a[s][lane] = fa[s];
-        s_u[s][lane] = fu[s];
+          for (int s = 0; s < SEGS; ++s) {
+            s_p[s][lane] = -t.m;
+            s_pe[s][lane] = t.e;
+            t.by(s_a[s][lane]);
+          }
+        }
+        total = t.product();
       }
       if (at.i > 0)
         h = take_over(p.hand + (at.tile - 1) * p.width + ch, mine, p.ctrl);
       else if (p.state_in && mine)
         h = p.state_in[held];
       s_h[lane] = h;
-      h = step_or_forget(ta, h, tu);
+      h = any_far ? step_over(total, h, tu) : fmaf(ta, h, tu);
       if (mine) {
         if (!last)
           hand_on(p.hand + at.tile * p.width + ch, h);
@@ -182,9 +238,13 @@ __global__ __launch_bounds__(TILE * 2) void scan_fwd_kernel(ScanParams p) {
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      h0[k][e] = TILE == kScanOnly ? s_u[seg + k][cl + e]
-                                   : step_or_forget(s_a[seg + k][cl + e], s_h[cl + e], s_u[seg + k][cl + e]);
+    for (int e = 0; e < V; ++e) {
+      if constexpr (TILE == kScanOnly) {
+        h0[k][e] = s_u[seg + k][cl + e];
+      } else {
+        h0[k][e] = step_over(s_p[seg + k][cl + e], &s_pe[seg + k][cl + e], s_h[cl + e], s_pu[seg + k][cl + e]);
+      }
+    }
   if (p.kept && seg * kSegment % kScanBwdTile == 0) {
     float* kept = p.kept + (kept_row(p, at.b, tok0) + (from + seg * kSegment) / kScanBwdTile) * p.width + c;
 #pragma unroll
@@ -205,7 +265,7 @@ __global__ __launch_bounds__(TILE * 2) void scan_fwd_kernel(ScanParams p) {
       if (decltype(full)::value || j < n) o.store(j, h);
     }
   };
-  if (forgets)
+  if (odd)
     run(std::false_type(), std::true_type());
   else if (full)
     run(std::true_type(), std::false_type());
