@@ -105,7 +105,12 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p) {
 
 // A wave walks `p.rows` tokens, kConvStep at a time, the next ones on their way from
 // memory; what it carries are the last K - 1 inputs and dz. It looks K - 1 tokens past
-// its own for the dx of its last ones.
+// its own for the dx of its last ones. dx goes past the caches, but not where rows end inside
+// a line of 128 bytes, whose parts two workgroups write. Past them and through them, a call
+// with x in memory and dout just written, that call with a matrix product that reads dx, and
+// calls one after the other: 2 x 8192 x 6000 163 / 326 / 151 us and 133 / 298 / 145, 4 x 2048 x
+// 7680 81 / 209 / 84 and 82 / 212 / 88, 2 x 8192 x 4096 87 / 193 / 94 and 85 / 192 / 96, 2 x
+// 8192 x 12288 278 / 575 / 255 and 267 / 565 / 261.
 constexpr int kConvStep = 8;
 
 template <typename T, int K, int V>
@@ -166,6 +171,7 @@ __global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
     const Rows<T, V> xs(line.x + t0 * p.x_stride, p.x_stride, rows, p.width, 0, c);
     const Rows<T, V> ds(dout + (int64_t)t0 * p.width, p.width, rows, p.width, 0, c);
     const Rows<T, V> to(dx + (int64_t)t0 * p.width, p.width, rows, p.width, 0, c);
+    const bool lines = (uint32_t)p.width * (uint32_t)sizeof(T) % 128 == 0;
     auto ask = [&](int t) {
       const int from = t - t0;
       if (from + S <= rows) {
@@ -197,9 +203,10 @@ __global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
         Lane<T, V>::get(nd[j], dz[H + j]);
       }
       if (t + S < end) ask(t + S);
-      auto step = [&](auto whole) {
+      auto step = [&](auto whole, auto stream) {
         // whole: every token is one of the wave's own, and none of the last H of the sequence
         constexpr bool FULL = decltype(whole)::value;
+        constexpr int POLICY = decltype(stream)::value ? kStreamed : 0;
 #pragma unroll
         for (int j = 0; j < S; ++j) {
           const bool there = FULL || t + j < end, own = FULL || (there && t + j < t0 + p.rows);
@@ -228,17 +235,21 @@ __global__ __launch_bounds__(256, 4) void conv_bwd_kernel(ConvParams p) {
           if (FULL || s >= t0) {
             if (FULL || (s < len && s < t0 + p.rows)) {
               if (!FULL) add_after(s, out);
-              if (inside) to.template store<kStreamed>(s - t0, out);
+              if (inside) to.template store<POLICY>(s - t0, out);
             }
           } else if (begins && p.d_state_in) {
             put_state(s, out);
           }
         }
       };
-      if (t > t0 && t + S <= min(t0 + p.rows, len))
-        step(std::true_type());
-      else
-        step(std::false_type());
+      if (t > t0 && t + S <= min(t0 + p.rows, len)) {
+        if (lines)
+          step(std::true_type(), std::true_type());
+        else
+          step(std::true_type(), std::false_type());
+      } else {
+        step(std::false_type(), std::false_type());
+      }
 #pragma unroll
       for (int j = 0; j < H; ++j)
 #pragma unroll
