@@ -1200,8 +1200,9 @@ def _cache_call(state, codes, scales, cache_slots, slots):
 
 
 def state_cache_write(state, codes, scales, cache_slots, *, slots=None):
-    """Parks states in 8 bits: state [num_slots, ...] (fp32; the states of any
-    of the recurrent calls) goes to slots of a cache, codes int8 [cache_size,
+    """Parks states in 8 bits: state [num_slots, ...] (fp32: the states of
+    retention, the delta rule and the gated recurrence; short_conv's few inputs,
+    in the tensors' type, stay as they are) goes to slots of a cache, codes int8 [cache_size,
     ...] and scales fp32 [cache_size, ceil(values / 64)]: every 64 values share a
     scale, a 127th of the largest magnitude. Sequence b (of cache_slots, GPU int32
     [batch]) goes from state slots[b] (GPU int32 [batch]; None: b) to cache slot

@@ -6,9 +6,10 @@
 // Bound by memory: a wave holds 64 V channels of a tile's tokens and the K - 1 rows
 // beside it, so each row is read once but for those.
 // Measured in bf16, 4 taps with bias and swish, kernel alone: forward 2 x 8192 x 12288 151 us
-// (5.3 TB/s; a copy reaches 5.07; its stores past the caches were 6 us faster, but then whoever
-// reads the result next takes 13 us longer); backward 4 x 2048 x 7680 82 us (4.6 TB/s) and
-// 4.8 for the sums, with the SIMDs computing in 66 % of their cycles.
+// to 154 (5.2 TB/s; a copy reaches 5.07; its stores past the caches were 6 us faster, but then whoever
+// reads the result next takes 13 us longer), 2 x 8192 x 6000 79 us (5.0 TB/s); backward 4 x
+// 2048 x 7680 85 us (4.5 TB/s) and 5.4 for the sums, with the SIMDs computing in 68 % of their
+// cycles, 2 x 8192 x 6000 147 us (4.0 TB/s). fp32, 2 x 8192 x 2048: 49 us (5.5 TB/s) and 90 (4.5).
 #include "norms.hpp"
 #include "scan_common.hpp"
 

@@ -17,10 +17,11 @@ inline int64_t tile_count(int batch, int seqlen, bool packed, int64_t total, int
 
 // The recurrence: tokens of a tile of the forward and of the backward. The states
 // that the forward keeps stand before each of the backward's tiles. Long tiles make
-// short chains, short ones leave less to wait for at a workgroup's begin and end:
-//   forward, 256 and 128: 1 x 32768 x 1024 88 and 152 us, packed 10287 x 2560 49 and 56,
-//     2 x 8192 x 4096 123 and 122, 4 x 2048 x 2560 with its inputs in the caches 40 and 36;
-//   backward, 128 and 64: 1 x 32768 x 1024 188 and 327 us, 4 x 2048 x 2560 72 and 70.
+// short chains, short ones leave less to wait for at a workgroup's begin and end. Calls in us,
+//   forward, 256 and 128: 1 x 32768 x 1024 88 and 160, 1 x 131072 x 2560 542 and 870, 2 x 8192 x
+//     4096 109 and 113, 4 x 2048 x 2560 with its inputs in the caches 39 and 36;
+//   backward, 128 and 64: 1 x 32768 x 1024 172 and 320, 1 x 131072 x 2560 1170 and 1786, 2 x 8192
+//     x 4096 191 and 205, 4 x 2048 x 2560 61 and 58.
 constexpr int kScanTile = 256, kScanBwdTile = 128;
 // Sequences of up to this many tokens may be one tile of the forward, of 1024 threads: then
 // there is nothing to hand on, and nothing to clear before (scan_fwd.hip tells when).

@@ -9,15 +9,19 @@
 // gradient of the state behind it comes from the tile after it, as a word in memory.
 // Tiles start from the last. A tile's share of drate goes to a row of sums that a
 // second launch adds up in a fixed order. The gradients' stores bypass the caches, which
-// leaves the inputs there: 4 x 2048 x 2560 again and again 63 us a call, not 80, right
-// after its forward 70 and 71. Not where rows end inside a line of 128 bytes, whose parts
-// two workgroups write: 4 x 8192 x 4100 609 us through the caches and 784 past them, 2 x
-// 8192 x 4095 284 and 346, 2 x 4096 x 6000 189 and 207.
-// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 69 us (4.3 TB/s); calls of
-// 2 x 8192 x 4096 195 to 220 us, 1 x 16384 x 8192 375 us (5.0 TB/s), 1 x 32768 x 1024 171 us
-// (the chain of 256 tiles), 1 x 131072 x 2560 1146 us (4.1 TB/s).
+// leaves the inputs there. Past them and through them, forward and gradients one after the
+// other over changing inputs; with inputs in memory and dout just written, the call and
+// the convolution's gradients after it; these and products that read all gradients: 4 x 2048 x
+// 2560 115 / 115 / 253 us and 120 / 114 / 251, 2 x 8192 x 4096 295 / 290 / 606 and 305 / 300 /
+// 618, 8 x 2048 x 1024 98 / 98 / 204 and 105 / 97 / 203. Not where rows end inside a line of 128
+// bytes, whose parts two workgroups write: 4 x 8192 x 4100 609 us a call through the caches and
+// 784 past them, 2 x 8192 x 4095 284 and 346, 2 x 4096 x 6000 189 and 207.
+// Measured in bf16 with both gates, kernel alone: 4 x 2048 x 2560 70 us (4.2 TB/s), 4 x 8192 x
+// 4100 600 us; calls of 2 x 8192 x 4096 191 us, 1 x 16384 x 8192 362 us (5.2 TB/s), 1 x 32768 x
+// 1024 172 us (the chain of 256 tiles), 1 x 131072 x 2560 1170 us (4.0 TB/s); fp32, kernel
+// alone, 2 x 8192 x 2048 195 us (4.8 TB/s).
 // Bound by memory and arithmetic together: the SIMDs compute in 59 % of
-// their cycles (71 vector instructions for 64 elements), waves wait in 38 % of theirs for
+// their cycles (71 vector instructions for 64 elements), waves wait in 37 % of theirs for
 // memory. 128 registers a lane, two workgroups a CU: one of each fetches while the other computes.
 #include "norms.hpp"
 #include "scan_common.hpp"

@@ -16,12 +16,14 @@
 // (256 tokens that forget a third of the state each) the wave that joins forms them again with
 // exponents, beside the others' inputs: with rates up to 10 2 x 8192 x 4096 takes 120 us, not
 // 115, 4 x 2048 x 2560 41, not 38.5; with rates up to 0.5 nothing.
-// Measured in bf16 with both gates, kernel alone: 2 x 8192 x 4096 109 to 115 us (4.7 to 4.9 TB/s; a
-// copy reaches 5.07), 4 x 2048 x 2560 with the states kept 43 us; calls of 1 x 16384 x 8192 200
-// us (5.4 TB/s), 1 x 32768 x 1024 86 us (the chain of 128 tiles), 1 x 131072 x 2560 562 us
-// (4.8 TB/s). Bound by memory: without any arithmetic or wait it took as long. 34 vector
-// instructions for 64 elements, more than half of the SIMDs' cycles. Segments of 8 tokens
-// and 1024 threads, twice the waves, took the same time.
+// Measured in bf16 with both gates, kernel alone: 2 x 8192 x 4096 109 to 118 us (4.5 to 4.9 TB/s; a
+// copy reaches 5.07), 4 x 2048 x 2560 with the states kept 43 us, 4 x 8192 x 4100 297 us (rows
+// that end inside a line); calls of 1 x 16384 x 8192 197 us (5.4 TB/s), 1 x 32768 x 1024 88 us
+// (the chain of 128 tiles), 1 x 131072 x 2560 542 us (5.0 TB/s); fp32, 2 x 8192 x 2048 111 us
+// (4.8 TB/s). Bound by memory, with 34 vector instructions for 64 elements, 63 % of the SIMDs'
+// cycles, close behind. Without any arithmetic or wait it took 120 us when it took 123, before
+// neighbouring groups shared an XCD; segments of 8 tokens in 1024 threads, twice the waves,
+// the same 123. Neither was measured again since.
 #include <algorithm>
 
 #include "scan_common.hpp"

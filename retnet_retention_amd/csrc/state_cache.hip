@@ -4,7 +4,7 @@
 // keep a state to half a 127th of its block's largest value; e4m3 of the same size
 // keeps each value to a 16th of itself, five times worse over values of one
 // size. Bound by memory: 4 bytes a value on one side, 1.06 on the other. Measured, 64
-// states of 4 MiB, kernels alone: written in 78 us (4.4 TB/s), read back in 49
+// states of 4 MiB, kernels alone: written in 83 us (4.1 TB/s), read back in 49
 // (6.9 TB/s by the bytes: the codes just written come from the caches), read from 24 others' in 45.
 #include "common.hpp"
 #include "state_cache.hpp"
@@ -156,9 +156,11 @@ static dim3 grid_of(const StateCacheParams& p, int at_once) {
   return dim3((unsigned)((p.blocks + 16 * at_once - 1) / (16 * at_once)), (unsigned)p.batch);
 }
 // States that do not fit the cache behind the L2s (256 MB) cannot be found there
-// by whoever reads them next, so they bypass it: 64 states of 4 MiB are written in 76
-// us, not 92, and read in 50, not 76. Smaller ones stay: a decode step right after 16
-// of 4 MiB were read back is 4 us shorter.
+// by whoever reads them next, so they bypass it; smaller ones stay. Through it and past it,
+// n states of 4 MiB, calls in us: written right after the decode step that made them, n = 32 /
+// 48 / 56 / 64 / 80 / 128 38 / 51 / 60 / 72 / 103 / 166 and 39 / 52 / 58 / 65 / 82 / 139; read
+// back from memory with a decode step after it 77 / 109 / 130 / 153 / 199 / 331 and 83 / 118 /
+// 134 / 152 / 188 / 305.
 constexpr size_t kStreamBytes = size_t(256) << 20;
 static bool streams(const StateCacheParams& p) { return (size_t)p.batch * p.values * sizeof(float) >= kStreamBytes; }
 
