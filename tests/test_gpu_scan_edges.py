@@ -419,3 +419,19 @@ def test_every_row_outside_the_sequences_has_a_gradient_of_zero(monkeypatch, dty
     assert len(g) == 5 and all(t is None or torch.isfinite(t.float()).all() for t in g)
     for t in g[:3]:
         assert t is None or ((t[:cu[0]] == 0).all() and (t[cu[2]:] == 0).all())
+
+
+@pytest.mark.parametrize("default", [torch.bfloat16, torch.float64])
+def test_training_under_another_default_type(default):
+    """The bits of the calls under fp32, from tensors made before."""
+    x = dev(scan_inputs(66, (2, 700), 66, "bf16", "gates", state=2))
+    want = run_scan(x, True)
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        _, kept = rr.gated_scan_fwd(x["x"], x["decay"], x["gate"], rate=x["rate"], normalize=True, state_in=x["s0"], keep=True)
+        got = run_scan(x, True)
+    finally:
+        torch.set_default_dtype(before)
+    assert kept.dtype == torch.float32
+    assert all(got[k] is None or (got[k].dtype == want[k].dtype and torch.equal(got[k], want[k])) for k in want)
